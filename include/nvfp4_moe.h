@@ -96,6 +96,143 @@ int nvfp4_quantize_experts(const float* w_dev, int64_t experts, int64_t rows, in
                            float* scratch_dev, void* stream);
 
 /* ---------------------------------------------------------------------- */
+/* Operators around the layer: routing by scores, bias and groups, the norms */
+/* of the block with its gate and residual, 8-bit linear products            */
+/* ---------------------------------------------------------------------- */
+
+/* Element types of the operators below. */
+typedef enum moe_dtype { MOE_BF16 = 0, MOE_F16 = 1, MOE_F32 = 2 } moe_dtype;
+
+typedef enum moe_score { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
+
+/*
+ * A routing rule.  Of a token with logits l over E experts and top_k = k:
+ *   s_e = softmax(l)_e (over all E) or sigmoid(l_e)
+ *   v_e = s_e + bias_e; without a bias the experts are ranked by l_e itself
+ *   groups: experts e * num_groups / E = g form group g; its score is the sum
+ *           of its best group_best (1 or 2) values v (of the one it has, if it
+ *           has one); the best top_groups groups stay, ties to the lower group
+ *   ids:    the k best of the experts that stay, best first, ties to the
+ *           lower index
+ *   w_j  =  s_{id_j}, over the sum of the k with renormalize, times scale
+ * The order is decided in binary64; values v within 2^-41 of their size may
+ * count as equal.  An expert is masked where its logit or its bias is -inf or
+ * NaN (+inf counts as FLT_MAX); masked experts and those of dropped groups
+ * come after all others, lower index first, with weight 0, so a token always
+ * has k different experts; a token without any has k weights of 0.  The
+ * weights are formed in binary64 and rounded once; where the k scores are so
+ * small that they or their sum underflow there, the weights are 0.
+ * num_groups: 1..64, a divisor of E; top_groups: 1..num_groups, with
+ * top_groups * E / num_groups >= k.  num_groups = 1 has no groups (top_groups
+ * and group_best are then 1).  scale: finite.
+ */
+typedef struct moe_router {
+  int32_t score;       /* moe_score */
+  int32_t num_groups;
+  int32_t top_groups;
+  int32_t group_best;  /* 1 or 2 */
+  int32_t renormalize; /* 0 or 1 */
+  float scale;
+} moe_router;
+
+/*
+ * Routing of T tokens.
+ *   logits_dev   dtype [T, ld], ld >= E, aligned to its element
+ *   E            1..1024;  top_k  1..min(16, E)
+ *   bias_dev     f32 [E], 4-byte aligned, or NULL
+ *   ids_dev      i32 [T, k] (written)     weights_dev  f32 [T, k] (written)
+ * T = 0 is a no-op; T < 2^31 / k.  Outputs must not overlap the inputs.
+ */
+int moe_route(const moe_router* r, const void* logits_dev, int32_t dtype, int64_t T, int64_t E, int64_t ld,
+              int32_t top_k, const float* bias_dev, int32_t* ids_dev, float* weights_dev, void* stream);
+
+typedef enum moe_norm_kind { MOE_NORM_RMS = 0, MOE_NORM_LAYER = 1 } moe_norm_kind;
+
+/* N(v) = (v - mean) / sqrt(mean((v - mean)^2) + eps) * (weight + offset) + bias
+ * over a row; MOE_NORM_RMS has mean = 0.  weight / bias: [cols] of the
+ * operator's dtype or NULL (no factor / no term); eps finite and >= 0. */
+typedef struct moe_norm {
+  int32_t kind; /* moe_norm_kind */
+  float eps;
+  float offset;
+  const void* weight_dev;
+  const void* bias_dev;
+} moe_norm;
+
+/*
+ * Between two blocks, row by row:
+ *   r' = res_scale * r + out_scale * act(gate) * after(y)      h = before(r')
+ * `after` is the norm behind a block, of its output y; `before` the norm in
+ * front of the next one.  h is taken of r' in binary32, before r' is rounded
+ * to its type.
+ *   rows >= 0 (0: no-op), < 2^31; 1 <= cols <= 65536
+ *   dtype           y, gate, weights, biases and h
+ *   residual_dtype  residual and residual_out: dtype, or MOE_F32
+ *   residual_dev    [rows, ld_residual]
+ *   y_dev           [rows, ld_y], or NULL: r' = res_scale * r (no after, no gate)
+ *   gate_dev        NULL, or rows ld_gate apart (0: one row for every token)
+ *                   of gate_cols values: 1 (for the whole row) or cols
+ *   gate_sigmoid    1: act is the sigmoid
+ *   after, before   NULL: no norm; before is required with h_dev
+ *   residual_out_dev  [rows, ld_residual_out] r', or NULL
+ *   h_dev           [rows, ld_h], or NULL (not both NULL)
+ * Leading dimensions are >= cols, pointers aligned to their element.  In
+ * place: residual_out may be residual and h may be y, with equal leading
+ * dimensions; any other overlap of an output is NVFP4_ERR_ALIAS.
+ */
+typedef struct moe_block_norm_args {
+  int64_t rows, cols;
+  int32_t dtype, residual_dtype;
+  const void* residual_dev;
+  int64_t ld_residual;
+  const void* y_dev;
+  int64_t ld_y;
+  const void* gate_dev;
+  int64_t ld_gate, gate_cols;
+  int32_t gate_sigmoid;
+  float res_scale, out_scale;
+  const moe_norm* after;
+  const moe_norm* before;
+  void* residual_out_dev;
+  int64_t ld_residual_out;
+  void* h_dev;
+  int64_t ld_h;
+} moe_block_norm_args;
+
+int moe_block_norm(const moe_block_norm_args* args, void* stream);
+
+/*
+ * Per-row quantization to 8-bit integers: activations a row per token, or
+ * weights [channels, in] a row per channel.
+ *   scale = RN(amax / 127), code = RNE(RN(x * RN(127 / amax))), amax = max|x|
+ *   of the row; a row with amax < 2^-119 has codes 0 and scale 1.
+ *   x_dev      dtype [rows, ld_x], aligned to its element, ld_x >= cols; finite
+ *              (an inf or NaN gives unspecified codes and scale for its row)
+ *   rows       0 <= rows < 2^31 (0: no-op);  1 <= cols <= 2^30
+ *   codes_dev  i8 [rows, ld_codes], 16-byte aligned, ld_codes a multiple of 16,
+ *              >= cols (written; a row's last 16-byte piece is filled with
+ *              zeros behind cols, the rest of ld_codes is left alone)
+ *   scale_dev  f32 [rows], 4-byte aligned (written)
+ */
+int int8_quantize_per_token(const void* x_dev, int32_t dtype, int64_t rows, int64_t cols, int64_t ld_x,
+                            void* codes_dev, int64_t ld_codes, float* scale_dev, void* stream);
+
+/*
+ * out[m, n] = scale_a[m] * scale_b[n] * sum_k a[m, k] * b[n, k] + bias[n]
+ * The sum is exact (32-bit integers), scaled in binary32, rounded once.
+ *   a_dev     i8 [M, lda] token rows;  b_dev  i8 [N, ldb] channel rows; 16-byte
+ *             aligned, lda and ldb multiples of 16, >= K; whole 16-byte pieces
+ *             are read, bytes behind K have no effect
+ *   scale_a_dev f32 [M], scale_b_dev f32 [N], bias_dev f32 [N] or NULL
+ *   M, N, K   0 <= M, N < 2^31 (0: no-op);  1 <= K <= 131071 (the sum's range)
+ *   out_dev   dtype [M, ldo], ldo >= N, aligned to its element; must not
+ *             overlap an input (NVFP4_ERR_ALIAS)
+ */
+int int8_matmul(const void* a_dev, int64_t lda, const float* scale_a_dev, const void* b_dev, int64_t ldb,
+                const float* scale_b_dev, const float* bias_dev, int64_t M, int64_t N, int64_t K, void* out_dev,
+                int32_t dtype, int64_t ldo, void* stream);
+
+/* ---------------------------------------------------------------------- */
 /* MoE layer                                                               */
 /* ---------------------------------------------------------------------- */
 
@@ -249,7 +386,8 @@ int moe_workspace_bind_weights(moe_workspace* ws, const moe_nvfp4_packed* w, voi
  * finalize around the expert GEMM; [P1] "Implementation breakdown" item 2:
  * quantize per token, then run the experts with the per-token scale.)
  * Router: the k largest logits (ties to the smaller expert index, slots in
- * descending order), weights = softmax over the chosen k.
+ * descending order), weights = softmax over the chosen k; another rule by
+ * moe_workspace_set_router.
  *
  *   x_dev        bf16 [T, H], 16-byte aligned
  *   logits_dev   f32 [T, E]
@@ -343,6 +481,21 @@ int refresh_scales_inplace(moe_workspace* ws, const moe_nvfp4_weights* w, void* 
  * NVFP4_ERR_INVALID_ARG for a workspace without the flag or NULL pointers.
  */
 int moe_workspace_set_act_scales(moe_workspace* ws, const float* scales_dev, void* stream);
+
+/*
+ * The workspace's router: later forwards route by *r (copied) instead of the
+ * k largest logits; E and k are the workspace's.  The bias (f32 [E], or NULL)
+ * is COPIED into the workspace on `stream`; the caller's array must stay
+ * valid until that copy has run.  Set again, a bias is replaced in place, so
+ * a captured forward uses the new values on its next replay; the rule, and
+ * whether there is a bias, is part of a captured graph and changes only by
+ * capturing again.  r = NULL
+ * (with a NULL bias) goes back to the k largest logits.  With shared experts,
+ * the shared one is not routed.  moe_nvfp4_forward_noalloc has no workspace
+ * and keeps the k largest logits.  The router is one more kernel, before the
+ * prologue and inside its stage time.
+ */
+int moe_workspace_set_router(moe_workspace* ws, const moe_router* r, const float* bias_dev, void* stream);
 
 /* Free library-owned memory (never the caller's packed weights).  NULL is a
  * no-op.  Synchronizes the device. */

@@ -33,6 +33,11 @@ BUF = dict(XQ_CODES=0, XQ_SCALES=1, XQ_GSCALE=2, TOPK_IDS=3, TOPK_W=4, COUNTS=5,
            PERM=7, INV=8, ACT=9, A2_CODES=10, A2_SCALES=11, A2_GSCALE=12, A2_16=13)
 
 
+DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+SCORES = {"softmax": 0, "sigmoid": 1}
+NORM_KINDS = {"rms": 0, "layer": 1}
+
+
 class Nvfp4Error(RuntimeError):
     def __init__(self, code: int, msg: str):
         super().__init__(f"{STATUS.get(code, code)}: {msg}")
@@ -57,6 +62,28 @@ class MoePacked(ctypes.Structure):
     _fields_ = [("num_experts", ctypes.c_int64), ("hidden", ctypes.c_int64), ("inter", ctypes.c_int64),
                 ("w13", ctypes.c_void_p), ("w13_gscale", ctypes.c_void_p),
                 ("w2", ctypes.c_void_p), ("w2_gscale", ctypes.c_void_p)]
+
+
+class MoeRouter(ctypes.Structure):
+    _fields_ = [("score", ctypes.c_int32), ("num_groups", ctypes.c_int32), ("top_groups", ctypes.c_int32),
+                ("group_best", ctypes.c_int32), ("renormalize", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class MoeNorm(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32), ("eps", ctypes.c_float), ("offset", ctypes.c_float),
+                ("weight", ctypes.c_void_p), ("bias", ctypes.c_void_p)]
+
+
+class MoeBlockNormArgs(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("residual_dtype", ctypes.c_int32),
+                ("residual", ctypes.c_void_p), ("ld_residual", ctypes.c_int64),
+                ("y", ctypes.c_void_p), ("ld_y", ctypes.c_int64),
+                ("gate", ctypes.c_void_p), ("ld_gate", ctypes.c_int64), ("gate_cols", ctypes.c_int64),
+                ("gate_sigmoid", ctypes.c_int32), ("res_scale", ctypes.c_float), ("out_scale", ctypes.c_float),
+                ("after", ctypes.POINTER(MoeNorm)), ("before", ctypes.POINTER(MoeNorm)),
+                ("residual_out", ctypes.c_void_p), ("ld_residual_out", ctypes.c_int64),
+                ("h", ctypes.c_void_p), ("ld_h", ctypes.c_int64)]
 
 
 _lib = None
@@ -103,6 +130,17 @@ def lib():
                                                 _I64, _P, _P]
         L.moe_workspace_buffer.restype = ctypes.c_int
         L.moe_workspace_buffer.argtypes = [_P, ctypes.c_int32, ctypes.POINTER(_P), ctypes.POINTER(_I64)]
+        _I32 = ctypes.c_int32
+        L.moe_route.restype = ctypes.c_int
+        L.moe_route.argtypes = [ctypes.POINTER(MoeRouter), _P, _I32, _I64, _I64, _I64, _I32, _P, _P, _P, _P]
+        L.moe_workspace_set_router.restype = ctypes.c_int
+        L.moe_workspace_set_router.argtypes = [_P, ctypes.POINTER(MoeRouter), _P, _P]
+        L.moe_block_norm.restype = ctypes.c_int
+        L.moe_block_norm.argtypes = [ctypes.POINTER(MoeBlockNormArgs), _P]
+        L.int8_quantize_per_token.restype = ctypes.c_int
+        L.int8_quantize_per_token.argtypes = [_P, _I32, _I64, _I64, _I64, _P, _I64, _P, _P]
+        L.int8_matmul.restype = ctypes.c_int
+        L.int8_matmul.argtypes = [_P, _I64, _P, _P, _I64, _P, _P, _I64, _I64, _I64, _P, _I32, _I64, _P]
         _lib = L
     return _lib
 
@@ -204,6 +242,235 @@ def token_ceiling(max_prefill, piecewise_max, graph_max_bs, spec_draft_tokens) -
     _check(lib().moe_token_ceiling(max_prefill, piecewise_max, graph_max_bs, spec_draft_tokens,
                                    ctypes.byref(out)))
     return out.value
+
+
+# --- operators around the layer --------------------------------------------------
+#
+# Each works on its tensors' device, which need not be the current one, on
+# `stream` (default: that device's current stream).  Tensors a call makes
+# belong to the stream it ran on.
+
+def _matrix(t, name, dtypes):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} must be one of {[str(d) for d in dtypes]}, got {t.dtype}")
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be a matrix with unit column stride")
+
+
+def _vector(t, name, n, dtype, device):
+    if not isinstance(t, torch.Tensor) or t.device != device:
+        raise ValueError(f"{name} must be a tensor on {device}")
+    if t.dtype != dtype or tuple(t.shape) != (n,) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {n} values, got {t.dtype} {tuple(t.shape)}")
+
+
+def _same(t, name, shape, device):
+    if t.device != device or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {tuple(shape)} on {device}, got {tuple(t.shape)} on {t.device}")
+
+
+def _ld(t):
+    """Elements between two rows (a single row's stride means nothing)."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _ld16(t):
+    return t.stride(0) if t.shape[0] > 1 else (t.shape[1] + 15) // 16 * 16
+
+
+def _run(device, stream, call):
+    """call(handle of the stream) with `device` and `stream` current."""
+    if stream is not None:
+        if stream.device != device:
+            raise ValueError(f"stream of {stream.device}, tensors on {device}")
+        with torch.cuda.stream(stream):
+            return call(stream.cuda_stream)
+    if device.index == torch.cuda.current_device():
+        return call(torch.cuda.current_stream().cuda_stream)
+    with torch.cuda.device(device):
+        return call(torch.cuda.current_stream().cuda_stream)
+
+
+class Router:
+    """A routing rule (moe_router): scores "softmax" or "sigmoid", experts in
+    `groups` of which the best `top_groups` (by the sum of their best
+    `group_best` values) stay, weights renormalized over the k or not, times
+    `scale`."""
+
+    def __init__(self, score="softmax", groups=1, top_groups=1, group_best=1, renormalize=True, scale=1.0):
+        if score not in SCORES:
+            raise ValueError("score must be 'softmax' or 'sigmoid'")
+        self.desc = MoeRouter(SCORES[score], groups, top_groups, group_best, 1 if renormalize else 0, scale)
+
+
+def route(logits, top_k, router, bias=None, out=None, stream=None):
+    """logits [T, E] (bf16, f16 or f32; the row stride may exceed E), bias f32
+    [E] -> (ids int32 [T, k], weights f32 [T, k]), into `out` if given."""
+    _matrix(logits, "logits", DTYPES)
+    T, E = logits.shape
+    device = logits.device
+    if bias is not None:
+        _vector(bias, "bias", E, torch.float32, device)
+    if out is not None:
+        for t, name, dtype in ((out[0], "ids", torch.int32), (out[1], "weights", torch.float32)):
+            _require(t, dtype, name)
+            _same(t, name, (T, top_k), device)
+            if not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous")
+
+    def call(s):
+        ids, w = out if out is not None else (
+            torch.empty((T, max(top_k, 0)), dtype=torch.int32, device=device),
+            torch.empty((T, max(top_k, 0)), dtype=torch.float32, device=device))
+        _check(lib().moe_route(router.desc, logits.data_ptr(), DTYPES[logits.dtype], T, E, _ld(logits), top_k,
+                               bias.data_ptr() if bias is not None else None, ids.data_ptr(), w.data_ptr(), s))
+        return ids, w
+    return _run(device, stream, call)
+
+
+class Norm:
+    """The norm of a row: "rms" or "layer", weight and bias [cols] (or None),
+    the weight counted from `offset` (moe_norm)."""
+
+    def __init__(self, weight=None, bias=None, kind="rms", eps=1e-6, offset=0.0):
+        if kind not in NORM_KINDS:
+            raise ValueError("kind must be 'rms' or 'layer'")
+        self.weight, self.bias = weight, bias
+        self._head = (NORM_KINDS[kind], eps, offset)
+
+    def desc(self, cols, dtype, device, name):
+        for t, part in ((self.weight, "weight"), (self.bias, "bias")):
+            if t is not None:
+                _vector(t, f"{name} {part}", cols, dtype, device)
+        return MoeNorm(*self._head, self.weight.data_ptr() if self.weight is not None else None,
+                       self.bias.data_ptr() if self.bias is not None else None)
+
+
+def block_norm(residual, y=None, before=None, after=None, gate=None, gate_sigmoid=False, res_scale=1.0,
+               out_scale=1.0, residual_out=None, h_out=None, stream=None):
+    """r' = res_scale * residual + out_scale * act(gate) * after(y), h = before(r')
+    (moe_block_norm) -> (r', h), h None without `before`.  Without y, with
+    res_scale 1 and no residual_out, r' is the residual itself, not copied.
+
+    residual [T, H] of y's dtype or f32 (without y: of any of the three, and h
+    is of its dtype); y [T, H] bf16, f16 or f32; gate None, [H] for each
+    channel, [T, 1] for each token or [T, H].  residual_out / h_out: outputs
+    to write, residual and y themselves allowed."""
+    _matrix(residual, "residual", DTYPES)
+    T, H = residual.shape
+    device = residual.device
+    if y is not None:
+        _matrix(y, "y", DTYPES)
+        _same(y, "y", (T, H), device)
+        dtype = y.dtype
+    else:
+        dtype = h_out.dtype if h_out is not None else residual.dtype
+    ld_gate = gate_cols = 0
+    if gate is not None:
+        if gate.device != device or gate.dtype != dtype:
+            raise ValueError(f"gate must be {dtype} on {device}")
+        if gate.dim() == 1:
+            _vector(gate, "gate", H, dtype, device)
+            gate_cols = H
+        else:
+            _matrix(gate, "gate", DTYPES)
+            if gate.shape[0] != T or gate.shape[1] not in (1, H):
+                raise ValueError(f"gate must be [{H}], [{T}, 1] or [{T}, {H}], got {tuple(gate.shape)}")
+            gate_cols = gate.shape[1]
+            ld_gate = _ld(gate)
+    for t, name, want in ((residual_out, "residual_out", residual.dtype), (h_out, "h_out", dtype)):
+        if t is not None:
+            _matrix(t, name, (want,))
+            _same(t, name, (T, H), device)
+    if h_out is not None and before is None:
+        raise ValueError("h_out needs a norm (before)")
+    as_is = y is None and before is not None and res_scale == 1.0 and residual_out is None
+    na = after.desc(H, dtype, device, "after") if after is not None else None
+    nb = before.desc(H, dtype, device, "before") if before is not None else None
+
+    def call(s):
+        r = residual_out if residual_out is not None or as_is else (
+            torch.empty((T, H), dtype=residual.dtype, device=device))
+        h = h_out if h_out is not None else (
+            torch.empty((T, H), dtype=dtype, device=device) if before is not None else None)
+        a = MoeBlockNormArgs(
+            T, H, DTYPES[dtype], DTYPES[residual.dtype], residual.data_ptr(), _ld(residual),
+            y.data_ptr() if y is not None else None, _ld(y) if y is not None else 0,
+            gate.data_ptr() if gate is not None else None, ld_gate, gate_cols, 1 if gate_sigmoid else 0,
+            res_scale, out_scale, ctypes.pointer(na) if na is not None else None,
+            ctypes.pointer(nb) if nb is not None else None, r.data_ptr() if r is not None else None,
+            _ld(r) if r is not None else 0,
+            h.data_ptr() if h is not None else None, _ld(h) if h is not None else 0)
+        _check(lib().moe_block_norm(a, s))
+        return (residual if r is None else r), h
+    return _run(device, stream, call)
+
+
+def int8_quantize_per_token(x, stream=None):
+    """x [rows, cols] (bf16, f16 or f32; the row stride may exceed cols) ->
+    (codes int8 [rows, cols], scale f32 [rows]).  The codes' rows start at
+    multiples of 16 bytes, as int8_matmul takes them.  Weights [channels, in]
+    give one scale a channel."""
+    _matrix(x, "x", DTYPES)
+    rows, cols = x.shape
+    device = x.device
+    ld = (cols + 15) // 16 * 16
+
+    def call(s):
+        codes = torch.empty((rows, ld), dtype=torch.int8, device=device)
+        scale = torch.empty((rows,), dtype=torch.float32, device=device)
+        _check(lib().int8_quantize_per_token(x.data_ptr(), DTYPES[x.dtype], rows, cols, _ld(x), codes.data_ptr(), ld,
+                                             scale.data_ptr(), s))
+        return (codes[:, :cols] if ld != cols else codes), scale
+    return _run(device, stream, call)
+
+
+def _int8_rows(t, name):
+    _matrix(t, name, (torch.int8,))
+    if t.shape[0] > 1 and t.stride(0) % 16 != 0:
+        raise ValueError(f"{name}: rows must start at multiples of 16 bytes, as int8_quantize_per_token lays them out")
+
+
+def int8_matmul(codes, scale, w_codes, w_scale, bias=None, out_dtype=torch.bfloat16, out=None, stream=None):
+    """codes int8 [M, K] and scale f32 [M] of the tokens, w_codes int8 [N, K]
+    and w_scale f32 [N] of the channels, bias f32 [N] ->
+    scale[m] * w_scale[n] * sum_k codes[m, k] * w_codes[n, k] + bias[n], [M, N]."""
+    _int8_rows(codes, "codes")
+    _int8_rows(w_codes, "w_codes")
+    M, K = codes.shape
+    N = w_codes.shape[0]
+    device = codes.device
+    _same(w_codes, "w_codes", (N, K), device)
+    _vector(scale, "scale", M, torch.float32, device)
+    _vector(w_scale, "w_scale", N, torch.float32, device)
+    if bias is not None:
+        _vector(bias, "bias", N, torch.float32, device)
+    if out is not None:
+        _matrix(out, "out", DTYPES)
+        _same(out, "out", (M, N), device)
+
+    def call(s):
+        o = out if out is not None else torch.empty((M, N), dtype=out_dtype, device=device)
+        if o.dtype not in DTYPES:
+            raise ValueError(f"out_dtype must be one of {[str(d) for d in DTYPES]}, got {o.dtype}")
+        _check(lib().int8_matmul(codes.data_ptr(), _ld16(codes), scale.data_ptr(), w_codes.data_ptr(), _ld16(w_codes),
+                                 w_scale.data_ptr(), bias.data_ptr() if bias is not None else None, M, N, K,
+                                 o.data_ptr(), DTYPES[o.dtype], _ld(o), s))
+        return o
+    return _run(device, stream, call)
+
+
+def int8_linear(x, w_codes, w_scale, bias=None, out_dtype=None, out=None, stream=None):
+    """x [M, K] (bf16, f16 or f32) quantized per token, then int8_matmul with
+    the channel-quantized weights; the result is of x's dtype unless
+    out_dtype (or out) says otherwise."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return int8_linear(x, w_codes, w_scale, bias, out_dtype, out)
+    codes, scale = int8_quantize_per_token(x)
+    return int8_matmul(codes, scale, w_codes, w_scale, bias, out_dtype or x.dtype, out)
 
 
 # --- synthetic weights (input generation) --------------------------------------
@@ -354,6 +621,18 @@ class MoeLayer:
         if scales.numel() != 2 or not scales.is_contiguous():
             raise ValueError("scales must be a contiguous float32 tensor of 2 values (g_x, g_a)")
         _check(lib().moe_workspace_set_act_scales(self.handle, _ptr(scales), _stream(stream)))
+
+    def set_router(self, router, bias=None, stream=None):
+        """Route later forwards by `router` (a Router; bias f32 [num_experts],
+        copied into the workspace) instead of the k largest logits; None goes
+        back to those.  A captured forward takes up a new bias on its next
+        replay, a new rule only when it is captured again."""
+        if bias is not None:
+            _require(bias, torch.float32, "bias")
+            if tuple(bias.shape) != (self.cfg.num_experts,) or not bias.is_contiguous():
+                raise ValueError("bias must be a contiguous float32 tensor of num_experts values")
+        _check(lib().moe_workspace_set_router(self.handle, router.desc if router is not None else None, _ptr(bias),
+                                              _stream(stream)))
 
     def forward_into(self, x, logits, out, T=None, stream=None):
         T = x.shape[0] if T is None else T

@@ -23,7 +23,8 @@ FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-Wall",
          "-I" + os.path.join(ROOT, "include")]
 
 LIBS = {
-    "libnvfp4moe.so": ["quantize.hip", "moe_kernels.hip", "gemm_kernels.hip", "moe_api.cpp", "noalloc.hip"],
+    "libnvfp4moe.so": ["quantize.hip", "moe_kernels.hip", "gemm_kernels.hip", "route.hip", "block_norm.hip",
+                      "int8_linear.hip", "moe_api.cpp", "ops_api.cpp", "noalloc.hip"],
     "libnvfp4synth.so": ["synth_weights.hip"],
 }
 

@@ -1,0 +1,88 @@
+// Element types of the operators around the layer: loads to binary32 and
+// stores rounded to nearest even, one element or eight at a time.
+#pragma once
+
+#include "common.hpp"
+
+namespace nvfp4 {
+
+struct Bf16 {
+  static constexpr int kBytes = 2;
+  __device__ static float get(const void* p, int64_t i) {
+    return __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(p)[i]) << 16);
+  }
+  __device__ static uint32_t bits(float f) {
+    return __builtin_bit_cast(uint16_t, static_cast<__bf16>(f));  // the converter keeps NaN a NaN
+  }
+  __device__ static void put(void* p, int64_t i, float f) {
+    static_cast<uint16_t*>(p)[i] = static_cast<uint16_t>(bits(f));
+  }
+  __device__ static void unpack(uint32_t w, float& lo, float& hi) {
+    lo = bf16_lo(w);
+    hi = bf16_hi(w);
+  }
+};
+
+struct F16 {
+  static constexpr int kBytes = 2;
+  __device__ static float get(const void* p, int64_t i) {
+    return static_cast<float>(static_cast<const _Float16*>(p)[i]);
+  }
+  __device__ static uint32_t bits(float f) { return __builtin_bit_cast(uint16_t, static_cast<_Float16>(f)); }
+  __device__ static void put(void* p, int64_t i, float f) {
+    static_cast<_Float16*>(p)[i] = static_cast<_Float16>(f);
+  }
+  __device__ static void unpack(uint32_t w, float& lo, float& hi) {
+    const half2v h = __builtin_bit_cast(half2v, w);
+    lo = static_cast<float>(h[0]);
+    hi = static_cast<float>(h[1]);
+  }
+};
+
+struct F32 {
+  static constexpr int kBytes = 4;
+  __device__ static float get(const void* p, int64_t i) { return static_cast<const float*>(p)[i]; }
+  __device__ static void put(void* p, int64_t i, float f) { static_cast<float*>(p)[i] = f; }
+};
+
+// The raw bits of eight consecutive elements (16-byte aligned).
+template <typename T>
+struct Raw8 {
+  u32x4 v[T::kBytes / 2];
+};
+
+template <typename T>
+__device__ __forceinline__ void load8(Raw8<T>& r, const void* p, int64_t i) {
+  const u32x4* s = reinterpret_cast<const u32x4*>(static_cast<const char*>(p) + i * T::kBytes);
+#pragma unroll
+  for (int j = 0; j < T::kBytes / 2; ++j) r.v[j] = s[j];
+}
+
+template <typename T>
+__device__ __forceinline__ void to_f32(const Raw8<T>& r, float (&f)[8]) {
+  if constexpr (T::kBytes == 4) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = __uint_as_float(r.v[j / 4][j % 4]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) T::unpack(r.v[0][j], f[2 * j], f[2 * j + 1]);
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ void store8(void* p, int64_t i, const float (&f)[8]) {
+  u32x4* d = reinterpret_cast<u32x4*>(static_cast<char*>(p) + i * T::kBytes);
+  if constexpr (T::kBytes == 4) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      d[j] = u32x4{__float_as_uint(f[4 * j]), __float_as_uint(f[4 * j + 1]), __float_as_uint(f[4 * j + 2]),
+                   __float_as_uint(f[4 * j + 3])};
+  } else {
+    u32x4 v;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = T::bits(f[2 * j]) | (T::bits(f[2 * j + 1]) << 16);
+    d[0] = v;
+  }
+}
+
+}  // namespace nvfp4

@@ -5,6 +5,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "nvfp4_moe.h"
+
 namespace nvfp4 {
 
 constexpr int kMaxExperts = 1024;
@@ -67,6 +69,8 @@ struct FwdParams {
   int tiled_gx;       // tiled kernels: tile slots of the grid (max tiles rounded up to 8)
   int deterministic;  // 1: slot-ordered finalize; 0: fp32 atomics into out_acc
   int a16;            // 1: W4A16 (x and act as bf16 GEMM inputs, no activation quantization)
+  int routed;         // 1: topk_ids / topk_w are already in place (the workspace's router wrote
+                      //    them on the same stream); the prologue only builds the schedule
   int preq;           // 1: x handed over already quantized: xq_codes / xq_scales / xq_g are
                       //    the caller's (read only), x is not read
   const float* static_g;  // NULL, or [2] static global scales of x and of GEMM2's input
@@ -137,6 +141,60 @@ hipError_t launch_quantize_experts(const float* w, int64_t experts, int64_t rows
                                    uint8_t* codes, uint8_t* scales, float* gs, uint32_t* amax_bits,
                                    hipStream_t s);
 
+// route.hip: the router with scores, bias and groups.
+constexpr int kMaxRouteGroups = 64;
+constexpr int kRouteWaveTokens = 1024;  // batches up to here take a whole wave a token
+struct RouteParams {
+  const void* logits;  // [T, ld] of dtype (moe_dtype)
+  const float* bias;   // [E] or NULL
+  int32_t* ids;        // [T, k]
+  float* weights;      // [T, k]
+  int64_t ld;
+  int T, E, k, dtype;
+  int score, groups, top_groups, group_best, renormalize;
+  float scale;
+  uint32_t group_magic;  // ceil(2^20 * groups / E): (e * magic) >> 20 is e's group (e < 1024)
+};
+hipError_t launch_route_scores(const RouteParams& q, hipStream_t s);
+
+// block_norm.hip
+struct NormParams {
+  int kind;  // -1: none, MOE_NORM_RMS, MOE_NORM_LAYER
+  float eps, offset;
+  const void* weight;  // or NULL
+  const void* bias;    // or NULL
+};
+struct BlockNormParams {
+  int64_t rows;
+  int cols;
+  const void* r;
+  const void* y;     // NULL: no block output
+  const void* gate;  // NULL: none
+  int64_t ld_r, ld_y, ld_gate;
+  int gate_cols, gate_sigmoid;
+  float res_scale, out_scale;
+  NormParams after, before;
+  void* r_out;  // or NULL
+  void* h;      // or NULL
+  int64_t ld_r_out, ld_h;
+};
+hipError_t launch_block_norm(const BlockNormParams& p, int dtype, int residual_dtype, bool vec, hipStream_t s);
+
+// int8_linear.hip
+hipError_t launch_int8_quantize_rows(const void* x, int dtype, int64_t rows, int64_t cols, int64_t ld,
+                                     int8_t* codes, int64_t ld_codes, float* scales, hipStream_t s);
+struct Int8GemmParams {
+  const int8_t* a;  // [M, lda]
+  const int8_t* b;  // [N, ldb]
+  const float* sa;
+  const float* sb;
+  const float* bias;  // [N] or NULL
+  void* out;          // [M, ldo] of dtype
+  int64_t lda, ldb, ldo;
+  int M, N, K, dtype;
+};
+hipError_t launch_int8_matmul(const Int8GemmParams& p, hipStream_t s);
+
 // gemm_kernels.hip
 // Rows per tile and kernel family for a forward of T tokens.
 void choose_gemm(int64_t T, FwdParams* p);
@@ -146,8 +204,9 @@ hipError_t launch_grouped_gemms(const FwdParams& p, int max_tiles, hipStream_t s
                                 hipEvent_t const* events);
 
 // moe_kernels.hip
-// events: NULL or 5 events recorded around the four kernels.
-hipError_t launch_moe_forward(const FwdParams& p, int max_tiles, hipStream_t s,
+// route: NULL, or the workspace's router, run before the prologue (p.routed).
+// events: NULL or 5 events recorded around the four stages.
+hipError_t launch_moe_forward(const FwdParams& p, const RouteParams* route, int max_tiles, hipStream_t s,
                               hipEvent_t const* events);
 // Copy row-major codes [E, N, K/2] and scales [E, N, K/16] of one weight
 // matrix into unit records.  w13: N = 2I, split = 1 (gate / up halves);

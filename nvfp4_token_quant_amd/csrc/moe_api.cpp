@@ -28,6 +28,14 @@ namespace {
 
 thread_local std::string g_last_error;
 
+// Tiles of R routed rows over E experts, plus those of the shared expert's
+// T rows (shared_T = 0 without one).
+int64_t tiles_bound(int64_t R, int64_t E, int mt, int64_t shared_T) {
+  return (R + mt - 1) / mt + std::min(E, R) + (shared_T + mt - 1) / mt;
+}
+
+}  // namespace
+
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
@@ -38,14 +46,6 @@ bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
 int hip_fail(hipError_t e, const char* what) {
   return api_fail(NVFP4_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
 }
-
-// Tiles of R routed rows over E experts, plus those of the shared expert's
-// T rows (shared_T = 0 without one).
-int64_t tiles_bound(int64_t R, int64_t E, int mt, int64_t shared_T) {
-  return (R + mt - 1) / mt + std::min(E, R) + (shared_T + mt - 1) / mt;
-}
-
-}  // namespace
 
 int api_fail(int code, const char* fmt, ...) {
   char buf[512];
@@ -142,6 +142,7 @@ int64_t layout_buffers(const moe_config& c, int64_t T_cap, bool own_gscales, uin
   take(&b->out_acc, det ? 0 : T * H * 4);
   take(&b->w13g, own_gscales ? Ew * 4 : 0);
   take(&b->w2g, own_gscales ? Ew * 4 : 0);
+  take(&b->route_bias, own_gscales ? E * 4 : 0);
   return off;
 }
 
@@ -161,7 +162,7 @@ int check_packed(const moe_config& c, const moe_nvfp4_packed* w) {
 }
 
 int run_forward(const moe_config& c, const FwdBuffers& b, const WeightView& wv, bool static_scales_set,
-                const void* x_dev, const XQ& xq, const float* logits_dev, int64_t T, void* out_dev,
+                const RouterView& router, const void* x_dev, const XQ& xq, const float* logits_dev, int64_t T, void* out_dev,
                 hipStream_t stream, const hipEvent_t* events) {
   const bool preq = xq.on;
   if (T < 0) return api_fail(NVFP4_ERR_INVALID_ARG, "T must be >= 0 (got %lld)", (long long)T);
@@ -252,7 +253,19 @@ int run_forward(const moe_config& c, const FwdBuffers& b, const WeightView& wv, 
   const int64_t route_blocks = (T + route_tokens_per_block(T) - 1) / route_tokens_per_block(T);
   if (route_blocks > b.route_blocks_cap)
     return api_fail(NVFP4_ERR_INVALID_ARG, "internal: route blocks exceed capacity");
-  hipError_t e = launch_moe_forward(p, static_cast<int>(max_tiles), stream, events);
+  RouteParams rp;
+  if (router.on) {
+    p.routed = 1;
+    rp = route_params(router.rule, E, c.top_k);
+    rp.logits = logits_dev;
+    rp.dtype = MOE_F32;
+    rp.ld = E;
+    rp.bias = router.bias;
+    rp.T = p.T;
+    rp.ids = b.topk_ids;
+    rp.weights = b.topk_w;
+  }
+  hipError_t e = launch_moe_forward(p, router.on ? &rp : nullptr, static_cast<int>(max_tiles), stream, events);
   if (e != hipSuccess) return hip_fail(e, "moe_nvfp4_forward launch");
   return api_ok();
 }
@@ -268,6 +281,8 @@ struct moe_workspace {
   uint8_t* block;  // the one device allocation the buffers are carved from
   nvfp4::FwdBuffers buf;
   bool act_scales_set;
+  bool has_router, has_route_bias;
+  moe_router router;
   // weights: the caller's packed records (borrowed); the workspace holds
   // copies of the global scales (buf.w13g / buf.w2g)
   bool bound;
@@ -280,16 +295,9 @@ struct moe_workspace {
 
 namespace {
 
-bool is_aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-bool overlaps(const void* a, int64_t na, const void* b, int64_t nb) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return na > 0 && nb > 0 && x < y + static_cast<uintptr_t>(nb) && y < x + static_cast<uintptr_t>(na);
-}
-
-int hip_error(hipError_t e, const char* what) {
-  return api_fail(NVFP4_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
-}
+using nvfp4::aligned;
+using nvfp4::hip_fail;
+using nvfp4::overlap;
 
 bool dims_ok(int64_t E, int64_t H, int64_t I) {
   return E >= 1 && E <= nvfp4::kMaxExperts && H >= 128 && H % 128 == 0 && H <= 65536 && I >= 128 &&
@@ -332,17 +340,17 @@ int nvfp4_quantize_per_token(const void* x_dev, int64_t rows, int64_t cols, int6
   if (rows > INT32_MAX) return api_fail(NVFP4_ERR_INVALID_ARG, "rows must be < 2^31 (got %lld)", (long long)rows);
   if (!x_dev || !codes_dev || !scales_dev || !gscale_dev)
     return api_fail(NVFP4_ERR_INVALID_ARG, "NULL pointer argument");
-  if (!is_aligned(x_dev, 16) || !is_aligned(codes_dev, 16) || !is_aligned(gscale_dev, 4))
+  if (!aligned(x_dev, 16) || !aligned(codes_dev, 16) || !aligned(gscale_dev, 4))
     return api_fail(NVFP4_ERR_INVALID_ARG, "x and codes must be 16-byte aligned, gscale 4-byte aligned");
   const int64_t xbytes = ((rows - 1) * ld_x + cols) * 2;
-  if (overlaps(x_dev, xbytes, codes_dev, rows * cols / 2) ||
-      overlaps(x_dev, xbytes, scales_dev, rows * cols / 16) || overlaps(x_dev, xbytes, gscale_dev, rows * 4))
+  if (overlap(x_dev, xbytes, codes_dev, rows * cols / 2) ||
+      overlap(x_dev, xbytes, scales_dev, rows * cols / 16) || overlap(x_dev, xbytes, gscale_dev, rows * 4))
     return api_fail(NVFP4_ERR_ALIAS, "outputs overlap the input x");
   hipError_t e = nvfp4::launch_quantize_rows(static_cast<const uint16_t*>(x_dev), rows, cols, ld_x,
                                              static_cast<uint8_t*>(codes_dev),
                                              static_cast<uint8_t*>(scales_dev), gscale_dev,
                                              static_cast<hipStream_t>(stream));
-  if (e != hipSuccess) return hip_error(e, "nvfp4_quantize_per_token launch");
+  if (e != hipSuccess) return hip_fail(e, "nvfp4_quantize_per_token launch");
   return api_ok();
 }
 
@@ -354,17 +362,17 @@ int nvfp4_quantize_experts(const float* w_dev, int64_t experts, int64_t rows, in
                     "need 1 <= experts <= 65535, rows >= 1, cols a positive multiple of 16");
   if (!w_dev || !codes_dev || !scales_dev || !gscale_dev || !scratch_dev)
     return api_fail(NVFP4_ERR_INVALID_ARG, "NULL pointer argument");
-  if (!is_aligned(w_dev, 16) || !is_aligned(codes_dev, 16) || !is_aligned(gscale_dev, 4) ||
-      !is_aligned(scratch_dev, 4))
+  if (!aligned(w_dev, 16) || !aligned(codes_dev, 16) || !aligned(gscale_dev, 4) ||
+      !aligned(scratch_dev, 4))
     return api_fail(NVFP4_ERR_INVALID_ARG, "w and codes must be 16-byte aligned");
   const int64_t n = experts * rows * cols;
-  if (overlaps(w_dev, n * 4, codes_dev, n / 2) || overlaps(w_dev, n * 4, scales_dev, n / 16))
+  if (overlap(w_dev, n * 4, codes_dev, n / 2) || overlap(w_dev, n * 4, scales_dev, n / 16))
     return api_fail(NVFP4_ERR_ALIAS, "outputs overlap the input");
   hipError_t e = nvfp4::launch_quantize_experts(w_dev, experts, rows, cols, static_cast<uint8_t*>(codes_dev),
                                                 static_cast<uint8_t*>(scales_dev), gscale_dev,
                                                 reinterpret_cast<uint32_t*>(scratch_dev),
                                                 static_cast<hipStream_t>(stream));
-  if (e != hipSuccess) return hip_error(e, "nvfp4_quantize_experts launch");
+  if (e != hipSuccess) return hip_fail(e, "nvfp4_quantize_experts launch");
   return api_ok();
 }
 
@@ -391,8 +399,8 @@ int moe_pack_weights(const moe_nvfp4_weights* w, void* w13_packed_dev, void* w2_
   const bool with_codes = w->w13_codes != nullptr;
   if (with_codes != (w->w2_codes != nullptr))
     return api_fail(NVFP4_ERR_INVALID_ARG, "give both code pointers or neither");
-  if (!is_aligned(w13_packed_dev, 16) || !is_aligned(w2_packed_dev, 16) ||
-      (with_codes && (!is_aligned(w->w13_codes, 16) || !is_aligned(w->w2_codes, 16))))
+  if (!aligned(w13_packed_dev, 16) || !aligned(w2_packed_dev, 16) ||
+      (with_codes && (!aligned(w->w13_codes, 16) || !aligned(w->w2_codes, 16))))
     return api_fail(NVFP4_ERR_INVALID_ARG, "packed buffers and codes must be 16-byte aligned");
   int64_t b13, b2;
   packed_sizes(E, H, I, &b13, &b2);
@@ -400,13 +408,13 @@ int moe_pack_weights(const moe_nvfp4_weights* w, void* w13_packed_dev, void* w2_
   const int64_t in_bytes[4] = {with_codes ? E * 2 * I * H / 2 : 0, E * 2 * I * H / 16,
                                with_codes ? E * H * I / 2 : 0, E * H * I / 16};
   for (int i = 0; i < 4; ++i)
-    if (overlaps(w13_packed_dev, b13, ins[i], in_bytes[i]) || overlaps(w2_packed_dev, b2, ins[i], in_bytes[i]))
+    if (overlap(w13_packed_dev, b13, ins[i], in_bytes[i]) || overlap(w2_packed_dev, b2, ins[i], in_bytes[i]))
       return api_fail(NVFP4_ERR_ALIAS, "packed buffers overlap the row-major weights");
-  if (overlaps(w13_packed_dev, b13, w2_packed_dev, b2))
+  if (overlap(w13_packed_dev, b13, w2_packed_dev, b2))
     return api_fail(NVFP4_ERR_ALIAS, "the two packed buffers overlap");
   hipError_t e = pack(w, static_cast<uint8_t*>(w13_packed_dev), static_cast<uint8_t*>(w2_packed_dev), with_codes,
                       static_cast<hipStream_t>(stream));
-  if (e != hipSuccess) return hip_error(e, "moe_pack_weights launch");
+  if (e != hipSuccess) return hip_fail(e, "moe_pack_weights launch");
   return api_ok();
 }
 
@@ -437,7 +445,7 @@ int moe_workspace_create(const moe_config* cfg, void* stream, moe_workspace** ou
   if (e != hipSuccess) {
     (void)hipFree(w->block);
     delete w;
-    return hip_error(e, "workspace initialization");
+    return hip_fail(e, "workspace initialization");
   }
   *out = w;
   return api_ok();
@@ -452,7 +460,7 @@ int moe_workspace_bind_weights(moe_workspace* ws, const moe_nvfp4_packed* w, voi
   hipStream_t s = static_cast<hipStream_t>(stream);
   hipError_t e = nvfp4::launch_copy_f32(w->w13_gscale, ws->buf.w13g, E, s);
   if (e == hipSuccess) e = nvfp4::launch_copy_f32(w->w2_gscale, ws->buf.w2g, E, s);
-  if (e != hipSuccess) return hip_error(e, "global scale copy");
+  if (e != hipSuccess) return hip_fail(e, "global scale copy");
   ws->w13 = static_cast<const uint8_t*>(w->w13);
   ws->w2 = static_cast<const uint8_t*>(w->w2);
   ws->bound = true;
@@ -477,13 +485,13 @@ int refresh_scales_inplace(moe_workspace* ws, const moe_nvfp4_weights* w, void* 
                     "moe_pack_weights)");
   if (!w->w13_scales || !w->w2_scales || !w->w13_gscale || !w->w2_gscale)
     return api_fail(NVFP4_ERR_INVALID_ARG, "scale pointers must be non-NULL");
-  if (!is_aligned(w->w13_gscale, 4) || !is_aligned(w->w2_gscale, 4))
+  if (!aligned(w->w13_gscale, 4) || !aligned(w->w2_gscale, 4))
     return api_fail(NVFP4_ERR_INVALID_ARG, "global scale pointers must be 4-byte aligned");
   hipStream_t s = static_cast<hipStream_t>(stream);
   hipError_t e = pack(w, const_cast<uint8_t*>(ws->w13), const_cast<uint8_t*>(ws->w2), false, s);
   if (e == hipSuccess) e = nvfp4::launch_copy_f32(w->w13_gscale, ws->buf.w13g, E, s);
   if (e == hipSuccess) e = nvfp4::launch_copy_f32(w->w2_gscale, ws->buf.w2g, E, s);
-  if (e != hipSuccess) return hip_error(e, "scale refresh");
+  if (e != hipSuccess) return hip_fail(e, "scale refresh");
   return api_ok();
 }
 
@@ -491,11 +499,32 @@ int moe_workspace_set_act_scales(moe_workspace* ws, const float* scales_dev, voi
   if (!ws) return api_fail(NVFP4_ERR_INVALID_ARG, "NULL workspace");
   if (!(ws->cfg.flags & MOE_STATIC_ACT_SCALES))
     return api_fail(NVFP4_ERR_INVALID_ARG, "workspace was created without MOE_STATIC_ACT_SCALES");
-  if (!scales_dev || !is_aligned(scales_dev, 4))
+  if (!scales_dev || !aligned(scales_dev, 4))
     return api_fail(NVFP4_ERR_INVALID_ARG, "NULL or misaligned scales");
   hipError_t e = nvfp4::launch_copy_f32(scales_dev, ws->buf.act_scales, 2, static_cast<hipStream_t>(stream));
-  if (e != hipSuccess) return hip_error(e, "activation scale copy");
+  if (e != hipSuccess) return hip_fail(e, "activation scale copy");
   ws->act_scales_set = true;
+  return api_ok();
+}
+
+int moe_workspace_set_router(moe_workspace* ws, const moe_router* r, const float* bias_dev, void* stream) {
+  if (!ws) return api_fail(NVFP4_ERR_INVALID_ARG, "NULL workspace");
+  if (!r) {
+    if (bias_dev) return api_fail(NVFP4_ERR_INVALID_ARG, "a bias needs a router");
+    ws->has_router = false;
+    return api_ok();
+  }
+  int st = nvfp4::check_router(r, ws->cfg.num_experts, ws->cfg.top_k);
+  if (st != NVFP4_OK) return st;
+  if (bias_dev) {
+    if (!aligned(bias_dev, 4)) return api_fail(NVFP4_ERR_INVALID_ARG, "bias must be 4-byte aligned");
+    hipError_t e = nvfp4::launch_copy_f32(bias_dev, ws->buf.route_bias, ws->cfg.num_experts,
+                                          static_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return hip_fail(e, "router bias copy");
+  }
+  ws->router = *r;
+  ws->has_router = true;
+  ws->has_route_bias = bias_dev != nullptr;
   return api_ok();
 }
 
@@ -504,7 +533,8 @@ static int workspace_forward(moe_workspace* ws, const void* x_dev, const nvfp4::
   if (!ws) return api_fail(NVFP4_ERR_INVALID_ARG, "NULL workspace");
   if (!ws->bound) return api_fail(NVFP4_ERR_NO_WEIGHTS, "no weights bound; call moe_workspace_bind_weights");
   const nvfp4::WeightView wv{ws->w13, ws->w2, ws->buf.w13g, ws->buf.w2g};
-  return nvfp4::run_forward(ws->cfg, ws->buf, wv, ws->act_scales_set, x_dev, xq, logits_dev, T, out_dev,
+  const nvfp4::RouterView rv{ws->has_router, ws->router, ws->has_route_bias ? ws->buf.route_bias : nullptr};
+  return nvfp4::run_forward(ws->cfg, ws->buf, wv, ws->act_scales_set, rv, x_dev, xq, logits_dev, T, out_dev,
                             static_cast<hipStream_t>(stream), ws->timing ? ws->events : nullptr);
 }
 

@@ -24,70 +24,9 @@
 #include "common.hpp"
 #include "kernels.hpp"
 #include "quant_row.hpp"
+#include "route.hpp"
 
 namespace nvfp4 {
-
-// ---------------------------------------------------------------------------
-// Router reductions.  A candidate is the 64-bit key (order-preserving bits of
-// the logit) << 32 | ~expert, so the larger key is the larger logit and, on
-// equal logits, the smaller expert index.  -0.0 is keyed as +0.0: a binary32
-// comparison finds the two equal, so their tie also goes to the smaller
-// index.  Reductions over a 16-lane DPP row use quad permutes (xor 1, xor 2)
-// and row rotates (4, 8), one instruction each.
-// ---------------------------------------------------------------------------
-__device__ __forceinline__ uint64_t route_key(float v, int e) {
-  const uint32_t u = __float_as_uint(v) == 0x80000000u ? 0u : __float_as_uint(v);
-  const uint32_t o = (u & 0x80000000u) ? ~u : (u | 0x80000000u);
-  return (static_cast<uint64_t>(o) << 32) | static_cast<uint32_t>(~e);
-}
-__device__ __forceinline__ float key_value(uint64_t k) {
-  const uint32_t o = static_cast<uint32_t>(k >> 32);
-  return __uint_as_float((o & 0x80000000u) ? (o & 0x7FFFFFFFu) : ~o);
-}
-__device__ __forceinline__ int key_expert(uint64_t k) { return static_cast<int>(~static_cast<uint32_t>(k)); }
-
-template <int CTRL>
-__device__ __forceinline__ float dpp_f32(float v) {
-  return __uint_as_float(dpp_u32<CTRL>(__float_as_uint(v)));
-}
-
-// The largest key over a 16-lane DPP row, or over the wave, as two 32-bit
-// maxima: of the high words (the ordered logits), then of the low words
-// (~expert) of the lanes whose high word is that maximum.  The pair is the
-// lexicographic, i.e. 64-bit, maximum; each DPP step is a single max with a
-// DPP operand (the 64-bit form takes two moves, a compare and two selects).
-__device__ __forceinline__ uint32_t row16_max_u32(uint32_t v) {
-  v = max(v, dpp_u32<kDppXor1>(v));
-  v = max(v, dpp_u32<kDppXor2>(v));
-  v = max(v, dpp_u32<kDppRor4>(v));
-  v = max(v, dpp_u32<kDppRor8>(v));
-  return v;
-}
-__device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
-  v = row16_max_u32(v);
-  uint32_t a, b;
-  lane_pair<16>(v, a, b);
-  v = max(a, b);
-  lane_pair<32>(v, a, b);
-  return max(a, b);
-}
-template <bool WAVE>
-__device__ __forceinline__ uint64_t key_max(uint64_t k) {
-  const uint32_t h = static_cast<uint32_t>(k >> 32), l = static_cast<uint32_t>(k);
-  const uint32_t mh = WAVE ? wave_max_u32(h) : row16_max_u32(h);
-  const uint32_t tl = h == mh ? l : 0u;
-  const uint32_t ml = WAVE ? wave_max_u32(tl) : row16_max_u32(tl);
-  return (static_cast<uint64_t>(mh) << 32) | ml;
-}
-// (the association, and so the rounding, depends on the lane: a slot's weight
-// is normalized by the sum its own lane forms)
-__device__ __forceinline__ float row16_sum(float v) {
-  v += dpp_f32<kDppXor1>(v);
-  v += dpp_f32<kDppXor2>(v);
-  v += dpp_f32<kDppRor4>(v);
-  v += dpp_f32<kDppRor8>(v);
-  return v;
-}
 
 // Inclusive prefix sum over the wave's lanes (every lane active): steps of
 // 1, 2, 4, 8 lanes within each 16-lane row (DPP row_shr; a lane shifted in
@@ -133,65 +72,12 @@ __device__ __forceinline__ int2 scan256_pair(int& a, int& b, int tid, int (&s_to
 }
 
 // ---------------------------------------------------------------------------
-// Router: the k largest logits of one token, ties to the smaller expert
-// index, slots in descending order; weights = exp(l_j - l_0) normalized over
-// the k slots (the softmax over all experts restricted to the chosen k).
-// Keys order the logits as binary32 compares do (-0 as +0) and, on equal
-// values, put the smaller expert first.
-//
-// Both routers below first sort each lane's keys (largest first) with
-// Batcher's odd-even merge sorting network (K. E. Batcher, "Sorting networks
-// and their applications", AFIPS 1968), so that each of the k selection
-// rounds only takes the maximum of the lanes' heads and pops the winning
-// lane's list.  Keys are unique (the expert index is part of them).  Slot j
-// ends in lane j of the token's lanes, and its weight is normalized by the
-// row-16 sum over the first 16 of them, so both routers give the same ids
-// and the same weights.
-// ---------------------------------------------------------------------------
-__device__ __forceinline__ void key_cx(uint64_t& a, uint64_t& b) {
-  const bool sw = b > a;
-  const uint64_t hi = sw ? b : a, lo = sw ? a : b;
-  a = hi;
-  b = lo;
-}
-
-template <int N>
-__device__ __forceinline__ void sort_keys_desc(uint64_t (&c)[N]) {
-#pragma unroll
-  for (int p = 1; p < N; p <<= 1)
-#pragma unroll
-    for (int d = p; d >= 1; d >>= 1)
-#pragma unroll
-      for (int j = d % p; j + d < N; j += 2 * d)
-#pragma unroll
-        for (int i = 0; i < d; ++i)
-          if (i + j + d < N && (i + j) / (2 * p) == (i + j + d) / (2 * p)) key_cx(c[i + j], c[i + j + d]);
-}
-
-// The k selection rounds over the lanes' sorted lists (KMAX >= k rounds at
-// most): each round takes the largest head over the 16-lane row (or the
-// wave) and pops it from the lane that held it; lane j keeps round j's key.
-// After round j at most KMAX - 1 - j more pops follow, so only that many
-// leading entries of a list can still become its head and only those are
-// shifted.
-template <int N, int KMAX, bool WAVE>
-__device__ __forceinline__ void select_rounds(uint64_t (&cand)[N], int k, int lane, uint64_t& mine,
-                                              uint64_t& top) {
-#pragma unroll
-  for (int j = 0; j < KMAX; ++j) {
-    if (j < k) {
-      const uint64_t best = key_max<WAVE>(cand[0]);
-      if (j == 0) top = best;
-      mine = lane == j ? best : mine;
-      const bool pop = cand[0] == best;  // this lane held the winner
-#pragma unroll
-      for (int i = 0; i < N && i + 1 < KMAX - j; ++i) cand[i] = pop ? (i + 1 < N ? cand[i + 1] : 0ull) : cand[i];
-    }
-  }
-}
-
+// Routers of the k largest logits (rule, keys and selection in route.hpp).
 // One wave per token (few tokens: the shortest dependency chain); lane l
 // holds experts l, l + 64, ...; lane j < k returns slot j.
+// (KPL = 0 in the prologue kernels below: the ids and weights are already in
+// place, written by the workspace's router on the same stream, and only the
+// schedule is built.)
 template <int KPW>
 __device__ void route_token_wave(const float* __restrict__ lrow, int E, int k, int lane, int& my_id,
                                  float& my_w) {
@@ -252,13 +138,17 @@ __global__ __launch_bounds__(256) void moe_route_kernel(FwdParams p, int tpb) {
       quantize_row_wave<NB>(p.x + t * H, H / 16, p.xq_codes + t * (H / 2), p.xq_scales + t * (H / 16),
                             p.xq_g + t, lane, p.xq16 ? p.xq16 + t * H : nullptr, p.static_g);
     }
-    int id;
-    float w;
-    route_token_wave<KPL>(p.logits + t * p.E, p.E, k, lane, id, w);
-    if (lane < k) {
-      p.topk_ids[t * k + lane] = id;
-      p.topk_w[t * k + lane] = w;
-      s_ids[lt * k + lane] = id;
+    if constexpr (KPL == 0) {
+      if (lane < k) s_ids[lt * k + lane] = p.topk_ids[t * k + lane];
+    } else {
+      int id;
+      float w;
+      route_token_wave<KPL>(p.logits + t * p.E, p.E, k, lane, id, w);
+      if (lane < k) {
+        p.topk_ids[t * k + lane] = id;
+        p.topk_w[t * k + lane] = w;
+        s_ids[lt * k + lane] = id;
+      }
     }
     if (!p.deterministic) {
       float4* row = reinterpret_cast<float4*>(p.out_acc + t * H);
@@ -475,17 +365,21 @@ __global__ __launch_bounds__(kSmallThreads) void moe_prologue_small_kernel(FwdPa
   __shared__ int s_tot[2][4];
   const int tid = threadIdx.x;
   // 1. routing, 4 tokens per wave at a time
-  const int grp = lane >> 4, gl = lane & 15;
-  for (int t0 = wave * 4; t0 < T; t0 += kSmallWaves * 4) {
-    const int t = t0 + grp;
-    const int tc = t < T ? t : T - 1;
-    int id;
-    float w;
-    route_token_group16<KPL>(p.logits + static_cast<int64_t>(tc) * E, E, k, gl, id, w);
-    if (t < T && gl < k) {
-      p.topk_ids[t * k + gl] = id;
-      p.topk_w[t * k + gl] = w;
-      s_ids[t * k + gl] = id;
+  if constexpr (KPL == 0) {
+    for (int i = tid; i < R; i += kSmallThreads) s_ids[i] = p.topk_ids[i];
+  } else {
+    const int grp = lane >> 4, gl = lane & 15;
+    for (int t0 = wave * 4; t0 < T; t0 += kSmallWaves * 4) {
+      const int t = t0 + grp;
+      const int tc = t < T ? t : T - 1;
+      int id;
+      float w;
+      route_token_group16<KPL>(p.logits + static_cast<int64_t>(tc) * E, E, k, gl, id, w);
+      if (t < T && gl < k) {
+        p.topk_ids[t * k + gl] = id;
+        p.topk_w[t * k + gl] = w;
+        s_ids[t * k + gl] = id;
+      }
     }
   }
   for (int i = tid; i < (kSmallMaxR / 64) * kSmallMaxE; i += kSmallThreads) (&s_cnt[0][0])[i] = 0;
@@ -671,8 +565,10 @@ __global__ __launch_bounds__(kSmallThreads) void moe_route64_kernel(FwdParams p,
   const int b = blockIdx.x, t0 = b * kRoute64Tokens;
   const int ntok = min(kRoute64Tokens, T - t0), n = ntok * k;
   // 1. routing: wave w, group g routes token t0 + 4 w + g
-  const int grp = lane >> 4, gl = lane & 15;
-  {
+  if constexpr (KPL == 0) {
+    if (tid < n) s_ids[tid] = p.topk_ids[static_cast<int64_t>(t0) * k + tid];
+  } else {
+    const int grp = lane >> 4, gl = lane & 15;
     const int lt = 4 * wave + grp;
     const int tc = t0 + min(lt, ntok - 1);
     int id;
@@ -819,7 +715,13 @@ __global__ __launch_bounds__(kSmallThreads) void moe_prologue_tiny_kernel(FwdPar
   // token w with all its lanes (the shortest chain: the block's routing is
   // the prologue's critical path); more: wave w, group g routes token
   // 4 w + g.  Waves past the last token skip it.
-  if (T <= kTinyWaveRouteT) {
+  if constexpr (KPL == 0) {
+    if (tid < T * k) {
+      const int id = p.topk_ids[tid];
+      s_ids[tid] = id;
+      atomicOr(reinterpret_cast<unsigned long long*>(&s_mask[id]), 1ull << (tid / k));
+    }
+  } else if (T <= kTinyWaveRouteT) {
     if (wave < T) {
       int id;
       float w;
@@ -898,7 +800,8 @@ bool use_tiny_prologue(const FwdParams& p) {
 template <int NBL>
 static void launch_prologue_tiny(const FwdParams& p, hipStream_t s) {
   const int blocks = 1 + (p.T + 3) / 4;
-  if (p.E <= 16) moe_prologue_tiny_kernel<NBL, 1><<<blocks, kSmallThreads, 0, s>>>(p);
+  if (p.routed) moe_prologue_tiny_kernel<NBL, 0><<<blocks, kSmallThreads, 0, s>>>(p);
+  else if (p.E <= 16) moe_prologue_tiny_kernel<NBL, 1><<<blocks, kSmallThreads, 0, s>>>(p);
   else if (p.E <= 32) moe_prologue_tiny_kernel<NBL, 2><<<blocks, kSmallThreads, 0, s>>>(p);
   else if (p.E <= 64) moe_prologue_tiny_kernel<NBL, 4><<<blocks, kSmallThreads, 0, s>>>(p);
   else if (p.E <= 128) moe_prologue_tiny_kernel<NBL, 8><<<blocks, kSmallThreads, 0, s>>>(p);
@@ -912,7 +815,8 @@ bool use_small_prologue(const FwdParams& p) {
 template <int NB>
 static void launch_prologue_small(const FwdParams& p, hipStream_t s) {
   const int blocks = 1 + (p.T + kSmallWaves - 1) / kSmallWaves;
-  if (p.E <= 16) moe_prologue_small_kernel<NB, 1><<<blocks, kSmallThreads, 0, s>>>(p);
+  if (p.routed) moe_prologue_small_kernel<NB, 0><<<blocks, kSmallThreads, 0, s>>>(p);
+  else if (p.E <= 16) moe_prologue_small_kernel<NB, 1><<<blocks, kSmallThreads, 0, s>>>(p);
   else if (p.E <= 32) moe_prologue_small_kernel<NB, 2><<<blocks, kSmallThreads, 0, s>>>(p);
   else if (p.E <= 64) moe_prologue_small_kernel<NB, 4><<<blocks, kSmallThreads, 0, s>>>(p);
   else if (p.E <= 128) moe_prologue_small_kernel<NB, 8><<<blocks, kSmallThreads, 0, s>>>(p);
@@ -1055,7 +959,9 @@ hipError_t launch_copy_f32(const float* src, float* dst, int64_t n, hipStream_t 
 
 template <int NB>
 static void launch_route(const FwdParams& p, int nblocks, int tpb, hipStream_t s) {
-  if (p.E <= 128)
+  if (p.routed)
+    moe_route_kernel<NB, 0><<<nblocks, 256, 0, s>>>(p, tpb);
+  else if (p.E <= 128)
     moe_route_kernel<NB, 2><<<nblocks, 256, 0, s>>>(p, tpb);
   else if (p.E <= 256)
     moe_route_kernel<NB, 4><<<nblocks, 256, 0, s>>>(p, tpb);
@@ -1072,7 +978,8 @@ template <int NB, int QB>
 static void launch_route64(const FwdParams& p, hipStream_t s) {
   const int nr = (p.T + kRoute64Tokens - 1) / kRoute64Tokens;
   const int nq = QB > 0 ? (p.T + 3) / 4 : (p.T + kSmallWaves - 1) / kSmallWaves;
-  if (p.E <= 16) moe_route64_kernel<NB, 1, QB><<<nr + nq, kSmallThreads, 0, s>>>(p, nr);
+  if (p.routed) moe_route64_kernel<NB, 0, QB><<<nr + nq, kSmallThreads, 0, s>>>(p, nr);
+  else if (p.E <= 16) moe_route64_kernel<NB, 1, QB><<<nr + nq, kSmallThreads, 0, s>>>(p, nr);
   else if (p.E <= 32) moe_route64_kernel<NB, 2, QB><<<nr + nq, kSmallThreads, 0, s>>>(p, nr);
   else if (p.E <= 64) moe_route64_kernel<NB, 4, QB><<<nr + nq, kSmallThreads, 0, s>>>(p, nr);
   else if (p.E <= 128) moe_route64_kernel<NB, 8, QB><<<nr + nq, kSmallThreads, 0, s>>>(p, nr);
@@ -1080,9 +987,13 @@ static void launch_route64(const FwdParams& p, hipStream_t s) {
   moe_place64_kernel<<<nr, kSmallThreads, 0, s>>>(p, nr);
 }
 
-hipError_t launch_moe_forward(const FwdParams& p, int max_tiles, hipStream_t s,
+hipError_t launch_moe_forward(const FwdParams& p, const RouteParams* route, int max_tiles, hipStream_t s,
                               hipEvent_t const* ev) {
   if (ev) (void)hipEventRecord(ev[0], s);
+  if (route) {
+    const hipError_t re = launch_route_scores(*route, s);
+    if (re != hipSuccess) return re;
+  }
   if (use_tiny_prologue(p)) {
     const int nbl = (p.H / 16 + 255) / 256;
     if (nbl <= 1) launch_prologue_tiny<1>(p, s);

@@ -49,6 +49,7 @@ struct FwdBuffers {
   // library copies of the per-expert global scales (own_gscales)
   float* w13g;
   float* w2g;
+  float* route_bias;  // [E] the workspace router's bias (own_gscales)
 };
 
 bool cfg_has_shared(const moe_config& c);
@@ -81,11 +82,29 @@ struct XQ {
   const float* g;
 };
 
+// The router of a forward: on = false is the k largest logits, softmax over
+// them.
+struct RouterView {
+  bool on;
+  moe_router rule;
+  const float* bias;  // NULL: none
+};
+
+// Checks of a router against E experts and top_k; NVFP4_OK or a status with
+// the error message set.
+int check_router(const moe_router* r, int64_t E, int64_t top_k);
+// The kernel's parameters of a checked router.
+RouteParams route_params(const moe_router& r, int64_t E, int64_t top_k);
+
+bool aligned(const void* p, uintptr_t a);
+bool overlap(const void* a, int64_t na, const void* b, int64_t nb);
+int hip_fail(hipError_t e, const char* what);
+
 // Host checks, then the forward's kernels on `s` (no allocation, no host
 // synchronization).  static_scales_set: the act_scales buffer holds values
 // (required with MOE_STATIC_ACT_SCALES).
 int run_forward(const moe_config& c, const FwdBuffers& b, const WeightView& w, bool static_scales_set,
-                const void* x, const XQ& xq, const float* logits, int64_t T, void* out, hipStream_t s,
+                const RouterView& router, const void* x, const XQ& xq, const float* logits, int64_t T, void* out, hipStream_t s,
                 const hipEvent_t* events);
 
 // Checks of a packed-weights descriptor against a configuration.

@@ -95,6 +95,6 @@ extern "C" int moe_nvfp4_forward_noalloc(const moe_config* cfg, const moe_nvfp4_
   nvfp4::layout_buffers(c, T, false, base, &b);
   const nvfp4::WeightView wv{static_cast<const uint8_t*>(w->w13), static_cast<const uint8_t*>(w->w2),
                              w->w13_gscale, w->w2_gscale};
-  return nvfp4::run_forward(c, b, wv, false, x_dev, nvfp4::XQ{false, nullptr, nullptr, nullptr}, logits_dev, T,
+  return nvfp4::run_forward(c, b, wv, false, nvfp4::RouterView{}, x_dev, nvfp4::XQ{false, nullptr, nullptr, nullptr}, logits_dev, T,
                             out_dev, static_cast<hipStream_t>(stream), nullptr);
 }
