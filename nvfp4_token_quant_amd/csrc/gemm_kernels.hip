@@ -44,24 +44,6 @@ __device__ __forceinline__ uint32_t word_of(const uint4& v, int q) {
   return q == 0 ? v.x : q == 1 ? v.y : q == 2 ? v.z : v.w;
 }
 
-// Workgroup barrier for LDS data only.  A full __syncthreads also waits for
-// every outstanding global load and store (the global->LDS copies count as
-// loads), which would drain the weight prefetch or wait for output stores;
-// here the caller has already waited for the copies it needs, this wave's
-// LDS accesses are complete (lgkmcnt 0), and the memory clobber keeps the
-// compiler from moving memory accesses across the barrier.
-__device__ __forceinline__ void lds_barrier() {
-  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-}
-
-// s_waitcnt with only the vector-memory counter limited (gfx9 encoding:
-// vmcnt bits [3:0] and [15:14], expcnt [6:4] and lgkmcnt [11:8] left at max).
-template <int N>
-__device__ __forceinline__ void wait_vmcnt() {
-  static_assert(N >= 0 && N < 64, "vmcnt range");
-  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
-}
-
 // ---------------------------------------------------------------------------
 // Epilogues.
 // ---------------------------------------------------------------------------

@@ -258,7 +258,256 @@ __global__ __launch_bounds__(64 * W) void int8_stream_kernel(Int8GemmParams p) {
   }
 }
 
+// ---------------------------------------------------------------------------
+// Tiled product for many tokens.  A block of WM x WN waves computes BM = 16 FM
+// WM tokens by BN = 16 FN WN channels; K goes by in steps of 128 bytes through
+// two LDS buffers.
+//
+// Copies go from global memory straight to LDS, one instruction for 8 rows of
+// 128 bytes (whole lines).  The 16-byte pieces of a row are permuted by a key
+// of the row, so that the eight lanes of an LDS read that take the same piece
+// of different rows touch different banks.  Token fragments are read from LDS
+// kAhead ahead of their MFMAs, across the step's barrier too: the last kAhead
+// fragments of a step are in registers when its buffer is handed back, so
+// their MFMAs run while the next step's first fragments are read and the
+// copies of the step after it start, a whole step before they are needed.
+//
+// Fragment f of a wave's channels holds channels 4 FN (r / 4) + 4 f + r % 4
+// (r its row), so a lane ends with 4 FN consecutive channels of a token and
+// stores them as whole 16-byte pieces.
+// ---------------------------------------------------------------------------
+constexpr int kStepBytes = 128;
+constexpr int kAhead = 3;
+
+template <int FN>
+__device__ __forceinline__ int channel_key(int row) { return (row & 3) | ((row / (4 * FN) & 1) << 2); }
+
+// Lane's part of the result: tokens t0 + 16 m, channels n0 .. n0 + 4 FN - 1.
+template <typename T, int FM, int FN>
+__device__ __forceinline__ void store_tile(const Int8GemmParams& p, const i32x4 (&acc)[FN][FM], int t0, int n0) {
+  float sb[4 * FN], bias[4 * FN];
+#pragma unroll
+  for (int i = 0; i < 4 * FN; ++i) {
+    const int n = min(n0 + i, p.N - 1);
+    sb[i] = p.sb[n];
+    bias[i] = p.bias ? p.bias[n] : 0.0f;
+  }
+#pragma unroll
+  for (int m = 0; m < FM; ++m) {
+    const int t = t0 + 16 * m;
+    if (t >= p.M) continue;
+    const float sa = p.sa[t];
+    const int64_t row = static_cast<int64_t>(t) * p.ldo;
+#pragma unroll
+    for (int f = 0; f < FN; f += 2) {
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        v[i] = static_cast<float>(acc[f + i / 4][m][i % 4]) * (sa * sb[4 * f + i]);
+        if (p.bias) v[i] += bias[4 * f + i];
+      }
+      const int n = n0 + 4 * f;
+      if (p.vec_out && n + 8 <= p.N) {
+        store8<T>(p.out, row + n, v);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (n + i < p.N) T::put(p.out, row + n + i, v[i]);
+      }
+    }
+  }
+}
+
+template <int WM, int WN, int FM, int FN>
+__global__ __launch_bounds__(64 * WM * WN)
+__attribute__((amdgpu_waves_per_eu(WM * WN / 4, WM * WN / 4))) void int8_tiled_kernel(Int8GemmParams p, int mtiles,
+                                                                                  int ntiles) {
+  constexpr int W = WM * WN, BM = 16 * FM * WM, BN = 16 * FN * WN;
+  constexpr int kStage = (BM + BN) * kStepBytes;
+  constexpr int NC = (BM + BN) / 8 / W;  // copy instructions of a wave and step
+  constexpr int NCA = BM / 8 / W;        // the token rows' part of them
+  constexpr int NI = 2 * FM;             // token fragments of a step
+  static_assert((BM / 8) % W == 0 && (BN / 8) % W == 0, "whole copies of each operand");
+  static_assert(FM > kAhead && FN % 2 == 0, "the window stays inside a half step");
+  extern __shared__ __align__(1024) uint8_t s_tile[];  // 2 * kStage
+  const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
+  const int r = lane & 15, g = lane >> 4;
+
+  // Tile of this block: each XCD (block % 8) takes a contiguous run of tiles,
+  // ordered in bands of 8 token tiles, so that the blocks that share an L2
+  // share operands.
+  const int total = mtiles * ntiles;
+  int id = blockIdx.x;
+  {
+    const int q = total / 8, rem = total % 8, x = id & 7;
+    id = x * q + min(x, rem) + (id >> 3);
+  }
+  const int band = id / (8 * ntiles), in_band = id - band * 8 * ntiles;
+  const int bh = min(8, mtiles - 8 * band);
+  const int m0 = (8 * band + in_band % bh) * BM, n0 = in_band / bh * BN;
+
+  // copies: instruction u of this wave fills LDS rows 8 (wave + W u) .. + 7 of
+  // the stage (token rows, then channel rows); lane l the piece l % 8 of row
+  // l / 8.  Rows behind the last one read that one again (never stored).
+  const int K16 = (p.K + 15) / 16 * 16;
+  const int mrows = min(BM, p.M - m0), nrows = min(BN, p.N - n0);
+  const auto rs_of = [&](const int8_t* base, int64_t bytes) {
+    // dword 3 = 0x00020000: 32-bit data format, no swizzle (raw buffer)
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t*>(base), static_cast<short>(0),
+                                             static_cast<int>(bytes), 0x00020000);
+  };
+  const __amdgpu_buffer_rsrc_t rsa = rs_of(p.a + m0 * p.lda, (mrows - 1) * p.lda + K16);
+  const __amdgpu_buffer_rsrc_t rsb = rs_of(p.b + n0 * p.ldb, (nrows - 1) * p.ldb + K16);
+  const int slot = lane & 7, sub = lane >> 3;
+  int off[NC];
+#pragma unroll
+  for (int u = 0; u < NC; ++u) {
+    const int row = 8 * (wave + W * u) + sub;
+    off[u] = u < NCA ? min(row, mrows - 1) * static_cast<int>(p.lda) + 16 * (slot ^ (row & 7))
+                     : min(row - BM, nrows - 1) * static_cast<int>(p.ldb) + 16 * (slot ^ channel_key<FN>(row - BM));
+  }
+  const int S = (p.K + kStepBytes - 1) / kStepBytes;
+  const bool ragged = p.K % kStepBytes != 0;
+  // in the last step a piece behind K reads the row's last one instead (cleared
+  // below): the bytes to go back, for the token and the channel rows (whose
+  // keys do not depend on u)
+  static_assert(W % FN == 0, "a wave's channel rows of all its copies have one key");
+  const int past = kStepBytes * (S - 1) - (K16 - 16);
+  const int back_a = max(0, past + 16 * (slot ^ sub));
+  const int back_b = max(0, past + 16 * (slot ^ channel_key<FN>(8 * wave + sub)));
+  const auto copy = [&](int s, uint8_t* stage, int u) {
+    const int o = off[u] - (s == S - 1 ? (u < NCA ? back_a : back_b) : 0);
+    auto* d = (__attribute__((address_space(3))) void*)(stage + 1024 * (wave + W * u));
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(u < NCA ? rsa : rsb, d, 16, o, kStepBytes * s, 0, 0);
+  };
+
+  // fragment reads: token row 16 m + r, channel row 4 FN (r / 4) + 4 f + r % 4;
+  // the second half's piece number differs in bit 2
+  const int wm = wave / WN, wn = wave % WN;
+  const int crow = 16 * FN * wn + 4 * FN * (r >> 2) + (r & 3);
+  const int xbase = (16 * FM * wm + r) * kStepBytes + 16 * (g ^ (r & 7));
+  const int wbase = (BM + crow) * kStepBytes + 16 * (g ^ channel_key<FN>(crow));
+  i32x4 acc[FN][FM];
+#pragma unroll
+  for (int f = 0; f < FN; ++f)
+#pragma unroll
+    for (int m = 0; m < FM; ++m) acc[f][m] = i32x4{0, 0, 0, 0};
+  i32x4 x[kAhead + 1], w[2][FN];
+  const auto read_x = [&](const uint8_t* stage, int i) {
+    return *reinterpret_cast<const i32x4*>(stage + (xbase ^ (64 * (i / FM))) + 16 * kStepBytes * (i % FM));
+  };
+  const auto read_w = [&](const uint8_t* stage, int h, int f) {
+    return *reinterpret_cast<const i32x4*>(stage + (wbase ^ (64 * h)) + 4 * kStepBytes * f);
+  };
+  // In the last step of a K that is no multiple of 128: zeros for the token
+  // bytes from K on.
+  const auto clear = [&](uint8_t* stage) {
+    for (int i = tid; i < BM * 8; i += 64 * W) {
+      const int c = kStepBytes * (S - 1) + 16 * ((i & 7) ^ (i >> 3 & 7));
+      i32x4* at = reinterpret_cast<i32x4*>(stage + 16 * i);
+      i32x4 v = *at;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int left = p.K - c - 4 * j;
+        if (left < 4) v[j] = left <= 0 ? 0 : v[j] & static_cast<int32_t>((1u << (8 * left)) - 1u);
+      }
+      *at = v;
+    }
+    lds_barrier();
+  };
+
+#pragma unroll
+  for (int u = 0; u < NC; ++u) copy(0, s_tile, u);
+#pragma unroll
+  for (int u = 0; u < NC; ++u) copy(min(1, S - 1), s_tile + kStage, u);
+  wait_vmcnt<NC>();
+  lds_barrier();
+  if (S == 1 && ragged) clear(s_tile);
+#pragma unroll
+  for (int f = 0; f < FN; ++f) w[0][f] = read_w(s_tile, 0, f);
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) x[i] = read_x(s_tile, i);
+
+  // One step on buffer `cur`, whose first kAhead token and first-half channel
+  // fragments are in registers.  In the last steps the copies and the reads of
+  // the next step are of data that nothing uses.
+  const auto mma = [&](int i) {
+#pragma unroll
+    for (int f = 0; f < FN; ++f)
+      acc[f][i % FM] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[i / FM][f], x[i % (kAhead + 1)], acc[f][i % FM], 0, 0, 0);
+  };
+  static_assert(NI % (kAhead + 1) == 0, "the window's slots repeat every step");
+  const auto step = [&](int s, uint8_t* cur, uint8_t* nxt) {
+#pragma unroll
+    for (int i = 0; i < NI - kAhead; ++i) {
+      x[(i + kAhead) % (kAhead + 1)] = read_x(cur, i + kAhead);
+      if (i < FN) w[1][i] = read_w(cur, 1, i);
+      mma(i);
+    }
+    // keep this order: reads kAhead ahead, between the MFMAs
+#pragma unroll
+    for (int i = 0; i < NI - kAhead; ++i) {
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);  // LDS reads
+      if (i < FN) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x008, FN, 0);              // MFMAs
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    wait_vmcnt<0>();
+    lds_barrier();  // step s + 1 has landed; every wave has read step s
+    if (ragged && s + 2 == S) clear(nxt);
+#pragma unroll
+    for (int f = 0; f < FN; ++f) w[0][f] = read_w(nxt, 0, f);
+    const int sn = min(s + 2, S - 1);
+#pragma unroll
+    for (int i = NI - kAhead; i < NI; ++i) {
+      mma(i);
+      x[(i + kAhead) % (kAhead + 1)] = read_x(nxt, i + kAhead - NI);
+#pragma unroll
+      for (int u = 0; u < NC; ++u)
+        if (u % kAhead == i - (NI - kAhead)) copy(sn, cur, u);
+    }
+    __builtin_amdgcn_sched_group_barrier(0x100, FN, 0);
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      __builtin_amdgcn_sched_group_barrier(0x008, FN / 2, 0);
+      __builtin_amdgcn_sched_group_barrier(0x010, NC / kAhead, 0);  // copies
+      if (i < NC % kAhead) __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x008, FN / 2, 0);
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  int s = 0;
+  for (; s + 1 < S; s += 2) {
+    step(s, s_tile, s_tile + kStage);
+    step(s + 1, s_tile + kStage, s_tile);
+  }
+  if (s < S) step(s, s_tile, s_tile + kStage);
+  wait_vmcnt<0>();  // no copy may land in LDS after the block has ended
+
+  const int t0 = m0 + 16 * FM * wm + r, nl = n0 + 16 * FN * wn + 4 * FN * g;
+  if (p.dtype == MOE_BF16) store_tile<Bf16, FM, FN>(p, acc, t0, nl);
+  else if (p.dtype == MOE_F16) store_tile<F16, FM, FN>(p, acc, t0, nl);
+  else store_tile<F32, FM, FN>(p, acc, t0, nl);
+}
+
+template <int WM, int WN, int FM, int FN>
+static hipError_t launch_tiled(const Int8GemmParams& p, hipStream_t s) {
+  constexpr int BM = 16 * FM * WM, BN = 16 * FN * WN;
+  constexpr int kLds = 2 * (BM + BN) * kStepBytes;
+  const int64_t mt = (static_cast<int64_t>(p.M) + BM - 1) / BM, nt = (static_cast<int64_t>(p.N) + BN - 1) / BN;
+  if (mt * nt * 8 > INT32_MAX) return hipErrorInvalidConfiguration;
+  const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(int8_tiled_kernel<WM, WN, FM, FN>),
+                                           hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
+  if (e != hipSuccess) return e;
+  int8_tiled_kernel<WM, WN, FM, FN><<<static_cast<unsigned>(mt * nt), 64 * WM * WN, kLds, s>>>(
+      p, static_cast<int>(mt), static_cast<int>(nt));
+  return hipGetLastError();
+}
+
 hipError_t launch_int8_matmul(const Int8GemmParams& p, hipStream_t s) {
+  // (the tiled kernel addresses a tile's rows with 32-bit byte offsets)
+  if (p.M > 128 && p.lda < (1 << 22) && p.ldb < (1 << 22)) return launch_tiled<2, 4, 8, 4>(p, s);
   const int64_t nt = (static_cast<int64_t>(p.N) + 15) / 16, mt = p.M <= 16 ? 1 : (static_cast<int64_t>(p.M) + 63) / 64;
   if (nt * mt > INT32_MAX) return hipErrorInvalidConfiguration;
   if (p.M <= 16) int8_stream_kernel<1, 4><<<static_cast<unsigned>(nt), 256, 0, s>>>(p);

@@ -272,6 +272,7 @@ int int8_matmul(const void* a_dev, int64_t lda, const float* scale_a_dev, const 
   p.N = static_cast<int>(N);
   p.K = static_cast<int>(K);
   p.dtype = dtype;
+  p.vec_out = row_vectors(out_dev, ldo, bytes) ? 1 : 0;
   hipError_t e = launch_int8_matmul(p, static_cast<hipStream_t>(stream));
   if (e != hipSuccess) return hip_fail(e, "int8_matmul launch");
   return api_ok();
