@@ -282,6 +282,43 @@ constexpr int kAhead = 3;
 template <int FN>
 __device__ __forceinline__ int channel_key(int row) { return (row & 3) | ((row / (4 * FN) & 1) << 2); }
 
+// Origin of this block's tile: each XCD (block % 8) takes a contiguous run of
+// tiles, ordered in bands of 4 token tiles, so that the blocks that share an
+// L2 share operands.
+template <int BM, int BN>
+__device__ __forceinline__ void tile_origin(int mtiles, int ntiles, int& m0, int& n0) {
+  const int total = mtiles * ntiles, x = blockIdx.x & 7;
+  const int id = x * (total / 8) + min(x, total % 8) + (static_cast<int>(blockIdx.x) >> 3);
+  const int band = id / (4 * ntiles), in_band = id - band * 4 * ntiles;
+  const int bh = min(4, mtiles - 4 * band);
+  m0 = (4 * band + in_band % bh) * BM;
+  n0 = in_band / bh * BN;
+}
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t code_rsrc(const int8_t* base, int64_t bytes) {
+  // dword 3 = 0x00020000: 32-bit data format, no swizzle (raw buffer)
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t*>(base), static_cast<short>(0),
+                                           static_cast<int>(bytes), 0x00020000);
+}
+
+// In the last step (columns c0 .. of a K that is no multiple of 128): zeros for
+// the bytes of the BM token rows in LDS from K on.
+template <int BM, int THREADS>
+__device__ __forceinline__ void clear_behind(uint8_t* rows, int c0, int K) {
+  for (int i = threadIdx.x; i < BM * 8; i += THREADS) {
+    const int c = c0 + 16 * ((i & 7) ^ (i >> 3 & 7));
+    i32x4* at = reinterpret_cast<i32x4*>(rows + 16 * i);
+    i32x4 v = *at;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int left = K - c - 4 * j;
+      if (left < 4) v[j] = left <= 0 ? 0 : v[j] & static_cast<int32_t>((1u << (8 * left)) - 1u);
+    }
+    *at = v;
+  }
+  lds_barrier();
+}
+
 // Lane's part of the result: tokens t0 + 16 m, channels n0 .. n0 + 4 FN - 1.
 template <typename T, int FM, int FN>
 __device__ __forceinline__ void store_tile(const Int8GemmParams& p, const i32x4 (&acc)[FN][FM], int t0, int n0) {
@@ -333,31 +370,16 @@ __attribute__((amdgpu_waves_per_eu(WM * WN / 4, WM * WN / 4))) void int8_tiled_k
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
   const int r = lane & 15, g = lane >> 4;
 
-  // Tile of this block: each XCD (block % 8) takes a contiguous run of tiles,
-  // ordered in bands of 8 token tiles, so that the blocks that share an L2
-  // share operands.
-  const int total = mtiles * ntiles;
-  int id = blockIdx.x;
-  {
-    const int q = total / 8, rem = total % 8, x = id & 7;
-    id = x * q + min(x, rem) + (id >> 3);
-  }
-  const int band = id / (8 * ntiles), in_band = id - band * 8 * ntiles;
-  const int bh = min(8, mtiles - 8 * band);
-  const int m0 = (8 * band + in_band % bh) * BM, n0 = in_band / bh * BN;
+  int m0, n0;
+  tile_origin<BM, BN>(mtiles, ntiles, m0, n0);
 
   // copies: instruction u of this wave fills LDS rows 8 (wave + W u) .. + 7 of
   // the stage (token rows, then channel rows); lane l the piece l % 8 of row
   // l / 8.  Rows behind the last one read that one again (never stored).
   const int K16 = (p.K + 15) / 16 * 16;
   const int mrows = min(BM, p.M - m0), nrows = min(BN, p.N - n0);
-  const auto rs_of = [&](const int8_t* base, int64_t bytes) {
-    // dword 3 = 0x00020000: 32-bit data format, no swizzle (raw buffer)
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t*>(base), static_cast<short>(0),
-                                             static_cast<int>(bytes), 0x00020000);
-  };
-  const __amdgpu_buffer_rsrc_t rsa = rs_of(p.a + m0 * p.lda, (mrows - 1) * p.lda + K16);
-  const __amdgpu_buffer_rsrc_t rsb = rs_of(p.b + n0 * p.ldb, (nrows - 1) * p.ldb + K16);
+  const __amdgpu_buffer_rsrc_t rsa = code_rsrc(p.a + m0 * p.lda, (mrows - 1) * p.lda + K16);
+  const __amdgpu_buffer_rsrc_t rsb = code_rsrc(p.b + n0 * p.ldb, (nrows - 1) * p.ldb + K16);
   const int slot = lane & 7, sub = lane >> 3;
   int off[NC];
 #pragma unroll
@@ -393,85 +415,98 @@ __attribute__((amdgpu_waves_per_eu(WM * WN / 4, WM * WN / 4))) void int8_tiled_k
 #pragma unroll
     for (int m = 0; m < FM; ++m) acc[f][m] = i32x4{0, 0, 0, 0};
   i32x4 x[kAhead + 1], w[2][FN];
+  // fragment i of a step: four token groups in the first half, the same four
+  // in the second, then the other four
+  static_assert(FM == 8, "two groups of four");
+  const auto half_of = [](int i) { return i / 4 % 2; };
+  const auto group_of = [](int i) { return 4 * (i / 8) + i % 4; };
   const auto read_x = [&](const uint8_t* stage, int i) {
-    return *reinterpret_cast<const i32x4*>(stage + (xbase ^ (64 * (i / FM))) + 16 * kStepBytes * (i % FM));
+    return *reinterpret_cast<const i32x4*>(stage + (xbase ^ (64 * half_of(i))) + 16 * kStepBytes * group_of(i));
   };
   const auto read_w = [&](const uint8_t* stage, int h, int f) {
     return *reinterpret_cast<const i32x4*>(stage + (wbase ^ (64 * h)) + 4 * kStepBytes * f);
   };
-  // In the last step of a K that is no multiple of 128: zeros for the token
-  // bytes from K on.
-  const auto clear = [&](uint8_t* stage) {
-    for (int i = tid; i < BM * 8; i += 64 * W) {
-      const int c = kStepBytes * (S - 1) + 16 * ((i & 7) ^ (i >> 3 & 7));
-      i32x4* at = reinterpret_cast<i32x4*>(stage + 16 * i);
-      i32x4 v = *at;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int left = p.K - c - 4 * j;
-        if (left < 4) v[j] = left <= 0 ? 0 : v[j] & static_cast<int32_t>((1u << (8 * left)) - 1u);
-      }
-      *at = v;
-    }
-    lds_barrier();
-  };
-
 #pragma unroll
   for (int u = 0; u < NC; ++u) copy(0, s_tile, u);
 #pragma unroll
   for (int u = 0; u < NC; ++u) copy(min(1, S - 1), s_tile + kStage, u);
   wait_vmcnt<NC>();
   lds_barrier();
-  if (S == 1 && ragged) clear(s_tile);
+  if (S == 1 && ragged) clear_behind<BM, 64 * W>(s_tile, kStepBytes * (S - 1), p.K);
 #pragma unroll
   for (int f = 0; f < FN; ++f) w[0][f] = read_w(s_tile, 0, f);
 #pragma unroll
   for (int i = 0; i < kAhead; ++i) x[i] = read_x(s_tile, i);
 
-  // One step on buffer `cur`, whose first kAhead token and first-half channel
-  // fragments are in registers.  In the last steps the copies and the reads of
-  // the next step are of data that nothing uses.
   const auto mma = [&](int i) {
+    const int m = group_of(i);
 #pragma unroll
     for (int f = 0; f < FN; ++f)
-      acc[f][i % FM] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[i / FM][f], x[i % (kAhead + 1)], acc[f][i % FM], 0, 0, 0);
+      acc[f][m] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[half_of(i)][f], x[i % (kAhead + 1)], acc[f][m], 0, 0, 0);
   };
-  static_assert(NI % (kAhead + 1) == 0, "the window's slots repeat every step");
+  static_assert(NI == 16 && NI % (kAhead + 1) == 0 && kAhead <= 4, "the window's slots repeat every step");
+  // Copies of the rows that are read by the middle of a step (all channel
+  // rows, the token rows of the first four groups), and of the others.
+  static_assert(W == FM, "a copy of each wave fills the rows of four groups");
+  constexpr int kEarly = NC - NCA + NCA / 2;
+  static_assert(NCA == 4 && kEarly <= NI / 2 - kAhead + 1, "one copy between the MFMAs of two fragments");
+  const auto early = [&](int j) { return j < NC - NCA ? NCA + j : 2 * (j - (NC - NCA)); };
+  // One step on buffer `cur`, whose first kAhead token and first-half channel
+  // fragments are in registers.  Behind its middle barrier the early rows'
+  // copies of step s + 2 go into `cur`, behind its end the others'.  In the
+  // last steps the copies and the reads of the next step are of data that
+  // nothing uses.
   const auto step = [&](int s, uint8_t* cur, uint8_t* nxt) {
+    const int sn = min(s + 2, S - 1);
 #pragma unroll
-    for (int i = 0; i < NI - kAhead; ++i) {
+    for (int i = 0; i < NI / 2; ++i) {
       x[(i + kAhead) % (kAhead + 1)] = read_x(cur, i + kAhead);
       if (i < FN) w[1][i] = read_w(cur, 1, i);
       mma(i);
     }
-    // keep this order: reads kAhead ahead, between the MFMAs
 #pragma unroll
-    for (int i = 0; i < NI - kAhead; ++i) {
+    for (int i = 0; i < NI / 2; ++i) {
       __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);  // LDS reads
       if (i < FN) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-      __builtin_amdgcn_sched_group_barrier(0x008, FN, 0);              // MFMAs
+      __builtin_amdgcn_sched_group_barrier(0x008, FN, 0);  // MFMAs
     }
     __builtin_amdgcn_sched_barrier(0);
-    wait_vmcnt<0>();
+    // the early rows' reads have returned in every wave: their MFMAs are issued
+    asm volatile("s_barrier" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int i = NI / 2; i < NI - kAhead; ++i) {
+      x[(i + kAhead) % (kAhead + 1)] = read_x(cur, i + kAhead);
+      mma(i);
+#pragma unroll
+      for (int j = 0; j < kEarly; ++j)
+        if (j * (NI / 2 - kAhead) / kEarly == i - NI / 2) copy(sn, cur, early(j));
+    }
+#pragma unroll
+    for (int i = NI / 2; i < NI - kAhead; ++i) {
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x008, FN / 2, 0);
+      __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);  // copies
+      if (i == NI / 2) __builtin_amdgcn_sched_group_barrier(0x010, kEarly - (NI / 2 - kAhead), 0);
+      __builtin_amdgcn_sched_group_barrier(0x008, FN / 2, 0);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    wait_vmcnt<kEarly>();
     lds_barrier();  // step s + 1 has landed; every wave has read step s
-    if (ragged && s + 2 == S) clear(nxt);
+    if (ragged && s + 2 == S) clear_behind<BM, 64 * W>(nxt, kStepBytes * (S - 1), p.K);
 #pragma unroll
     for (int f = 0; f < FN; ++f) w[0][f] = read_w(nxt, 0, f);
-    const int sn = min(s + 2, S - 1);
 #pragma unroll
     for (int i = NI - kAhead; i < NI; ++i) {
       mma(i);
       x[(i + kAhead) % (kAhead + 1)] = read_x(nxt, i + kAhead - NI);
-#pragma unroll
-      for (int u = 0; u < NC; ++u)
-        if (u % kAhead == i - (NI - kAhead)) copy(sn, cur, u);
+      if (i - (NI - kAhead) < NCA / 2) copy(sn, cur, 2 * (i - (NI - kAhead)) + 1);
     }
     __builtin_amdgcn_sched_group_barrier(0x100, FN, 0);
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
       __builtin_amdgcn_sched_group_barrier(0x008, FN / 2, 0);
-      __builtin_amdgcn_sched_group_barrier(0x010, NC / kAhead, 0);  // copies
-      if (i < NC % kAhead) __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);
+      if (i < NCA / 2) __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);
       __builtin_amdgcn_sched_group_barrier(0x008, FN / 2, 0);
       __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
     }
@@ -489,6 +524,136 @@ __attribute__((amdgpu_waves_per_eu(WM * WN / 4, WM * WN / 4))) void int8_tiled_k
   if (p.dtype == MOE_BF16) store_tile<Bf16, FM, FN>(p, acc, t0, nl);
   else if (p.dtype == MOE_F16) store_tile<F16, FM, FN>(p, acc, t0, nl);
   else store_tile<F32, FM, FN>(p, acc, t0, nl);
+}
+
+// The same product for tiles that fill the chip with less work each: a ring of
+// NS stages (NS - 1 of them in flight).  KG groups of WM x WN waves share a
+// tile: group kg takes the steps kg, kg + KG, ... (a stage holds one for each
+// group), so that a CU with one block still has two waves a SIMD to hide the
+// reads of one behind the MFMAs of the other; the groups' sums meet in LDS.
+template <int WM, int WN, int FM, int FN, int KG, int NS, int BLOCKS>
+__global__ __launch_bounds__(64 * WM * WN * KG)
+__attribute__((amdgpu_waves_per_eu(WM * WN * KG * BLOCKS / 4))) void int8_ring_kernel(Int8GemmParams p, int mtiles,
+                                                                                      int ntiles) {
+  constexpr int W = WM * WN, BM = 16 * FM * WM, BN = 16 * FN * WN;
+  constexpr int kPart = (BM + BN) * kStepBytes, kStage = KG * kPart;
+  constexpr int NC = (BM + BN) / 8 / W, NCA = BM / 8 / W;
+  static_assert((BM / 8) % W == 0 && (BN / 8) % W == 0 && W % FN == 0 && FN % 2 == 0, "whole copies of each operand");
+  static_assert((KG - 1) * BM * BN * 4 <= NS * kStage, "the groups' sums fit the ring");
+  extern __shared__ __align__(1024) uint8_t s_tile[];  // NS * kStage
+  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave % W;
+  const int kg = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / (kWave * W));
+  const int r = lane & 15, g = lane >> 4;
+  int m0, n0;
+  tile_origin<BM, BN>(mtiles, ntiles, m0, n0);
+
+  // copies and fragments as in the kernel above
+  const int K16 = (p.K + 15) / 16 * 16;
+  const int mrows = min(BM, p.M - m0), nrows = min(BN, p.N - n0);
+  const __amdgpu_buffer_rsrc_t rsa = code_rsrc(p.a + m0 * p.lda, (mrows - 1) * p.lda + K16);
+  const __amdgpu_buffer_rsrc_t rsb = code_rsrc(p.b + n0 * p.ldb, (nrows - 1) * p.ldb + K16);
+  const int slot = lane & 7, sub = lane >> 3;
+  int off[NC];
+#pragma unroll
+  for (int u = 0; u < NC; ++u) {
+    const int row = 8 * (wave + W * u) + sub;
+    off[u] = u < NCA ? min(row, mrows - 1) * static_cast<int>(p.lda) + 16 * (slot ^ (row & 7))
+                     : min(row - BM, nrows - 1) * static_cast<int>(p.ldb) + 16 * (slot ^ channel_key<FN>(row - BM));
+  }
+  const int S = (p.K + kStepBytes - 1) / kStepBytes;
+  const bool ragged = p.K % kStepBytes != 0;
+  const int past = kStepBytes * (S - 1) - (K16 - 16);
+  const int back_a = max(0, past + 16 * (slot ^ sub));
+  const int back_b = max(0, past + 16 * (slot ^ channel_key<FN>(8 * wave + sub)));
+  const auto copy = [&](int round, int at) {  // this group's step of a round into stage `at`
+    const int s = min(round * KG + kg, S - 1);
+    uint8_t* part = s_tile + at * kStage + kg * kPart;
+#pragma unroll
+    for (int u = 0; u < NC; ++u) {
+      const int o = off[u] - (s == S - 1 ? (u < NCA ? back_a : back_b) : 0);
+      auto* d = (__attribute__((address_space(3))) void*)(part + 1024 * (wave + W * u));
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(u < NCA ? rsa : rsb, d, 16, o, kStepBytes * s, 0, 0);
+    }
+  };
+  const int wm = wave / WN, wn = wave % WN;
+  const int crow = 16 * FN * wn + 4 * FN * (r >> 2) + (r & 3);
+  const int xbase = (16 * FM * wm + r) * kStepBytes + 16 * (g ^ (r & 7));
+  const int wbase = (BM + crow) * kStepBytes + 16 * (g ^ channel_key<FN>(crow));
+  i32x4 acc[FN][FM];
+#pragma unroll
+  for (int f = 0; f < FN; ++f)
+#pragma unroll
+    for (int m = 0; m < FM; ++m) acc[f][m] = i32x4{0, 0, 0, 0};
+
+  const int rounds = (S + KG - 1) / KG;
+#pragma unroll
+  for (int i = 0; i < NS - 1; ++i) copy(i, i);
+  int at = 0;  // stage of this round
+  for (int i = 0; i < rounds; ++i) {
+    wait_vmcnt<(NS - 2) * NC>();
+    lds_barrier();  // the round has landed; every wave has read the one before
+    if (ragged && i == rounds - 1)
+      clear_behind<BM, 64 * W * KG>(s_tile + at * kStage + (S - 1) % KG * kPart, kStepBytes * (S - 1), p.K);
+    copy(i + NS - 1, at == 0 ? NS - 1 : at - 1);
+    if (i * KG + kg < S) {
+      const uint8_t* cur = s_tile + at * kStage + kg * kPart;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        i32x4 x[FM], w[FN];
+#pragma unroll
+        for (int f = 0; f < FN; ++f)
+          w[f] = *reinterpret_cast<const i32x4*>(cur + (wbase ^ (64 * h)) + 4 * kStepBytes * f);
+#pragma unroll
+        for (int m = 0; m < FM; ++m)
+          x[m] = *reinterpret_cast<const i32x4*>(cur + (xbase ^ (64 * h)) + 16 * kStepBytes * m);
+#pragma unroll
+        for (int m = 0; m < FM; ++m)
+#pragma unroll
+          for (int f = 0; f < FN; ++f)
+            acc[f][m] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[f], x[m], acc[f][m], 0, 0, 0);
+      }
+    }
+    at = at == NS - 1 ? 0 : at + 1;
+  }
+  wait_vmcnt<0>();  // no copy may land in LDS after the block has ended, or in the sums
+  if constexpr (KG > 1) {
+    lds_barrier();
+    i32x4* sums = reinterpret_cast<i32x4*>(s_tile);  // [KG - 1][W][FN * FM][64]
+    if (kg > 0) {
+#pragma unroll
+      for (int f = 0; f < FN; ++f)
+#pragma unroll
+        for (int m = 0; m < FM; ++m) sums[(((kg - 1) * W + wave) * FN * FM + f * FM + m) * kWave + lane] = acc[f][m];
+    }
+    lds_barrier();
+    if (kg > 0) return;
+#pragma unroll
+    for (int k = 0; k < KG - 1; ++k)
+#pragma unroll
+      for (int f = 0; f < FN; ++f)
+#pragma unroll
+        for (int m = 0; m < FM; ++m) acc[f][m] += sums[((k * W + wave) * FN * FM + f * FM + m) * kWave + lane];
+  }
+  const int t0 = m0 + 16 * FM * wm + r, nl = n0 + 16 * FN * wn + 4 * FN * g;
+  if (p.dtype == MOE_BF16) store_tile<Bf16, FM, FN>(p, acc, t0, nl);
+  else if (p.dtype == MOE_F16) store_tile<F16, FM, FN>(p, acc, t0, nl);
+  else store_tile<F32, FM, FN>(p, acc, t0, nl);
+}
+
+template <int WM, int WN, int FM, int FN, int KG, int NS, int BLOCKS>
+static hipError_t launch_ring(const Int8GemmParams& p, hipStream_t s) {
+  constexpr int BM = 16 * FM * WM, BN = 16 * FN * WN;
+  constexpr int kLds = NS * KG * (BM + BN) * kStepBytes;
+  static_assert(kLds * BLOCKS <= 160 * 1024, "the blocks of a CU share its LDS");
+  const int64_t mt = (static_cast<int64_t>(p.M) + BM - 1) / BM, nt = (static_cast<int64_t>(p.N) + BN - 1) / BN;
+  if (mt * nt * 4 > INT32_MAX) return hipErrorInvalidConfiguration;
+  const auto kernel = int8_ring_kernel<WM, WN, FM, FN, KG, NS, BLOCKS>;
+  const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                                           hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
+  if (e != hipSuccess) return e;
+  kernel<<<static_cast<unsigned>(mt * nt), 64 * WM * WN * KG, kLds, s>>>(p, static_cast<int>(mt),
+                                                                         static_cast<int>(nt));
+  return hipGetLastError();
 }
 
 template <int WM, int WN, int FM, int FN>
