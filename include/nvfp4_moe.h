@@ -221,8 +221,8 @@ int int8_quantize_per_token(const void* x_dev, int32_t dtype, int64_t rows, int6
  * out[m, n] = scale_a[m] * scale_b[n] * sum_k a[m, k] * b[n, k] + bias[n]
  * The sum is exact (32-bit integers), scaled in binary32, rounded once.
  *   a_dev     i8 [M, lda] token rows;  b_dev  i8 [N, ldb] channel rows; 16-byte
- *             aligned, lda and ldb multiples of 16, >= K; whole 16-byte pieces
- *             are read, bytes behind K have no effect
+ *             aligned, lda and ldb multiples of 16, >= K, <= 2^26; whole 16-byte
+ *             pieces are read, bytes behind K have no effect
  *   scale_a_dev f32 [M], scale_b_dev f32 [N], bias_dev f32 [N] or NULL
  *   M, N, K   0 <= M, N < 2^31 (0: no-op);  1 <= K <= 131071 (the sum's range)
  *   out_dev   dtype [M, ldo], ldo >= N, aligned to its element; must not

@@ -4,6 +4,9 @@
 //   product:  out[m, n] = sa[m] sb[n] sum_k a[m, k] b[n, k] + bias[n]
 // The sum is exact in int32 for K < 2^31 / 128^2; it is converted to binary32
 // once, scaled there and rounded once to the output's type.
+#include <algorithm>
+#include <iterator>
+
 #include "common.hpp"
 #include "dtype.hpp"
 #include "kernels.hpp"
@@ -173,19 +176,14 @@ hipError_t launch_int8_quantize_rows(const void* x, int dtype, int64_t rows, int
 // assigned to lanes in any order that both operands share.
 // ---------------------------------------------------------------------------
 
-// out[m, n] for n .. n + 3 (those below N) of token m.
-__device__ __forceinline__ void store_scaled(const Int8GemmParams& p, int m, int n, const i32x4& acc) {
-  const float sa = p.sa[m];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (n + i >= p.N) break;
-    float f = static_cast<float>(acc[i]) * (sa * p.sb[n + i]);
-    if (p.bias) f += p.bias[n + i];
-    const int64_t at = static_cast<int64_t>(m) * p.ldo + n + i;
-    if (p.dtype == MOE_BF16) Bf16::put(p.out, at, f);
-    else if (p.dtype == MOE_F16) F16::put(p.out, at, f);
-    else F32::put(p.out, at, f);
-  }
+// out[m, n]
+__device__ __forceinline__ void store_one(const Int8GemmParams& p, int m, int n, int acc) {
+  float f = static_cast<float>(acc) * (p.sa[m] * p.sb[n]);
+  if (p.bias) f += p.bias[n];
+  const int64_t at = static_cast<int64_t>(m) * p.ldo + n;
+  if (p.dtype == MOE_BF16) Bf16::put(p.out, at, f);
+  else if (p.dtype == MOE_F16) F16::put(p.out, at, f);
+  else F32::put(p.out, at, f);
 }
 
 // 16 bytes of a row at column c, zero from column K on.  The row's last
@@ -200,62 +198,43 @@ __device__ __forceinline__ i32x4 load_k16(const int8_t* row, int c, int K) {
   return v;
 }
 
-// 16 channels by 16 MT tokens a block; its waves take K in steps of 128, every
-// W-th step each, and add their sums through LDS.
-template <int MT, int W>
-__global__ __launch_bounds__(64 * W) void int8_stream_kernel(Int8GemmParams p) {
-  __shared__ i32x4 s_acc[W > 1 ? W : 1][MT][kWave];
-  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
-  const int r = lane & 15, g = lane >> 4;
-  const int nt = (p.N + 15) / 16;
-  const int n0 = static_cast<int>(blockIdx.x % nt) * 16, m0 = static_cast<int>(blockIdx.x / nt) * (16 * MT);
-  const int8_t* brow = p.b + static_cast<int64_t>(min(n0 + r, p.N - 1)) * p.ldb;
-  const int8_t* arow[MT];
+// One token: a wave a channel, products of four bytes at a time in the vector
+// ALU.  A row's loads are whole kilobytes; kDotLoads of them are in flight
+// together.
+constexpr int kDotLoads = 8;
+
+__device__ __forceinline__ int wave_sum_i32(int v) {
+  v += static_cast<int>(dpp_u32<kDppXor1>(static_cast<uint32_t>(v)));
+  v += static_cast<int>(dpp_u32<kDppXor2>(static_cast<uint32_t>(v)));
+  v += static_cast<int>(dpp_u32<kDppHalfMirror>(static_cast<uint32_t>(v)));
+  v += static_cast<int>(dpp_u32<kDppMirror>(static_cast<uint32_t>(v)));
+  uint32_t a, b;
+  lane_pair<16>(static_cast<uint32_t>(v), a, b);
+  v = static_cast<int>(a) + static_cast<int>(b);
+  lane_pair<32>(static_cast<uint32_t>(v), a, b);
+  return static_cast<int>(a) + static_cast<int>(b);
+}
+
+__global__ __launch_bounds__(256) void int8_dot_kernel(Int8GemmParams p) {
+  const int lane = threadIdx.x & (kWave - 1);
+  const int n = static_cast<int>(blockIdx.x) * 4 + static_cast<int>(threadIdx.x) / kWave;
+  if (n >= p.N) return;  // whole waves
+  const int8_t* brow = p.b + static_cast<int64_t>(n) * p.ldb;
+  const int last = (p.K - 1) / 16 * 16;  // a row's last piece
+  int acc = 0;
+  for (int c0 = 16 * lane; c0 < p.K; c0 += 1024 * kDotLoads) {
+    i32x4 b[kDotLoads];
 #pragma unroll
-  for (int t = 0; t < MT; ++t) arow[t] = p.a + static_cast<int64_t>(min(m0 + 16 * t + r, p.M - 1)) * p.lda;
-  i32x4 acc[MT];
+    for (int i = 0; i < kDotLoads; ++i) b[i] = *reinterpret_cast<const i32x4*>(brow + min(c0 + 1024 * i, last));
 #pragma unroll
-  for (int t = 0; t < MT; ++t) acc[t] = i32x4{0, 0, 0, 0};
-  const int full = p.K / 128;
-  for (int s = wave; s < full; s += W) {
-    const int c = 128 * s + 32 * g;
-    const i32x4 b0 = *reinterpret_cast<const i32x4*>(brow + c), b1 = *reinterpret_cast<const i32x4*>(brow + c + 16);
+    for (int i = 0; i < kDotLoads; ++i) {
+      const i32x4 a = load_k16(p.a, c0 + 1024 * i, p.K);
 #pragma unroll
-    for (int t = 0; t < MT; ++t) {
-      const i32x4 a0 = *reinterpret_cast<const i32x4*>(arow[t] + c);
-      const i32x4 a1 = *reinterpret_cast<const i32x4*>(arow[t] + c + 16);
-      acc[t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(b0, a0, acc[t], 0, 0, 0);
-      acc[t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(b1, a1, acc[t], 0, 0, 0);
+      for (int j = 0; j < 4; ++j) acc = __builtin_amdgcn_sdot4(a[j], b[i][j], acc, false);
     }
   }
-  if (p.K % 128 != 0 && full % W == wave) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int c = 128 * full + 32 * g + 16 * h;
-      const i32x4 b = load_k16(brow, c, p.K);
-#pragma unroll
-      for (int t = 0; t < MT; ++t)
-        acc[t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(b, load_k16(arow[t], c, p.K), acc[t], 0, 0, 0);
-    }
-  }
-  if constexpr (W > 1) {
-#pragma unroll
-    for (int t = 0; t < MT; ++t) s_acc[wave][t][lane] = acc[t];
-    __syncthreads();
-    for (int t = wave; t < MT; t += W) {
-      i32x4 sum = s_acc[0][t][lane];
-#pragma unroll
-      for (int w = 1; w < W; ++w) sum += s_acc[w][t][lane];
-      const int m = m0 + 16 * t + r;
-      if (m < p.M) store_scaled(p, m, n0 + 4 * g, sum);
-    }
-  } else {
-#pragma unroll
-    for (int t = 0; t < MT; ++t) {
-      const int m = m0 + 16 * t + r;
-      if (m < p.M) store_scaled(p, m, n0 + 4 * g, acc[t]);
-    }
-  }
+  acc = wave_sum_i32(acc);
+  if (lane == 0) store_one(p, 0, n, acc);
 }
 
 // ---------------------------------------------------------------------------
@@ -277,6 +256,7 @@ __global__ __launch_bounds__(64 * W) void int8_stream_kernel(Int8GemmParams p) {
 // stores them as whole 16-byte pieces.
 // ---------------------------------------------------------------------------
 constexpr int kStepBytes = 128;
+constexpr int64_t kMaxTileLd = int64_t(1) << 22;  // 256 rows within 31-bit offsets
 constexpr int kAhead = 3;
 
 template <int FN>
@@ -337,18 +317,20 @@ __device__ __forceinline__ void store_tile(const Int8GemmParams& p, const i32x4 
     const int64_t row = static_cast<int64_t>(t) * p.ldo;
 #pragma unroll
     for (int f = 0; f < FN; f += 2) {
-      float v[8];
+      constexpr int kP = FN == 1 ? 4 : 8;  // channels of a store
+      float v[kP];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < kP; ++i) {
         v[i] = static_cast<float>(acc[f + i / 4][m][i % 4]) * (sa * sb[4 * f + i]);
         if (p.bias) v[i] += bias[4 * f + i];
       }
       const int n = n0 + 4 * f;
-      if (p.vec_out && n + 8 <= p.N) {
-        store8<T>(p.out, row + n, v);
+      if (p.vec_out && n + kP <= p.N) {
+        if constexpr (FN == 1) store4<T>(p.out, row + n, v);
+        else store8<T>(p.out, row + n, v);
       } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < kP; ++i)
           if (n + i < p.N) T::put(p.out, row + n + i, v[i]);
       }
     }
@@ -538,7 +520,7 @@ __attribute__((amdgpu_waves_per_eu(WM * WN * KG * BLOCKS / 4))) void int8_ring_k
   constexpr int W = WM * WN, BM = 16 * FM * WM, BN = 16 * FN * WN;
   constexpr int kPart = (BM + BN) * kStepBytes, kStage = KG * kPart;
   constexpr int NC = (BM + BN) / 8 / W, NCA = BM / 8 / W;
-  static_assert((BM / 8) % W == 0 && (BN / 8) % W == 0 && W % FN == 0 && FN % 2 == 0, "whole copies of each operand");
+  static_assert((BM / 8) % W == 0 && (BN / 8) % W == 0 && (FN == 1 || FN % 2 == 0), "whole copies of each operand");
   static_assert((KG - 1) * BM * BN * 4 <= NS * kStage, "the groups' sums fit the ring");
   extern __shared__ __align__(1024) uint8_t s_tile[];  // NS * kStage
   const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave % W;
@@ -553,24 +535,23 @@ __attribute__((amdgpu_waves_per_eu(WM * WN * KG * BLOCKS / 4))) void int8_ring_k
   const __amdgpu_buffer_rsrc_t rsa = code_rsrc(p.a + m0 * p.lda, (mrows - 1) * p.lda + K16);
   const __amdgpu_buffer_rsrc_t rsb = code_rsrc(p.b + n0 * p.ldb, (nrows - 1) * p.ldb + K16);
   const int slot = lane & 7, sub = lane >> 3;
-  int off[NC];
+  const int S = (p.K + kStepBytes - 1) / kStepBytes;
+  const bool ragged = p.K % kStepBytes != 0;
+  int off[NC], back[NC];  // back: what a piece behind K goes back in the last step
 #pragma unroll
   for (int u = 0; u < NC; ++u) {
     const int row = 8 * (wave + W * u) + sub;
-    off[u] = u < NCA ? min(row, mrows - 1) * static_cast<int>(p.lda) + 16 * (slot ^ (row & 7))
-                     : min(row - BM, nrows - 1) * static_cast<int>(p.ldb) + 16 * (slot ^ channel_key<FN>(row - BM));
+    const int col = 16 * (slot ^ (u < NCA ? row & 7 : channel_key<FN>(row - BM)));
+    off[u] = (u < NCA ? min(row, mrows - 1) * static_cast<int>(p.lda)
+                      : min(row - BM, nrows - 1) * static_cast<int>(p.ldb)) + col;
+    back[u] = max(0, kStepBytes * (S - 1) + col - (K16 - 16));
   }
-  const int S = (p.K + kStepBytes - 1) / kStepBytes;
-  const bool ragged = p.K % kStepBytes != 0;
-  const int past = kStepBytes * (S - 1) - (K16 - 16);
-  const int back_a = max(0, past + 16 * (slot ^ sub));
-  const int back_b = max(0, past + 16 * (slot ^ channel_key<FN>(8 * wave + sub)));
   const auto copy = [&](int round, int at) {  // this group's step of a round into stage `at`
     const int s = min(round * KG + kg, S - 1);
     uint8_t* part = s_tile + at * kStage + kg * kPart;
 #pragma unroll
     for (int u = 0; u < NC; ++u) {
-      const int o = off[u] - (s == S - 1 ? (u < NCA ? back_a : back_b) : 0);
+      const int o = off[u] - (s == S - 1 ? back[u] : 0);
       auto* d = (__attribute__((address_space(3))) void*)(part + 1024 * (wave + W * u));
       __builtin_amdgcn_raw_ptr_buffer_load_lds(u < NCA ? rsa : rsb, d, 16, o, kStepBytes * s, 0, 0);
     }
@@ -646,7 +627,7 @@ static hipError_t launch_ring(const Int8GemmParams& p, hipStream_t s) {
   constexpr int kLds = NS * KG * (BM + BN) * kStepBytes;
   static_assert(kLds * BLOCKS <= 160 * 1024, "the blocks of a CU share its LDS");
   const int64_t mt = (static_cast<int64_t>(p.M) + BM - 1) / BM, nt = (static_cast<int64_t>(p.N) + BN - 1) / BN;
-  if (mt * nt * 4 > INT32_MAX) return hipErrorInvalidConfiguration;
+  if (mt * nt > UINT32_MAX / (64 * WM * WN * KG)) return hipErrorInvalidConfiguration;
   const auto kernel = int8_ring_kernel<WM, WN, FM, FN, KG, NS, BLOCKS>;
   const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
                                            hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
@@ -661,7 +642,7 @@ static hipError_t launch_tiled(const Int8GemmParams& p, hipStream_t s) {
   constexpr int BM = 16 * FM * WM, BN = 16 * FN * WN;
   constexpr int kLds = 2 * (BM + BN) * kStepBytes;
   const int64_t mt = (static_cast<int64_t>(p.M) + BM - 1) / BM, nt = (static_cast<int64_t>(p.N) + BN - 1) / BN;
-  if (mt * nt * 8 > INT32_MAX) return hipErrorInvalidConfiguration;
+  if (mt * nt > UINT32_MAX / (64 * WM * WN)) return hipErrorInvalidConfiguration;
   const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(int8_tiled_kernel<WM, WN, FM, FN>),
                                            hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
   if (e != hipSuccess) return e;
@@ -670,14 +651,46 @@ static hipError_t launch_tiled(const Int8GemmParams& p, hipStream_t s) {
   return hipGetLastError();
 }
 
+// How long `tiles` take where `slots` run at once, in units of one round: the
+// mean of the whole rounds and of the share of work, since the chip's CUs
+// drift apart over several rounds.
+static double rounds(int64_t tiles, int64_t slots) {
+  const double t = static_cast<double>(tiles) / static_cast<double>(slots);
+  return 0.5 * (static_cast<double>((tiles + slots - 1) / slots) + (t > 1.0 ? t : 1.0));
+}
+
 hipError_t launch_int8_matmul(const Int8GemmParams& p, hipStream_t s) {
-  // (the tiled kernel addresses a tile's rows with 32-bit byte offsets)
-  if (p.M > 128 && p.lda < (1 << 22) && p.ldb < (1 << 22)) return launch_tiled<2, 4, 8, 4>(p, s);
-  const int64_t nt = (static_cast<int64_t>(p.N) + 15) / 16, mt = p.M <= 16 ? 1 : (static_cast<int64_t>(p.M) + 63) / 64;
-  if (nt * mt > INT32_MAX) return hipErrorInvalidConfiguration;
-  if (p.M <= 16) int8_stream_kernel<1, 4><<<static_cast<unsigned>(nt), 256, 0, s>>>(p);
-  else int8_stream_kernel<4, 4><<<static_cast<unsigned>(nt * mt), 256, 0, s>>>(p);
-  return hipGetLastError();
+  // One token and fewer channels than SIMDs: no tile to share (8000 x 1000:
+  // 4.0 us, 16 x 16 tiles 5.4; 7168 x 2048: 6.5 and 5.6).
+  if (p.M == 1 && p.N <= 1024) {
+    int8_dot_kernel<<<static_cast<unsigned>((p.N + 3) / 4), 256, 0, s>>>(p);
+    return hipGetLastError();
+  }
+  // Rows far apart: a tile's rows are addressed with 32-bit byte offsets, and
+  // these tiles have the fewest.
+  if (p.lda > kMaxTileLd || p.ldb > kMaxTileLd) return launch_ring<1, 1, 1, 2, 4, 3, 2>(p, s);
+  const auto tiles = [&](int bm, int bn) {
+    return ((static_cast<int64_t>(p.M) + bm - 1) / bm) * ((static_cast<int64_t>(p.N) + bn - 1) / bn);
+  };
+  // The measured time of a round of each tile, in microseconds for 128 bytes
+  // of K (where two blocks share a CU: with one, and with both): small tiles
+  // fill the chip when there are few, large ones move fewer bytes.
+  const auto paired = [&](int64_t t, double alone, double both) { return t <= 256 ? alone : both * rounds(t, 512); };
+  const double cost[] = {
+      0.06 * rounds(tiles(16, 16), 256),      paired(tiles(16, 32), 0.085, 0.155),
+      paired(tiles(32, 32), 0.14, 0.20),      0.18 * rounds(tiles(64, 32), 256),
+      0.25 * rounds(tiles(64, 64), 256),      0.62 * rounds(tiles(128, 128), 256),
+      1.09 * rounds(tiles(128, 128), 512),    1.8 * rounds(tiles(256, 256), 256)};
+  switch (std::min_element(std::begin(cost), std::end(cost)) - std::begin(cost)) {
+    case 0: return launch_ring<1, 1, 1, 1, 8, 4, 1>(p, s);
+    case 1: return launch_ring<1, 1, 1, 2, 4, 3, 2>(p, s);
+    case 2: return launch_ring<1, 1, 2, 2, 4, 2, 2>(p, s);
+    case 3: return launch_ring<2, 1, 2, 2, 4, 3, 1>(p, s);
+    case 4: return launch_ring<2, 2, 2, 2, 2, 4, 1>(p, s);
+    case 5: return launch_ring<2, 2, 4, 4, 2, 2, 1>(p, s);
+    case 6: return launch_ring<2, 4, 4, 2, 1, 2, 2>(p, s);
+    default: return launch_tiled<2, 4, 8, 4>(p, s);
+  }
 }
 
 }  // namespace nvfp4

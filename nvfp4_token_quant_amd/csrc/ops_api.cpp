@@ -246,6 +246,9 @@ int int8_matmul(const void* a_dev, int64_t lda, const float* scale_a_dev, const 
   if (lda < K || ldb < K || lda % 16 != 0 || ldb % 16 != 0)
     return api_fail(NVFP4_ERR_INVALID_ARG, "lda and ldb must be >= K and multiples of 16 (got %lld, %lld)",
                     (long long)lda, (long long)ldb);
+  if (lda > (int64_t(1) << 26) || ldb > (int64_t(1) << 26))
+    return api_fail(NVFP4_ERR_INVALID_ARG, "lda and ldb must be <= 2^26 (got %lld, %lld)", (long long)lda,
+                    (long long)ldb);
   if (ldo < N) return api_fail(NVFP4_ERR_INVALID_ARG, "ldo must be >= N (got %lld)", (long long)ldo);
   if (M == 0 || N == 0) return api_ok();
   if (!a_dev || !b_dev || !scale_a_dev || !scale_b_dev || !out_dev)

@@ -83,7 +83,10 @@ def _check_product(a, sa, b, sb, bias=None, dtype=BF16, **kw):
 SIZES = [(1, 1, 1), (1, 16, 64), (1, 300, 7168), (2, 17, 100), (3, 2048, 256), (5, 64, 131071), (16, 16, 128), (17, 33, 65),
          (31, 100, 1999), (40, 256, 2048), (64, 512, 1024), (65, 130, 513), (100, 1003, 777), (128, 128, 128),
          (129, 257, 300), (200, 512, 640), (255, 255, 255), (256, 256, 256), (257, 1030, 1111), (300, 768, 2048),
-         (513, 1024, 384), (777, 1003, 1999), (1024, 512, 1024), (1030, 2050, 128), (2100, 384, 272)]
+         (513, 1024, 384), (777, 1003, 1999), (1024, 512, 1024), (1030, 2050, 128), (2100, 384, 272),
+         # every tile shape of the kernel, one to a few steps of K, whole and partial
+         (90, 1100, 300), (150, 1900, 131), (300, 1001, 400), (500, 1033, 200), (1000, 3001, 129), (2050, 3000, 260),
+         (1111, 5999, 100), (2060, 6900, 100), (2060, 6901, 256), (2050, 6900, 300), (2100, 6904, 388)]
 
 
 @pytest.mark.parametrize("M,N,K", SIZES)

@@ -102,6 +102,7 @@ def test_int8_refusals():
     assert _quant(rows=0, x=0) == 0
     assert _matmul(dtype=-1) == 1 and _matmul(M=-1) == 1 and _matmul(N=2 ** 31) == 1 and _matmul(K=0) == 1
     assert _matmul(K=131072, lda=131072, ldb=131072) == 1 and _matmul(lda=72) == 1 and _matmul(ldb=48) == 1
+    assert _matmul(lda=(1 << 26) + 16) == 1 and _matmul(ldb=(1 << 26) + 16) == 1
     assert _matmul(ldo=7) == 1 and _matmul(a=0) == 1 and _matmul(sa=0) == 1 and _matmul(out=0) == 1
     assert _matmul(a=(1 << 20) + 8) == 1 and _matmul(b=(1 << 22) + 4) == 1 and _matmul(bias=2) == 1
     assert _matmul(out=(1 << 20) + 16) == 3 and _matmul(out=1 << 22) == 3 and _matmul(out=1 << 23) == 3
