@@ -232,6 +232,23 @@ int int8_matmul(const void* a_dev, int64_t lda, const float* scale_a_dev, const 
                 const float* scale_b_dev, const float* bias_dev, int64_t M, int64_t N, int64_t K, void* out_dev,
                 int32_t dtype, int64_t ldo, void* stream);
 
+/*
+ * int8_quantize_per_token of x (dtype [M, ld_x], K columns) and int8_matmul
+ * with the channel rows w, in one call.  The codes and scales are kept in
+ * caller-owned scratch memory: workspace_dev, 16-byte aligned, of at least
+ * int8_linear_workspace bytes, used by one call at a time (calls on one stream
+ * may share it, calls that overlap and graphs that replay together may not).
+ * The other arguments are those two calls'; workspace and out must not overlap
+ * any input or each other.
+ */
+int int8_linear(const void* x_dev, int32_t dtype, int64_t ld_x, const void* w_dev, int64_t ldw,
+                const float* scale_w_dev, const float* bias_dev, int64_t M, int64_t N, int64_t K,
+                void* workspace_dev, int64_t workspace_bytes, void* out_dev, int32_t out_dtype, int64_t ldo,
+                void* stream);
+
+/* Bytes of int8_linear's workspace for M tokens of K columns.  Host-only. */
+int int8_linear_workspace(int64_t M, int64_t K, int64_t* bytes);
+
 /* ---------------------------------------------------------------------- */
 /* MoE layer                                                               */
 /* ---------------------------------------------------------------------- */

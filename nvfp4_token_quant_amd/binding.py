@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import os
 import re
+import struct
 
 import torch
 
@@ -136,11 +137,15 @@ def lib():
         L.moe_workspace_set_router.restype = ctypes.c_int
         L.moe_workspace_set_router.argtypes = [_P, ctypes.POINTER(MoeRouter), _P, _P]
         L.moe_block_norm.restype = ctypes.c_int
-        L.moe_block_norm.argtypes = [ctypes.POINTER(MoeBlockNormArgs), _P]
+        L.moe_block_norm.argtypes = [_P, _P]  # moe_block_norm_args
         L.int8_quantize_per_token.restype = ctypes.c_int
         L.int8_quantize_per_token.argtypes = [_P, _I32, _I64, _I64, _I64, _P, _I64, _P, _P]
         L.int8_matmul.restype = ctypes.c_int
         L.int8_matmul.argtypes = [_P, _I64, _P, _P, _I64, _P, _P, _I64, _I64, _I64, _P, _I32, _I64, _P]
+        L.int8_linear.restype = ctypes.c_int
+        L.int8_linear.argtypes = [_P, _I32, _I64, _P, _I64, _P, _P, _I64, _I64, _I64, _P, _I64, _P, _I32, _I64, _P]
+        L.int8_linear_workspace.restype = ctypes.c_int
+        L.int8_linear_workspace.argtypes = [_I64, _I64, ctypes.POINTER(_I64)]
         _lib = L
     return _lib
 
@@ -248,26 +253,49 @@ def token_ceiling(max_prefill, piecewise_max, graph_max_bs, spec_draft_tokens) -
 #
 # Each works on its tensors' device, which need not be the current one, on
 # `stream` (default: that device's current stream).  Tensors a call makes
-# belong to the stream it ran on.
+# belong to the stream it ran on.  These calls serve single tokens, whose
+# kernels take a few microseconds: what surrounds the launch is kept short.
 
-def _matrix(t, name, dtypes):
+def _raw_stream(device):
+    """The handle of the device's current stream."""
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+def _elsewhere(device, stream):
+    """Whether a call has to switch to another device or stream."""
+    return stream is not None or device.index != torch.cuda.current_device()
+
+
+def _switched(device, stream):
+    """The context in which `stream` (or the device's current stream) is the current one."""
+    if stream is None:
+        return torch.cuda.device(device)
+    if stream.device != device:
+        raise ValueError(f"stream of {stream.device}, tensors on {device}")
+    return torch.cuda.stream(stream)
+
+
+def _matrix(t, name, dtypes=DTYPES):
+    """Checks a matrix of unit column stride; its shape and device."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype not in dtypes:
         raise ValueError(f"{name} must be one of {[str(d) for d in dtypes]}, got {t.dtype}")
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+    if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1):
         raise ValueError(f"{name} must be a matrix with unit column stride")
+    return t.shape, t.device
 
 
 def _vector(t, name, n, dtype, device):
     if not isinstance(t, torch.Tensor) or t.device != device:
         raise ValueError(f"{name} must be a tensor on {device}")
-    if t.dtype != dtype or tuple(t.shape) != (n,) or not t.is_contiguous():
+    if t.dtype is not dtype or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of {n} values, got {t.dtype} {tuple(t.shape)}")
+    return t.data_ptr()
 
 
 def _same(t, name, shape, device):
-    if t.device != device or tuple(t.shape) != tuple(shape):
+    if t.device != device or t.shape != torch.Size(shape):
         raise ValueError(f"{name} must be {tuple(shape)} on {device}, got {tuple(t.shape)} on {t.device}")
 
 
@@ -276,21 +304,13 @@ def _ld(t):
     return t.stride(0) if t.shape[0] > 1 else t.shape[1]
 
 
-def _ld16(t):
-    return t.stride(0) if t.shape[0] > 1 else (t.shape[1] + 15) // 16 * 16
-
-
-def _run(device, stream, call):
-    """call(handle of the stream) with `device` and `stream` current."""
-    if stream is not None:
-        if stream.device != device:
-            raise ValueError(f"stream of {stream.device}, tensors on {device}")
-        with torch.cuda.stream(stream):
-            return call(stream.cuda_stream)
-    if device.index == torch.cuda.current_device():
-        return call(torch.cuda.current_stream().cuda_stream)
-    with torch.cuda.device(device):
-        return call(torch.cuda.current_stream().cuda_stream)
+def _ld16(t, name):
+    """The same for 8-bit codes, whose rows start at multiples of 16 bytes."""
+    if t.shape[0] <= 1:
+        return (t.shape[1] + 15) // 16 * 16
+    if t.stride(0) % 16 != 0:
+        raise ValueError(f"{name}: rows must start at multiples of 16 bytes, as int8_quantize_per_token lays them out")
+    return t.stride(0)
 
 
 class Router:
@@ -308,26 +328,25 @@ class Router:
 def route(logits, top_k, router, bias=None, out=None, stream=None):
     """logits [T, E] (bf16, f16 or f32; the row stride may exceed E), bias f32
     [E] -> (ids int32 [T, k], weights f32 [T, k]), into `out` if given."""
-    _matrix(logits, "logits", DTYPES)
-    T, E = logits.shape
-    device = logits.device
-    if bias is not None:
-        _vector(bias, "bias", E, torch.float32, device)
-    if out is not None:
-        for t, name, dtype in ((out[0], "ids", torch.int32), (out[1], "weights", torch.float32)):
+    (T, E), device = _matrix(logits, "logits")
+    if _elsewhere(device, stream):
+        with _switched(device, stream):
+            return route(logits, top_k, router, bias, out)
+    b = _vector(bias, "bias", E, torch.float32, device) if bias is not None else None
+    if out is None:
+        shape = (T, max(top_k, 0))
+        ids, w = torch.empty(shape, dtype=torch.int32, device=device), torch.empty(shape, device=device,
+                                                                                   dtype=torch.float32)
+    else:
+        ids, w = out
+        for t, name, dtype in ((ids, "ids", torch.int32), (w, "weights", torch.float32)):
             _require(t, dtype, name)
             _same(t, name, (T, top_k), device)
             if not t.is_contiguous():
                 raise ValueError(f"{name} must be contiguous")
-
-    def call(s):
-        ids, w = out if out is not None else (
-            torch.empty((T, max(top_k, 0)), dtype=torch.int32, device=device),
-            torch.empty((T, max(top_k, 0)), dtype=torch.float32, device=device))
-        _check(lib().moe_route(router.desc, logits.data_ptr(), DTYPES[logits.dtype], T, E, _ld(logits), top_k,
-                               bias.data_ptr() if bias is not None else None, ids.data_ptr(), w.data_ptr(), s))
-        return ids, w
-    return _run(device, stream, call)
+    _check(lib().moe_route(router.desc, logits.data_ptr(), DTYPES[logits.dtype], T, E, _ld(logits), top_k, b,
+                           ids.data_ptr(), w.data_ptr(), _raw_stream(device)))
+    return ids, w
 
 
 class Norm:
@@ -338,14 +357,21 @@ class Norm:
         if kind not in NORM_KINDS:
             raise ValueError("kind must be 'rms' or 'layer'")
         self.weight, self.bias = weight, bias
-        self._head = (NORM_KINDS[kind], eps, offset)
+        self._desc = MoeNorm(NORM_KINDS[kind], eps, offset, None, None)
+        self._address = ctypes.addressof(self._desc)
 
     def desc(self, cols, dtype, device, name):
-        for t, part in ((self.weight, "weight"), (self.bias, "bias")):
-            if t is not None:
-                _vector(t, f"{name} {part}", cols, dtype, device)
-        return MoeNorm(*self._head, self.weight.data_ptr() if self.weight is not None else None,
-                       self.bias.data_ptr() if self.bias is not None else None)
+        """The address of this norm's moe_norm, of the weight and bias it has now."""
+        w, b, d = self.weight, self.bias, self._desc
+        d.weight = _vector(w, f"{name} weight", cols, dtype, device) if w is not None else None
+        d.bias = _vector(b, f"{name} bias", cols, dtype, device) if b is not None else None
+        return self._address
+
+
+# moe_block_norm_args as bytes (the layout of MoeBlockNormArgs, natively
+# aligned; quicker to fill)
+_BLOCK_NORM = struct.Struct("@qqiiPqPqPqqiffPPPqPq")
+assert _BLOCK_NORM.size == ctypes.sizeof(MoeBlockNormArgs)
 
 
 def block_norm(residual, y=None, before=None, after=None, gate=None, gate_sigmoid=False, res_scale=1.0,
@@ -358,54 +384,47 @@ def block_norm(residual, y=None, before=None, after=None, gate=None, gate_sigmoi
     is of its dtype); y [T, H] bf16, f16 or f32; gate None, [H] for each
     channel, [T, 1] for each token or [T, H].  residual_out / h_out: outputs
     to write, residual and y themselves allowed."""
-    _matrix(residual, "residual", DTYPES)
-    T, H = residual.shape
-    device = residual.device
+    (T, H), device = _matrix(residual, "residual")
+    if _elsewhere(device, stream):
+        with _switched(device, stream):
+            return block_norm(residual, y, before, after, gate, gate_sigmoid, res_scale, out_scale, residual_out,
+                              h_out)
+    yp = ld_y = gp = ld_gate = gate_cols = 0
     if y is not None:
-        _matrix(y, "y", DTYPES)
-        _same(y, "y", (T, H), device)
-        dtype = y.dtype
+        _matrix(y, "y")
+        _same(y, "y", residual.shape, device)
+        dtype, yp, ld_y = y.dtype, y.data_ptr(), _ld(y)
     else:
         dtype = h_out.dtype if h_out is not None else residual.dtype
-    ld_gate = gate_cols = 0
     if gate is not None:
-        if gate.device != device or gate.dtype != dtype:
+        if not isinstance(gate, torch.Tensor) or gate.device != device or gate.dtype != dtype:
             raise ValueError(f"gate must be {dtype} on {device}")
         if gate.dim() == 1:
-            _vector(gate, "gate", H, dtype, device)
-            gate_cols = H
+            gp, gate_cols = _vector(gate, "gate", H, dtype, device), H
         else:
-            _matrix(gate, "gate", DTYPES)
+            _matrix(gate, "gate")
             if gate.shape[0] != T or gate.shape[1] not in (1, H):
                 raise ValueError(f"gate must be [{H}], [{T}, 1] or [{T}, {H}], got {tuple(gate.shape)}")
-            gate_cols = gate.shape[1]
-            ld_gate = _ld(gate)
+            gp, gate_cols, ld_gate = gate.data_ptr(), gate.shape[1], _ld(gate)
     for t, name, want in ((residual_out, "residual_out", residual.dtype), (h_out, "h_out", dtype)):
         if t is not None:
             _matrix(t, name, (want,))
-            _same(t, name, (T, H), device)
+            _same(t, name, residual.shape, device)
     if h_out is not None and before is None:
         raise ValueError("h_out needs a norm (before)")
-    as_is = y is None and before is not None and res_scale == 1.0 and residual_out is None
-    na = after.desc(H, dtype, device, "after") if after is not None else None
-    nb = before.desc(H, dtype, device, "before") if before is not None else None
-
-    def call(s):
-        r = residual_out if residual_out is not None or as_is else (
-            torch.empty((T, H), dtype=residual.dtype, device=device))
-        h = h_out if h_out is not None else (
-            torch.empty((T, H), dtype=dtype, device=device) if before is not None else None)
-        a = MoeBlockNormArgs(
-            T, H, DTYPES[dtype], DTYPES[residual.dtype], residual.data_ptr(), _ld(residual),
-            y.data_ptr() if y is not None else None, _ld(y) if y is not None else 0,
-            gate.data_ptr() if gate is not None else None, ld_gate, gate_cols, 1 if gate_sigmoid else 0,
-            res_scale, out_scale, ctypes.pointer(na) if na is not None else None,
-            ctypes.pointer(nb) if nb is not None else None, r.data_ptr() if r is not None else None,
-            _ld(r) if r is not None else 0,
-            h.data_ptr() if h is not None else None, _ld(h) if h is not None else 0)
-        _check(lib().moe_block_norm(a, s))
-        return (residual if r is None else r), h
-    return _run(device, stream, call)
+    na = after.desc(H, dtype, device, "after") if after is not None else 0
+    nb = before.desc(H, dtype, device, "before") if before is not None else 0
+    r, h = residual_out, h_out
+    if r is None and (y is not None or before is None or res_scale != 1.0):
+        r = torch.empty((T, H), dtype=residual.dtype, device=device)
+    if h is None and before is not None:
+        h = torch.empty((T, H), dtype=dtype, device=device)
+    _check(lib().moe_block_norm(_BLOCK_NORM.pack(
+        T, H, DTYPES[dtype], DTYPES[residual.dtype], residual.data_ptr(), _ld(residual), yp, ld_y, gp, ld_gate,
+        gate_cols, 1 if gate_sigmoid else 0, res_scale, out_scale, na, nb,
+        r.data_ptr() if r is not None else 0, _ld(r) if r is not None else 0,
+        h.data_ptr() if h is not None else 0, _ld(h) if h is not None else 0), _raw_stream(device)))
+    return (residual if r is None else r), h
 
 
 def int8_quantize_per_token(x, stream=None):
@@ -413,64 +432,71 @@ def int8_quantize_per_token(x, stream=None):
     (codes int8 [rows, cols], scale f32 [rows]).  The codes' rows start at
     multiples of 16 bytes, as int8_matmul takes them.  Weights [channels, in]
     give one scale a channel."""
-    _matrix(x, "x", DTYPES)
-    rows, cols = x.shape
-    device = x.device
+    (rows, cols), device = _matrix(x, "x")
+    if _elsewhere(device, stream):
+        with _switched(device, stream):
+            return int8_quantize_per_token(x)
     ld = (cols + 15) // 16 * 16
-
-    def call(s):
-        codes = torch.empty((rows, ld), dtype=torch.int8, device=device)
-        scale = torch.empty((rows,), dtype=torch.float32, device=device)
-        _check(lib().int8_quantize_per_token(x.data_ptr(), DTYPES[x.dtype], rows, cols, _ld(x), codes.data_ptr(), ld,
-                                             scale.data_ptr(), s))
-        return (codes[:, :cols] if ld != cols else codes), scale
-    return _run(device, stream, call)
+    codes = torch.empty((rows, ld), dtype=torch.int8, device=device)
+    scale = torch.empty((rows,), dtype=torch.float32, device=device)
+    _check(lib().int8_quantize_per_token(x.data_ptr(), DTYPES[x.dtype], rows, cols, _ld(x), codes.data_ptr(), ld,
+                                         scale.data_ptr(), _raw_stream(device)))
+    return (codes[:, :cols] if ld != cols else codes), scale
 
 
-def _int8_rows(t, name):
-    _matrix(t, name, (torch.int8,))
-    if t.shape[0] > 1 and t.stride(0) % 16 != 0:
-        raise ValueError(f"{name}: rows must start at multiples of 16 bytes, as int8_quantize_per_token lays them out")
+_CODES = (torch.int8,)
+
+
+def _product_out(out, out_dtype, M, N, device):
+    if out is None:
+        if out_dtype not in DTYPES:
+            raise ValueError(f"out_dtype must be one of {[str(d) for d in DTYPES]}, got {out_dtype}")
+        return torch.empty((M, N), dtype=out_dtype, device=device)
+    _matrix(out, "out")
+    _same(out, "out", (M, N), device)
+    return out
 
 
 def int8_matmul(codes, scale, w_codes, w_scale, bias=None, out_dtype=torch.bfloat16, out=None, stream=None):
     """codes int8 [M, K] and scale f32 [M] of the tokens, w_codes int8 [N, K]
     and w_scale f32 [N] of the channels, bias f32 [N] ->
     scale[m] * w_scale[n] * sum_k codes[m, k] * w_codes[n, k] + bias[n], [M, N]."""
-    _int8_rows(codes, "codes")
-    _int8_rows(w_codes, "w_codes")
-    M, K = codes.shape
-    N = w_codes.shape[0]
-    device = codes.device
+    (M, K), device = _matrix(codes, "codes", _CODES)
+    if _elsewhere(device, stream):
+        with _switched(device, stream):
+            return int8_matmul(codes, scale, w_codes, w_scale, bias, out_dtype, out)
+    (N, _), _ = _matrix(w_codes, "w_codes", _CODES)
     _same(w_codes, "w_codes", (N, K), device)
-    _vector(scale, "scale", M, torch.float32, device)
-    _vector(w_scale, "w_scale", N, torch.float32, device)
-    if bias is not None:
-        _vector(bias, "bias", N, torch.float32, device)
-    if out is not None:
-        _matrix(out, "out", DTYPES)
-        _same(out, "out", (M, N), device)
-
-    def call(s):
-        o = out if out is not None else torch.empty((M, N), dtype=out_dtype, device=device)
-        if o.dtype not in DTYPES:
-            raise ValueError(f"out_dtype must be one of {[str(d) for d in DTYPES]}, got {o.dtype}")
-        _check(lib().int8_matmul(codes.data_ptr(), _ld16(codes), scale.data_ptr(), w_codes.data_ptr(), _ld16(w_codes),
-                                 w_scale.data_ptr(), bias.data_ptr() if bias is not None else None, M, N, K,
-                                 o.data_ptr(), DTYPES[o.dtype], _ld(o), s))
-        return o
-    return _run(device, stream, call)
+    sa, sb = _vector(scale, "scale", M, torch.float32, device), _vector(w_scale, "w_scale", N, torch.float32, device)
+    b = _vector(bias, "bias", N, torch.float32, device) if bias is not None else None
+    lda, ldb = _ld16(codes, "codes"), _ld16(w_codes, "w_codes")
+    out = _product_out(out, out_dtype, M, N, device)
+    _check(lib().int8_matmul(codes.data_ptr(), lda, sa, w_codes.data_ptr(), ldb, sb, b, M, N, K, out.data_ptr(),
+                             DTYPES[out.dtype], _ld(out), _raw_stream(device)))
+    return out
 
 
 def int8_linear(x, w_codes, w_scale, bias=None, out_dtype=None, out=None, stream=None):
-    """x [M, K] (bf16, f16 or f32) quantized per token, then int8_matmul with
-    the channel-quantized weights; the result is of x's dtype unless
-    out_dtype (or out) says otherwise."""
-    if stream is not None:
-        with torch.cuda.stream(stream):
+    """x [M, K] (bf16, f16 or f32) quantized per token, times the
+    channel-quantized weights, as int8_quantize_per_token and int8_matmul
+    would; the result is of x's dtype unless out_dtype (or out) says
+    otherwise."""
+    (M, K), device = _matrix(x, "x")
+    if _elsewhere(device, stream):
+        with _switched(device, stream):
             return int8_linear(x, w_codes, w_scale, bias, out_dtype, out)
-    codes, scale = int8_quantize_per_token(x)
-    return int8_matmul(codes, scale, w_codes, w_scale, bias, out_dtype or x.dtype, out)
+    (N, _), _ = _matrix(w_codes, "w_codes", _CODES)
+    _same(w_codes, "w_codes", (N, K), device)
+    sb = _vector(w_scale, "w_scale", N, torch.float32, device)
+    b = _vector(bias, "bias", N, torch.float32, device) if bias is not None else None
+    ldb = _ld16(w_codes, "w_codes")
+    out = _product_out(out, out_dtype or x.dtype, M, N, device)
+    work = M * ((K + 15) // 16 * 16 + 4)  # int8_linear_workspace
+    scratch = torch.empty((work,), dtype=torch.uint8, device=device)
+    _check(lib().int8_linear(x.data_ptr(), DTYPES[x.dtype], _ld(x), w_codes.data_ptr(), ldb, sb, b, M, N, K,
+                             scratch.data_ptr(), work, out.data_ptr(), DTYPES[out.dtype], _ld(out),
+                             _raw_stream(device)))
+    return out
 
 
 # --- synthetic weights (input generation) --------------------------------------

@@ -5,6 +5,7 @@
 // The sum is exact in int32 for K < 2^31 / 128^2; it is converted to binary32
 // once, scaled there and rounded once to the output's type.
 #include <algorithm>
+#include <atomic>
 #include <iterator>
 
 #include "common.hpp"
@@ -508,6 +509,20 @@ __attribute__((amdgpu_waves_per_eu(WM * WN / 4, WM * WN / 4))) void int8_tiled_k
   else store_tile<F32, FM, FN>(p, acc, t0, nl);
 }
 
+// Lets a kernel use `bytes` of dynamic LDS.  The attribute belongs to the
+// current device: set once per device (devices past the mask's 64 set it on
+// every call).
+static hipError_t allow_lds(const void* kernel, int bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  hipError_t e = hipGetDevice(&dev);
+  if (e != hipSuccess) return e;
+  const uint64_t bit = dev >= 0 && dev < 64 ? uint64_t{1} << dev : 0;
+  if (bit != 0 && (done.load(std::memory_order_relaxed) & bit) != 0) return hipSuccess;
+  e = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == hipSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
+
 // The same product for tiles that fill the chip with less work each: a ring of
 // NS stages (NS - 1 of them in flight).  KG groups of WM x WN waves share a
 // tile: group kg takes the steps kg, kg + KG, ... (a stage holds one for each
@@ -629,8 +644,8 @@ static hipError_t launch_ring(const Int8GemmParams& p, hipStream_t s) {
   const int64_t mt = (static_cast<int64_t>(p.M) + BM - 1) / BM, nt = (static_cast<int64_t>(p.N) + BN - 1) / BN;
   if (mt * nt > UINT32_MAX / (64 * WM * WN * KG)) return hipErrorInvalidConfiguration;
   const auto kernel = int8_ring_kernel<WM, WN, FM, FN, KG, NS, BLOCKS>;
-  const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
-                                           hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
+  static std::atomic<uint64_t> lds_set{0};
+  const hipError_t e = allow_lds(reinterpret_cast<const void*>(kernel), kLds, lds_set);
   if (e != hipSuccess) return e;
   kernel<<<static_cast<unsigned>(mt * nt), 64 * WM * WN * KG, kLds, s>>>(p, static_cast<int>(mt),
                                                                          static_cast<int>(nt));
@@ -643,8 +658,8 @@ static hipError_t launch_tiled(const Int8GemmParams& p, hipStream_t s) {
   constexpr int kLds = 2 * (BM + BN) * kStepBytes;
   const int64_t mt = (static_cast<int64_t>(p.M) + BM - 1) / BM, nt = (static_cast<int64_t>(p.N) + BN - 1) / BN;
   if (mt * nt > UINT32_MAX / (64 * WM * WN)) return hipErrorInvalidConfiguration;
-  const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(int8_tiled_kernel<WM, WN, FM, FN>),
-                                           hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
+  static std::atomic<uint64_t> lds_set{0};
+  const hipError_t e = allow_lds(reinterpret_cast<const void*>(int8_tiled_kernel<WM, WN, FM, FN>), kLds, lds_set);
   if (e != hipSuccess) return e;
   int8_tiled_kernel<WM, WN, FM, FN><<<static_cast<unsigned>(mt * nt), 64 * WM * WN, kLds, s>>>(
       p, static_cast<int>(mt), static_cast<int>(nt));

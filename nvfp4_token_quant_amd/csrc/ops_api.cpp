@@ -41,6 +41,99 @@ NormParams norm_params(const moe_norm* n) {
   return NormParams{n->kind, n->eps, n->offset, n->weight_dev, n->bias_dev};
 }
 
+// Argument checks of the two 8-bit entry points (status; 0 rows pass early)
+// and their launches.
+int check_quantize(const void* x_dev, int32_t dtype, int64_t rows, int64_t cols, int64_t ld_x, const void* codes_dev,
+                   int64_t ld_codes, const float* scale_dev) {
+  const int64_t bytes = dtype_bytes(dtype);
+  if (!bytes) return api_fail(NVFP4_ERR_INVALID_ARG, "unknown dtype %d", dtype);
+  if (rows < 0 || rows > INT32_MAX)
+    return api_fail(NVFP4_ERR_INVALID_ARG, "rows must be in [0, 2^31) (got %lld)", (long long)rows);
+  if (cols < 1 || cols > (int64_t(1) << 30))
+    return api_fail(NVFP4_ERR_INVALID_ARG, "cols must be in [1, 2^30] (got %lld)", (long long)cols);
+  if (ld_x < cols) return api_fail(NVFP4_ERR_INVALID_ARG, "ld_x must be >= cols (got %lld)", (long long)ld_x);
+  if (ld_codes < cols || ld_codes % 16 != 0)
+    return api_fail(NVFP4_ERR_INVALID_ARG, "ld_codes must be >= cols and a multiple of 16 (got %lld)",
+                    (long long)ld_codes);
+  if (rows == 0) return NVFP4_OK;
+  if (!x_dev || !codes_dev || !scale_dev) return api_fail(NVFP4_ERR_INVALID_ARG, "NULL pointer argument");
+  if (!aligned(x_dev, bytes) || !aligned(codes_dev, 16) || !aligned(scale_dev, 4))
+    return api_fail(NVFP4_ERR_INVALID_ARG, "codes must be 16-byte aligned, x and scale to their element");
+  const int64_t nx = span(rows, ld_x, cols, bytes), nc = span(rows, ld_codes, (cols + 15) / 16 * 16, 1);
+  if (overlap(codes_dev, nc, x_dev, nx) || overlap(scale_dev, rows * 4, x_dev, nx) ||
+      overlap(scale_dev, rows * 4, codes_dev, nc))
+    return api_fail(NVFP4_ERR_ALIAS, "codes and scale must not overlap x or each other");
+  return NVFP4_OK;
+}
+
+int run_quantize(const void* x_dev, int32_t dtype, int64_t rows, int64_t cols, int64_t ld_x, void* codes_dev,
+                 int64_t ld_codes, float* scale_dev, void* stream) {
+  hipError_t e = launch_int8_quantize_rows(x_dev, dtype, rows, cols, ld_x, static_cast<int8_t*>(codes_dev), ld_codes,
+                                           scale_dev, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "int8_quantize_per_token launch");
+  return api_ok();
+}
+
+int check_matmul(const void* a_dev, int64_t lda, const float* scale_a_dev, const void* b_dev, int64_t ldb,
+                 const float* scale_b_dev, const float* bias_dev, int64_t M, int64_t N, int64_t K, const void* out_dev,
+                 int32_t dtype, int64_t ldo) {
+  const int64_t bytes = dtype_bytes(dtype);
+  if (!bytes) return api_fail(NVFP4_ERR_INVALID_ARG, "unknown dtype %d", dtype);
+  // (the last tile's row and channel numbers also stay below 2^31)
+  if (M < 0 || N < 0 || M > INT32_MAX - 512 || N > INT32_MAX - 512)
+    return api_fail(NVFP4_ERR_INVALID_ARG, "M and N must be in [0, 2^31 - 512) (got %lld, %lld)", (long long)M,
+                    (long long)N);
+  if (K < 1 || K > 131071)
+    return api_fail(NVFP4_ERR_INVALID_ARG, "K must be in [1, 131071], the range of 32-bit sums (got %lld)",
+                    (long long)K);
+  if (lda < K || ldb < K || lda % 16 != 0 || ldb % 16 != 0)
+    return api_fail(NVFP4_ERR_INVALID_ARG, "lda and ldb must be >= K and multiples of 16 (got %lld, %lld)",
+                    (long long)lda, (long long)ldb);
+  if (lda > (int64_t(1) << 26) || ldb > (int64_t(1) << 26))
+    return api_fail(NVFP4_ERR_INVALID_ARG, "lda and ldb must be <= 2^26 (got %lld, %lld)", (long long)lda,
+                    (long long)ldb);
+  if (ldo < N) return api_fail(NVFP4_ERR_INVALID_ARG, "ldo must be >= N (got %lld)", (long long)ldo);
+  if (M == 0 || N == 0) return NVFP4_OK;
+  if (!a_dev || !b_dev || !scale_a_dev || !scale_b_dev || !out_dev)
+    return api_fail(NVFP4_ERR_INVALID_ARG, "NULL pointer argument");
+  if (!aligned(a_dev, 16) || !aligned(b_dev, 16) || !aligned(scale_a_dev, 4) || !aligned(scale_b_dev, 4) ||
+      !aligned(bias_dev, 4) || !aligned(out_dev, bytes))
+    return api_fail(NVFP4_ERR_INVALID_ARG, "codes must be 16-byte aligned, scales, bias and out to their element");
+  const int64_t K16 = (K + 15) / 16 * 16, no = span(M, ldo, N, bytes);
+  if (overlap(out_dev, no, a_dev, span(M, lda, K16, 1)) || overlap(out_dev, no, b_dev, span(N, ldb, K16, 1)) ||
+      overlap(out_dev, no, scale_a_dev, M * 4) || overlap(out_dev, no, scale_b_dev, N * 4) ||
+      (bias_dev && overlap(out_dev, no, bias_dev, N * 4)))
+    return api_fail(NVFP4_ERR_ALIAS, "out overlaps an input");
+  return NVFP4_OK;
+}
+
+int run_matmul(const void* a_dev, int64_t lda, const float* scale_a_dev, const void* b_dev, int64_t ldb,
+               const float* scale_b_dev, const float* bias_dev, int64_t M, int64_t N, int64_t K, void* out_dev,
+               int32_t dtype, int64_t ldo, void* stream) {
+  Int8GemmParams p{};
+  p.a = static_cast<const int8_t*>(a_dev);
+  p.b = static_cast<const int8_t*>(b_dev);
+  p.sa = scale_a_dev;
+  p.sb = scale_b_dev;
+  p.bias = bias_dev;
+  p.out = out_dev;
+  p.lda = lda;
+  p.ldb = ldb;
+  p.ldo = ldo;
+  p.M = static_cast<int>(M);
+  p.N = static_cast<int>(N);
+  p.K = static_cast<int>(K);
+  p.dtype = dtype;
+  p.vec_out = row_vectors(out_dev, ldo, dtype_bytes(dtype)) ? 1 : 0;
+  hipError_t e = launch_int8_matmul(p, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "int8_matmul launch");
+  return api_ok();
+}
+
+// int8_linear's workspace: the codes (rows of whole 16-byte pieces), then the
+// scales.
+int64_t linear_codes_bytes(int64_t M, int64_t K) { return M * ((K + 15) / 16 * 16); }
+
 }  // namespace
 
 int check_router(const moe_router* r, int64_t E, int64_t top_k) {
@@ -207,78 +300,61 @@ int moe_block_norm(const moe_block_norm_args* args, void* stream) {
 
 int int8_quantize_per_token(const void* x_dev, int32_t dtype, int64_t rows, int64_t cols, int64_t ld_x,
                             void* codes_dev, int64_t ld_codes, float* scale_dev, void* stream) {
-  const int64_t bytes = dtype_bytes(dtype);
-  if (!bytes) return api_fail(NVFP4_ERR_INVALID_ARG, "unknown dtype %d", dtype);
-  if (rows < 0 || rows > INT32_MAX)
-    return api_fail(NVFP4_ERR_INVALID_ARG, "rows must be in [0, 2^31) (got %lld)", (long long)rows);
-  if (cols < 1 || cols > (int64_t(1) << 30))
-    return api_fail(NVFP4_ERR_INVALID_ARG, "cols must be in [1, 2^30] (got %lld)", (long long)cols);
-  if (ld_x < cols) return api_fail(NVFP4_ERR_INVALID_ARG, "ld_x must be >= cols (got %lld)", (long long)ld_x);
-  if (ld_codes < cols || ld_codes % 16 != 0)
-    return api_fail(NVFP4_ERR_INVALID_ARG, "ld_codes must be >= cols and a multiple of 16 (got %lld)",
-                    (long long)ld_codes);
+  const int st = check_quantize(x_dev, dtype, rows, cols, ld_x, codes_dev, ld_codes, scale_dev);
+  if (st != NVFP4_OK) return st;
   if (rows == 0) return api_ok();
-  if (!x_dev || !codes_dev || !scale_dev) return api_fail(NVFP4_ERR_INVALID_ARG, "NULL pointer argument");
-  if (!aligned(x_dev, bytes) || !aligned(codes_dev, 16) || !aligned(scale_dev, 4))
-    return api_fail(NVFP4_ERR_INVALID_ARG, "codes must be 16-byte aligned, x and scale to their element");
-  const int64_t nx = span(rows, ld_x, cols, bytes), nc = span(rows, ld_codes, (cols + 15) / 16 * 16, 1);
-  if (overlap(codes_dev, nc, x_dev, nx) || overlap(scale_dev, rows * 4, x_dev, nx) ||
-      overlap(scale_dev, rows * 4, codes_dev, nc))
-    return api_fail(NVFP4_ERR_ALIAS, "codes and scale must not overlap x or each other");
-  hipError_t e = launch_int8_quantize_rows(x_dev, dtype, rows, cols, ld_x, static_cast<int8_t*>(codes_dev), ld_codes,
-                                           scale_dev, static_cast<hipStream_t>(stream));
-  if (e != hipSuccess) return hip_fail(e, "int8_quantize_per_token launch");
-  return api_ok();
+  return run_quantize(x_dev, dtype, rows, cols, ld_x, codes_dev, ld_codes, scale_dev, stream);
 }
 
 int int8_matmul(const void* a_dev, int64_t lda, const float* scale_a_dev, const void* b_dev, int64_t ldb,
                 const float* scale_b_dev, const float* bias_dev, int64_t M, int64_t N, int64_t K, void* out_dev,
                 int32_t dtype, int64_t ldo, void* stream) {
-  const int64_t bytes = dtype_bytes(dtype);
-  if (!bytes) return api_fail(NVFP4_ERR_INVALID_ARG, "unknown dtype %d", dtype);
-  // (the last tile's row and channel numbers also stay below 2^31)
-  if (M < 0 || N < 0 || M > INT32_MAX - 512 || N > INT32_MAX - 512)
-    return api_fail(NVFP4_ERR_INVALID_ARG, "M and N must be in [0, 2^31 - 512) (got %lld, %lld)", (long long)M,
-                    (long long)N);
-  if (K < 1 || K > 131071)
-    return api_fail(NVFP4_ERR_INVALID_ARG, "K must be in [1, 131071], the range of 32-bit sums (got %lld)",
-                    (long long)K);
-  if (lda < K || ldb < K || lda % 16 != 0 || ldb % 16 != 0)
-    return api_fail(NVFP4_ERR_INVALID_ARG, "lda and ldb must be >= K and multiples of 16 (got %lld, %lld)",
-                    (long long)lda, (long long)ldb);
-  if (lda > (int64_t(1) << 26) || ldb > (int64_t(1) << 26))
-    return api_fail(NVFP4_ERR_INVALID_ARG, "lda and ldb must be <= 2^26 (got %lld, %lld)", (long long)lda,
-                    (long long)ldb);
-  if (ldo < N) return api_fail(NVFP4_ERR_INVALID_ARG, "ldo must be >= N (got %lld)", (long long)ldo);
+  const int st =
+      check_matmul(a_dev, lda, scale_a_dev, b_dev, ldb, scale_b_dev, bias_dev, M, N, K, out_dev, dtype, ldo);
+  if (st != NVFP4_OK) return st;
   if (M == 0 || N == 0) return api_ok();
-  if (!a_dev || !b_dev || !scale_a_dev || !scale_b_dev || !out_dev)
-    return api_fail(NVFP4_ERR_INVALID_ARG, "NULL pointer argument");
-  if (!aligned(a_dev, 16) || !aligned(b_dev, 16) || !aligned(scale_a_dev, 4) || !aligned(scale_b_dev, 4) ||
-      !aligned(bias_dev, 4) || !aligned(out_dev, bytes))
-    return api_fail(NVFP4_ERR_INVALID_ARG, "codes must be 16-byte aligned, scales, bias and out to their element");
-  const int64_t K16 = (K + 15) / 16 * 16, no = span(M, ldo, N, bytes);
-  if (overlap(out_dev, no, a_dev, span(M, lda, K16, 1)) || overlap(out_dev, no, b_dev, span(N, ldb, K16, 1)) ||
-      overlap(out_dev, no, scale_a_dev, M * 4) || overlap(out_dev, no, scale_b_dev, N * 4) ||
-      (bias_dev && overlap(out_dev, no, bias_dev, N * 4)))
-    return api_fail(NVFP4_ERR_ALIAS, "out overlaps an input");
-  Int8GemmParams p{};
-  p.a = static_cast<const int8_t*>(a_dev);
-  p.b = static_cast<const int8_t*>(b_dev);
-  p.sa = scale_a_dev;
-  p.sb = scale_b_dev;
-  p.bias = bias_dev;
-  p.out = out_dev;
-  p.lda = lda;
-  p.ldb = ldb;
-  p.ldo = ldo;
-  p.M = static_cast<int>(M);
-  p.N = static_cast<int>(N);
-  p.K = static_cast<int>(K);
-  p.dtype = dtype;
-  p.vec_out = row_vectors(out_dev, ldo, bytes) ? 1 : 0;
-  hipError_t e = launch_int8_matmul(p, static_cast<hipStream_t>(stream));
-  if (e != hipSuccess) return hip_fail(e, "int8_matmul launch");
+  return run_matmul(a_dev, lda, scale_a_dev, b_dev, ldb, scale_b_dev, bias_dev, M, N, K, out_dev, dtype, ldo, stream);
+}
+
+int int8_linear_workspace(int64_t M, int64_t K, int64_t* bytes) {
+  if (!bytes) return api_fail(NVFP4_ERR_INVALID_ARG, "NULL output");
+  if (M < 0 || M > INT32_MAX || K < 1 || K > 131071)
+    return api_fail(NVFP4_ERR_INVALID_ARG, "M must be in [0, 2^31) and K in [1, 131071] (got %lld, %lld)",
+                    (long long)M, (long long)K);
+  *bytes = linear_codes_bytes(M, K) + M * 4;
   return api_ok();
+}
+
+int int8_linear(const void* x_dev, int32_t dtype, int64_t ld_x, const void* w_dev, int64_t ldw,
+                const float* scale_w_dev, const float* bias_dev, int64_t M, int64_t N, int64_t K,
+                void* workspace_dev, int64_t workspace_bytes, void* out_dev, int32_t out_dtype, int64_t ldo,
+                void* stream) {
+  const int64_t xb = dtype_bytes(dtype), ob = dtype_bytes(out_dtype);
+  if (!xb || !ob) return api_fail(NVFP4_ERR_INVALID_ARG, "unknown dtype %d or %d", dtype, out_dtype);
+  int64_t need = 0;
+  int st = int8_linear_workspace(M, K, &need);
+  if (st != NVFP4_OK) return st;
+  const int64_t ldc = (K + 15) / 16 * 16, codes_bytes = linear_codes_bytes(M, K);
+  if (M > 0 && (!workspace_dev || !aligned(workspace_dev, 16) || workspace_bytes < need))
+    return api_fail(NVFP4_ERR_INVALID_ARG, "workspace must be 16-byte aligned, of at least %lld bytes (got %lld)",
+                    (long long)need, (long long)workspace_bytes);
+  float* scales = reinterpret_cast<float*>(static_cast<char*>(workspace_dev) + codes_bytes);
+  // The product's checks first (nothing is enqueued on an error), with x in
+  // place of the codes where they are about x.
+  st = check_matmul(workspace_dev, ldc, scales, w_dev, ldw, scale_w_dev, bias_dev, M, N, K, out_dev, out_dtype, ldo);
+  if (st != NVFP4_OK) return st;
+  if (M == 0 || N == 0) return api_ok();
+  st = check_quantize(x_dev, dtype, M, K, ld_x, workspace_dev, ldc, scales);
+  if (st != NVFP4_OK) return st;
+  const int64_t no = span(M, ldo, N, ob);
+  if (overlap(out_dev, no, x_dev, span(M, ld_x, K, xb)) ||
+      overlap(workspace_dev, need, w_dev, span(N, ldw, ldc, 1)) || overlap(workspace_dev, need, scale_w_dev, N * 4) ||
+      (bias_dev && overlap(workspace_dev, need, bias_dev, N * 4)))
+    return api_fail(NVFP4_ERR_ALIAS, "out or workspace overlaps an input");
+  st = run_quantize(x_dev, dtype, M, K, ld_x, workspace_dev, ldc, scales, stream);
+  if (st != NVFP4_OK) return st;
+  return run_matmul(workspace_dev, ldc, scales, w_dev, ldw, scale_w_dev, bias_dev, M, N, K, out_dev, out_dtype, ldo,
+                    stream);
 }
 
 }  // extern "C"

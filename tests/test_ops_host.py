@@ -57,7 +57,7 @@ def _norm_args(**kw):
     a = binding.MoeBlockNormArgs(**c)
     a.after = ctypes.pointer(after) if after is not None else None
     a.before = ctypes.pointer(before) if before is not None else None
-    return binding.lib().moe_block_norm(a, None)
+    return binding.lib().moe_block_norm(ctypes.byref(a), None)
 
 
 def test_block_norm_refusals():
@@ -109,6 +109,33 @@ def test_int8_refusals():
     assert _matmul(bias=1 << 24) == 3
     assert _matmul(M=0) == 0 and _matmul(N=0) == 0
     assert b"" == binding.lib().nvfp4_last_error()
+
+
+def _linear(x=1 << 20, dtype=BF16, ldx=60, w=1 << 21, ldw=64, sw=1 << 22, bias=0, M=4, N=8, K=60, ws=1 << 23,
+            wsb=4 * 68, out=1 << 24, odt=BF16, ldo=8):
+    return binding.lib().int8_linear(P(x), dtype, ldx, P(w), ldw, P(sw), P(bias), M, N, K, P(ws), wsb, P(out), odt, ldo,
+                                     None)
+
+
+def test_int8_linear_refusals():
+    n = ctypes.c_int64()
+    assert binding.lib().int8_linear_workspace(4, 60, ctypes.byref(n)) == 0 and n.value == 4 * 68
+    assert binding.lib().int8_linear_workspace(4, 0, ctypes.byref(n)) == 1
+    assert binding.lib().int8_linear_workspace(-1, 60, ctypes.byref(n)) == 1
+    assert binding.lib().int8_linear_workspace(4, 60, None) == 1
+    assert _linear(dtype=3) == 1 and _linear(odt=3) == 1 and _linear(ldx=59) == 1 and _linear(K=0) == 1
+    assert _linear(ldw=60) == 1 and _linear(wsb=4 * 68 - 1) == 1 and _linear(ws=0) == 1 and _linear(ws=(1 << 23) + 8) == 1
+    assert _linear(x=0) == 1 and _linear(w=0) == 1 and _linear(sw=0) == 1 and _linear(out=0) == 1 and _linear(M=-1) == 1
+    for alias in (dict(out=1 << 20), dict(out=1 << 21), dict(out=1 << 22), dict(out=1 << 23), dict(ws=1 << 20),
+                  dict(ws=1 << 21), dict(ws=1 << 22), dict(bias=1 << 23), dict(bias=1 << 24)):
+        assert _linear(**alias) == 3, alias
+    assert _linear(M=0, x=0, ws=0, wsb=0, out=0) == 0 and _linear(N=0, w=0, sw=0, out=0) == 0
+
+
+def test_packed_layouts():
+    """The bytes that the binding fills equal the structures' fields."""
+    f = binding.MoeBlockNormArgs(1, 2, 3, 4, 5, 6, 7, 8, 9, 10, 11, 12, 0.5, 0.25, None, None, 13, 14, 15, 16)
+    assert bytes(f) == binding._BLOCK_NORM.pack(1, 2, 3, 4, 5, 6, 7, 8, 9, 10, 11, 12, 0.5, 0.25, 0, 0, 13, 14, 15, 16)
 
 
 def test_python_refusals():
