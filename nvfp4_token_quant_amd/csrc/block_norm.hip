@@ -18,6 +18,9 @@
 
 namespace nvfp4 {
 
+// Batches of at most this many rows give a row of 513 to 1024 columns two waves.
+constexpr int kFewNormRows = 2048;
+
 namespace {
 
 __device__ __forceinline__ float wave_sum(float v) {
@@ -33,7 +36,8 @@ __device__ __forceinline__ float wave_sum(float v) {
 }
 
 // Sum over the TPR threads of a row, the same in each of them.  buf: one LDS
-// slot a wave, not used by another reduction of the kernel.
+// slot a wave, not used by another reduction of the kernel.  Where a block
+// holds several rows of more than a wave, every thread of it calls this.
 template <int TPR>
 __device__ __forceinline__ float row_sum(float v, float* buf) {
   v = wave_sum(v);
@@ -41,105 +45,122 @@ __device__ __forceinline__ float row_sum(float v, float* buf) {
     const int wave = threadIdx.x / kWave;
     if ((threadIdx.x & (kWave - 1)) == 0) buf[wave] = v;
     __syncthreads();
+    const float* row = buf + threadIdx.x / TPR * (TPR / kWave);
     v = 0.0f;
 #pragma unroll
-    for (int w = 0; w < TPR / kWave; ++w) v += buf[w];
+    for (int w = 0; w < TPR / kWave; ++w) v += row[w];
   }
   return v;
 }
 
-// Eight consecutive values at column c of a row: VEC reads whole 16-byte
-// pieces (cols a multiple of 8, rows 16-byte aligned), else one by one; 0 past
-// the end, which every step below keeps 0.
-template <typename T, bool VEC>
-struct Piece {
-  Raw8<T> raw;
-  __device__ __forceinline__ void load(const void* row, int c, int cols) {
-    if (c < cols) load8<T>(raw, row, c);
-  }
-  __device__ __forceinline__ void get(float (&f)[8], int c, int cols) const {
-    to_f32<T>(raw, f);
-    if (c >= cols) {
+// A thread's part of a row of T: NC pieces of eight consecutive columns, piece
+// i at column 8 (lt + TPR i).  VEC: cols is a multiple of 8 and rows start at
+// multiples of 16 bytes; else pieces are read at any address, and the first
+// cols % 8 threads hold one column each of the rest.  Columns that a thread
+// does not have are 0, and every step below keeps them 0.
+template <bool VEC, int NC>
+using Own = float[8 * NC + (VEC ? 0 : 1)];
+
+template <typename T, bool VEC, int TPR, int NC>
+struct Part {
+  Raw8<T> piece[NC];
+  float rest;
+  __device__ __forceinline__ void load(const void* row, int lt, int cols) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] = 0.0f;
+    for (int i = 0; i < NC; ++i) {
+      const int c = 8 * (lt + TPR * i);
+      if (c + 8 <= cols) {
+        if constexpr (VEC) load8<T>(piece[i], row, c);
+        else load8_any<T>(piece[i], row, c);
+      }
+    }
+    if (!VEC && lt < cols % 8) rest = T::get(row, cols / 8 * 8 + lt);
+  }
+  __device__ __forceinline__ void get(Own<VEC, NC>& f, int lt, int cols) const {
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const bool own = 8 * (lt + TPR * i) + 8 <= cols;
+      float v[8];
+      to_f32<T>(piece[i], v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[8 * i + j] = own ? v[j] : 0.0f;
+    }
+    if constexpr (!VEC) f[8 * NC] = lt < cols % 8 ? rest : 0.0f;
+  }
+};
+
+template <typename T, bool VEC, int TPR, int NC>
+__device__ __forceinline__ void put_part(void* row, int lt, int cols, const Own<VEC, NC>& f) {
+#pragma unroll
+  for (int i = 0; i < NC; ++i) {
+    const int c = 8 * (lt + TPR * i);
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = f[8 * i + j];
+    if (c + 8 <= cols) {
+      if constexpr (VEC) store8<T>(row, c, v);
+      else store8_any<T>(row, c, v);
     }
   }
-};
-template <typename T>
-struct Piece<T, false> {
-  float v[8];
-  __device__ __forceinline__ void load(const void* row, int c, int cols) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = c + j < cols ? T::get(row, c + j) : 0.0f;
+  if constexpr (!VEC) {
+    if (lt < cols % 8) T::put(row, cols / 8 * 8 + lt, f[8 * NC]);
   }
-  __device__ __forceinline__ void get(float (&f)[8], int, int) const {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) f[j] = v[j];
-  }
-};
+}
 
 template <typename T>
 __device__ __forceinline__ const void* row_at(const void* p, int64_t elements) {
   return static_cast<const char*>(p) + elements * T::kBytes;
 }
 
-// N(v) in place on the row's pieces.  w, b: the loaded weight and bias.
+// Up to two pieces a thread, everything a row needs is loaded before its first
+// reduction; with more, the registers hold only the row, and the rest is
+// loaded where it is used (65536 columns, one row: 62 us with all loads first,
+// most of them spilled).
+template <int NC>
+constexpr bool kLoadFirst = NC <= 2;
+
+// N(v) in place.  w, b: the loaded weight and bias (kLoadFirst).
 template <typename T, bool VEC, int TPR, int NC>
-__device__ __forceinline__ void apply_norm(float (&v)[NC][8], const NormParams& n, const Piece<T, VEC> (&w)[NC],
-                                           const Piece<T, VEC> (&b)[NC], int lt, int cols, float* buf0,
-                                           float* buf1) {
+__device__ __forceinline__ void apply_norm(Own<VEC, NC>& v, const NormParams& n,
+                                           Part<T, VEC, TPR, NC>& w, Part<T, VEC, TPR, NC>& b, int lt, int cols,
+                                           float* buf0, float* buf1) {
+  constexpr int N = 8 * NC + (VEC ? 0 : 1);
   const float inv_n = 1.0f / static_cast<float>(cols);
   if (n.kind == MOE_NORM_LAYER) {
     float s = 0.0f;
 #pragma unroll
-    for (int i = 0; i < NC; ++i)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) s += v[i][j];
+    for (int j = 0; j < N; ++j) s += v[j];
     const float mean = row_sum<TPR>(s, buf0) * inv_n;
 #pragma unroll
-    for (int i = 0; i < NC; ++i)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int c = 8 * (lt + TPR * i) + (VEC ? 0 : j);
-        v[i][j] = c < cols ? v[i][j] - mean : 0.0f;
-      }
+    for (int j = 0; j < N; ++j) {
+      const bool own = j < 8 * NC ? 8 * (lt + TPR * (j / 8)) + 8 <= cols : lt < cols % 8;
+      v[j] = own ? v[j] - mean : 0.0f;
+    }
   }
   float q = 0.0f;
 #pragma unroll
-  for (int i = 0; i < NC; ++i)
-#pragma unroll
-    for (int j = 0; j < 8; ++j) q = __builtin_fmaf(v[i][j], v[i][j], q);
+  for (int j = 0; j < N; ++j) q = __builtin_fmaf(v[j], v[j], q);
   const float inv = 1.0f / sqrtf(row_sum<TPR>(q, buf1) * inv_n + n.eps);
+  if (n.weight) {
+    float f[N];
+    if constexpr (!kLoadFirst<NC>) w.load(n.weight, lt, cols);
+    w.get(f, lt, cols);
 #pragma unroll
-  for (int i = 0; i < NC; ++i) {
-    const int c = 8 * (lt + TPR * i);
-    float f[8];
-    if (n.weight) {
-      w[i].get(f, c, cols);
+    for (int j = 0; j < N; ++j) v[j] *= inv * (f[j] + n.offset);
+  } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] *= inv * (f[j] + n.offset);
-    } else {
+    for (int j = 0; j < N; ++j) v[j] *= inv;
+  }
+  if (n.bias) {
+    float f[N];
+    if constexpr (!kLoadFirst<NC>) b.load(n.bias, lt, cols);
+    b.get(f, lt, cols);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] *= inv;
-    }
-    if (n.bias) {
-      b[i].get(f, c, cols);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] += f[j];
-    }
+    for (int j = 0; j < N; ++j) v[j] += f[j];
   }
 }
 
-template <typename T, bool VEC>
-__device__ __forceinline__ void put_piece(void* row, int c, int cols, const float (&f)[8]) {
-  if constexpr (VEC) {
-    if (c < cols) store8<T>(row, c, f);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (c + j < cols) T::put(row, c + j, f[j]);
-  }
-}
+__device__ __forceinline__ float sigmoid32(float g) { return 1.0f / (1.0f + expf(-g)); }
 
 }  // namespace
 
@@ -147,90 +168,85 @@ __device__ __forceinline__ void put_piece(void* row, int c, int cols, const floa
 template <typename T, typename R, bool VEC, int TPR, int NC>
 __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void block_norm_kernel(BlockNormParams p) {
   constexpr int kThreads = TPR > 256 ? TPR : 256;
+  constexpr int N = 8 * NC + (VEC ? 0 : 1);
   __shared__ float s_red[4][kThreads / kWave];
   const int lt = threadIdx.x % TPR;
   const int cols = p.cols;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * (kThreads / TPR) + threadIdx.x / TPR;
-  if (row >= p.rows) return;  // whole waves, and no barrier where a block holds several rows
+  const int64_t row_own = static_cast<int64_t>(blockIdx.x) * (kThreads / TPR) + threadIdx.x / TPR;
+  const bool active = row_own < p.rows;
+  const int64_t row = active ? row_own : p.rows - 1;  // past the end: the last row again, not stored
 
-  Piece<R, VEC> pr[NC];
-  Piece<T, VEC> py[NC], pg[NC], wa[NC], ba[NC], wb[NC], bb[NC];
-  const void* rrow = row_at<R>(p.r, row * p.ld_r);
-  const void* yrow = row_at<T>(p.y, p.y ? row * p.ld_y : 0);
+  Part<R, VEC, TPR, NC> pr;
+  Part<T, VEC, TPR, NC> py, pg, wa, ba, wb, bb;
   const void* grow = row_at<T>(p.gate, p.gate ? row * p.ld_gate : 0);
   const bool wide_gate = p.gate && p.gate_cols != 1;
-#pragma unroll
-  for (int i = 0; i < NC; ++i) {
-    const int c = 8 * (lt + TPR * i);
-    pr[i].load(rrow, c, cols);
-    if (p.y) py[i].load(yrow, c, cols);
-  }
+  const void* rrow = row_at<R>(p.r, row * p.ld_r);
+  if (kLoadFirst<NC> || !p.y) pr.load(rrow, lt, cols);
+  if (p.y) py.load(row_at<T>(p.y, row * p.ld_y), lt, cols);
   float g1 = p.gate && !wide_gate ? T::get(grow, 0) : 1.0f;
-#pragma unroll
-  for (int i = 0; i < NC; ++i) {
-    const int c = 8 * (lt + TPR * i);
-    if (wide_gate) pg[i].load(grow, c, cols);
-    if (p.after.weight) wa[i].load(p.after.weight, c, cols);
-    if (p.after.bias) ba[i].load(p.after.bias, c, cols);
-    if (p.before.weight) wb[i].load(p.before.weight, c, cols);
-    if (p.before.bias) bb[i].load(p.before.bias, c, cols);
+  if constexpr (kLoadFirst<NC>) {
+    if (wide_gate) pg.load(grow, lt, cols);
+    if (p.after.weight) wa.load(p.after.weight, lt, cols);
+    if (p.after.bias) ba.load(p.after.bias, lt, cols);
+    if (p.before.weight) wb.load(p.before.weight, lt, cols);
+    if (p.before.bias) bb.load(p.before.bias, lt, cols);
   }
 
-  float v[NC][8];
+  float v[N], f[N];
   if (p.y) {
-#pragma unroll
-    for (int i = 0; i < NC; ++i) py[i].get(v[i], 8 * (lt + TPR * i), cols);
-    if (p.after.kind >= 0)
-      apply_norm<T, VEC, TPR, NC>(v, p.after, wa, ba, lt, cols, s_red[0], s_red[1]);
-    if (p.gate && p.gate_sigmoid && !wide_gate) g1 = 1.0f / (1.0f + expf(-g1));
+    py.get(v, lt, cols);
+    if (p.after.kind >= 0) apply_norm<T, VEC, TPR, NC>(v, p.after, wa, ba, lt, cols, s_red[0], s_red[1]);
+    if (p.gate && p.gate_sigmoid && !wide_gate) g1 = sigmoid32(g1);
     g1 *= p.out_scale;
+    if (wide_gate) {
+      if constexpr (!kLoadFirst<NC>) pg.load(grow, lt, cols);
+      pg.get(f, lt, cols);
 #pragma unroll
-    for (int i = 0; i < NC; ++i) {
-      float f[8];
-      pr[i].get(f, 8 * (lt + TPR * i), cols);
-      if (wide_gate) {
-        float g[8];
-        pg[i].get(g, 8 * (lt + TPR * i), cols);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[i][j] *= p.gate_sigmoid ? 1.0f / (1.0f + expf(-g[j])) : g[j];
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] = p.res_scale * f[j] + g1 * v[i][j];
+      for (int j = 0; j < N; ++j) v[j] *= p.gate_sigmoid ? sigmoid32(f[j]) : f[j];
     }
+    if constexpr (!kLoadFirst<NC>) pr.load(rrow, lt, cols);
+    pr.get(f, lt, cols);
+#pragma unroll
+    for (int j = 0; j < N; ++j) v[j] = p.res_scale * f[j] + g1 * v[j];
   } else {
+    pr.get(v, lt, cols);
 #pragma unroll
-    for (int i = 0; i < NC; ++i) {
-      pr[i].get(v[i], 8 * (lt + TPR * i), cols);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] *= p.res_scale;
-    }
+    for (int j = 0; j < N; ++j) v[j] *= p.res_scale;
   }
-  if (p.r_out) {
-    void* orow = static_cast<char*>(p.r_out) + row * p.ld_r_out * R::kBytes;
-#pragma unroll
-    for (int i = 0; i < NC; ++i) put_piece<R, VEC>(orow, 8 * (lt + TPR * i), cols, v[i]);
-  }
+  if (p.r_out && active)
+    put_part<R, VEC, TPR, NC>(static_cast<char*>(p.r_out) + row * p.ld_r_out * R::kBytes, lt, cols, v);
   if (p.h) {
     apply_norm<T, VEC, TPR, NC>(v, p.before, wb, bb, lt, cols, s_red[2], s_red[3]);
-    void* hrow = static_cast<char*>(p.h) + row * p.ld_h * T::kBytes;
-#pragma unroll
-    for (int i = 0; i < NC; ++i) put_piece<T, VEC>(hrow, 8 * (lt + TPR * i), cols, v[i]);
+    if (active) put_part<T, VEC, TPR, NC>(static_cast<char*>(p.h) + row * p.ld_h * T::kBytes, lt, cols, v);
   }
 }
 
+template <typename T, typename R, bool VEC, int TPR, int NC>
+static void launch_norm_shape(const BlockNormParams& p, hipStream_t s) {
+  constexpr int kThreads = TPR > 256 ? TPR : 256;
+  constexpr int kRows = kThreads / TPR;
+  block_norm_kernel<T, R, VEC, TPR, NC>
+      <<<static_cast<unsigned>((p.rows + kRows - 1) / kRows), kThreads, 0, s>>>(p);
+}
+
+// One piece a thread up to 8192 columns: the shortest chain for a single row
+// (7168 columns: 3.8 us with 1024 threads, 4.5 with 256 of four pieces) and as
+// fast with many (16384 rows: 252 and 257 us).  Narrow rows share a block; in
+// large batches a wave takes one of up to 1024 columns by itself, without a
+// barrier (4096 x 1000: 8.8 us, with two waves a row 9.5; 1027 x 1001: 6.3 and
+// 5.8).
 template <typename T, typename R, bool VEC>
 static void launch_norm_width(const BlockNormParams& p, hipStream_t s) {
-  const auto grid = [&](int rows_per_block) {
-    return static_cast<unsigned>((p.rows + rows_per_block - 1) / rows_per_block);
-  };
-  if (p.cols <= 512) block_norm_kernel<T, R, VEC, 64, 1><<<grid(4), 256, 0, s>>>(p);
-  else if (p.cols <= 1024) block_norm_kernel<T, R, VEC, 64, 2><<<grid(4), 256, 0, s>>>(p);
-  else if (p.cols <= 2048) block_norm_kernel<T, R, VEC, 256, 1><<<grid(1), 256, 0, s>>>(p);
-  else if (p.cols <= 4096) block_norm_kernel<T, R, VEC, 256, 2><<<grid(1), 256, 0, s>>>(p);
-  else if (p.cols <= 8192) block_norm_kernel<T, R, VEC, 256, 4><<<grid(1), 256, 0, s>>>(p);
-  else if (p.cols <= 16384) block_norm_kernel<T, R, VEC, 1024, 2><<<grid(1), 1024, 0, s>>>(p);
-  else if (p.cols <= 32768) block_norm_kernel<T, R, VEC, 1024, 4><<<grid(1), 1024, 0, s>>>(p);
-  else block_norm_kernel<T, R, VEC, 1024, 8><<<grid(1), 1024, 0, s>>>(p);
+  const int w = p.cols;
+  if (w <= 512) launch_norm_shape<T, R, VEC, 64, 1>(p, s);
+  else if (w <= 1024 && p.rows <= kFewNormRows) launch_norm_shape<T, R, VEC, 128, 1>(p, s);
+  else if (w <= 1024) launch_norm_shape<T, R, VEC, 64, 2>(p, s);
+  else if (w <= 2048) launch_norm_shape<T, R, VEC, 256, 1>(p, s);
+  else if (w <= 4096) launch_norm_shape<T, R, VEC, 512, 1>(p, s);
+  else if (w <= 8192) launch_norm_shape<T, R, VEC, 1024, 1>(p, s);
+  else if (w <= 16384) launch_norm_shape<T, R, VEC, 1024, 2>(p, s);
+  else if (w <= 32768) launch_norm_shape<T, R, VEC, 1024, 4>(p, s);
+  else launch_norm_shape<T, R, VEC, 1024, 8>(p, s);
 }
 
 template <typename T, typename R>

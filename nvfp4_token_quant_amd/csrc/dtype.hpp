@@ -58,6 +58,13 @@ __device__ __forceinline__ void load8(Raw8<T>& r, const void* p, int64_t i) {
   for (int j = 0; j < T::kBytes / 2; ++j) r.v[j] = s[j];
 }
 
+// The same where a row starts anywhere (its elements are aligned): global
+// memory is read in 16-byte pieces at any address.
+template <typename T>
+__device__ __forceinline__ void load8_any(Raw8<T>& r, const void* p, int64_t i) {
+  __builtin_memcpy(&r, static_cast<const char*>(p) + i * T::kBytes, sizeof(r));
+}
+
 template <typename T>
 __device__ __forceinline__ void to_f32(const Raw8<T>& r, float (&f)[8]) {
   if constexpr (T::kBytes == 4) {
@@ -70,19 +77,28 @@ __device__ __forceinline__ void to_f32(const Raw8<T>& r, float (&f)[8]) {
 }
 
 template <typename T>
-__device__ __forceinline__ void store8(void* p, int64_t i, const float (&f)[8]) {
-  u32x4* d = reinterpret_cast<u32x4*>(static_cast<char*>(p) + i * T::kBytes);
+__device__ __forceinline__ void from_f32(Raw8<T>& r, const float (&f)[8]) {
   if constexpr (T::kBytes == 4) {
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
-      d[j] = u32x4{__float_as_uint(f[4 * j]), __float_as_uint(f[4 * j + 1]), __float_as_uint(f[4 * j + 2]),
-                   __float_as_uint(f[4 * j + 3])};
+    for (int j = 0; j < 8; ++j) r.v[j / 4][j % 4] = __float_as_uint(f[j]);
   } else {
-    u32x4 v;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = T::bits(f[2 * j]) | (T::bits(f[2 * j + 1]) << 16);
-    d[0] = v;
+    for (int j = 0; j < 4; ++j) r.v[0][j] = T::bits(f[2 * j]) | (T::bits(f[2 * j + 1]) << 16);
   }
+}
+template <typename T>
+__device__ __forceinline__ void store8(void* p, int64_t i, const float (&f)[8]) {
+  Raw8<T> r;
+  from_f32<T>(r, f);
+  u32x4* d = reinterpret_cast<u32x4*>(static_cast<char*>(p) + i * T::kBytes);
+#pragma unroll
+  for (int j = 0; j < T::kBytes / 2; ++j) d[j] = r.v[j];
+}
+template <typename T>
+__device__ __forceinline__ void store8_any(void* p, int64_t i, const float (&f)[8]) {
+  Raw8<T> r;
+  from_f32<T>(r, f);
+  __builtin_memcpy(static_cast<char*>(p) + i * T::kBytes, &r, sizeof(r));
 }
 
 // Four elements at once (8-byte aligned; binary32: 16-byte).

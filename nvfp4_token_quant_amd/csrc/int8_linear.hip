@@ -34,23 +34,24 @@ __device__ __forceinline__ u32x2 pack_codes(const float (&f)[8], float inv) {
   return r;
 }
 
+// Eight columns of a row as binary32, 0 past the end.  VEC: cols a multiple of
+// 8, rows 16-byte aligned; else pieces at any address, and the row's last one
+// value by value.
 template <typename T, bool VEC>
 __device__ __forceinline__ void load_piece(float (&f)[8], const void* row, int64_t c, int64_t cols) {
+  Raw8<T> raw;
   if constexpr (VEC) {
-    Raw8<T> raw;
-    load8<T>(raw, row, min(c, cols - 8));
+    load8<T>(raw, row, min(c, cols - 8));  // unconditional, so that all pieces' loads are in flight together
+    to_f32<T>(raw, f);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = c < cols ? f[j] : 0.0f;
+  } else if (c + 8 <= cols) {
+    load8_any<T>(raw, row, c);
     to_f32<T>(raw, f);
   } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) f[j] = T::get(row, min(c + j, cols - 1));
+    for (int j = 0; j < 8; ++j) f[j] = c + j < cols ? T::get(row, c + j) : 0.0f;
   }
-}
-// columns past the end count as 0
-template <bool VEC>
-__device__ __forceinline__ void clear_tail(float (&f)[8], int64_t c, int64_t cols) {
-#pragma unroll
-  for (int j = 0; j < 8; ++j)
-    if ((VEC ? c : c + j) >= cols) f[j] = 0.0f;
 }
 
 __device__ __forceinline__ float amax8(const float (&f)[8]) {
@@ -81,10 +82,7 @@ __global__ __launch_bounds__(256) void int8_quantize_kernel(const void* __restri
   for (int i = 0; i < NC; ++i) load_piece<T, VEC>(f[i], xrow, 8 * (lt + TPR * i), cols);
   float am = 0.0f;
 #pragma unroll
-  for (int i = 0; i < NC; ++i) {
-    clear_tail<VEC>(f[i], 8 * (lt + TPR * i), cols);
-    am = fmaxf(am, amax8(f[i]));
-  }
+  for (int i = 0; i < NC; ++i) am = fmaxf(am, amax8(f[i]));
   am = wave_max(am);
   if constexpr (TPR > kWave) {
     if ((threadIdx.x & (kWave - 1)) == 0) s_am[threadIdx.x / kWave] = am;
@@ -115,7 +113,7 @@ __global__ __launch_bounds__(256) void int8_quantize_long_kernel(const void* __r
   for (int64_t c = 8 * static_cast<int64_t>(threadIdx.x); c < cols; c += 8 * 256) {
     float f[8];
     load_piece<T, VEC>(f, xrow, c, cols);
-    am = fmaxf(am, amax8(f));  // a column read twice changes no maximum
+    am = fmaxf(am, amax8(f));
   }
   am = wave_max(am);
   if ((threadIdx.x & (kWave - 1)) == 0) s_am[threadIdx.x / kWave] = am;
@@ -126,7 +124,6 @@ __global__ __launch_bounds__(256) void int8_quantize_long_kernel(const void* __r
   for (int64_t c = 8 * static_cast<int64_t>(threadIdx.x); c < cols16; c += 8 * 256) {
     float f[8];
     load_piece<T, VEC>(f, xrow, c, cols);
-    clear_tail<VEC>(f, c, cols);
     *reinterpret_cast<u32x2*>(codes + row * ld_codes + c) = pack_codes(f, inv);
   }
   if (threadIdx.x == 0) scales[row] = some ? am / 127.0f : 1.0f;
