@@ -120,8 +120,7 @@ typedef enum moe_score { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_scor
  * NaN (+inf counts as FLT_MAX); masked experts and those of dropped groups
  * come after all others, lower index first, with weight 0, so a token always
  * has k different experts; a token without any has k weights of 0.  The
- * weights are formed in binary64 and rounded once; where the k scores are so
- * small that they or their sum underflow there, the weights are 0.
+ * weights are formed in binary64 and rounded once.
  * num_groups: 1..64, a divisor of E; top_groups: 1..num_groups, with
  * top_groups * E / num_groups >= k.  num_groups = 1 has no groups (top_groups
  * and group_best are then 1).  scale: finite.

@@ -143,7 +143,7 @@ hipError_t launch_quantize_experts(const float* w, int64_t experts, int64_t rows
 
 // route.hip: the router with scores, bias and groups.
 constexpr int kMaxRouteGroups = 64;
-constexpr int kRouteWaveTokens = 1024;  // batches up to here take a whole wave a token
+constexpr int kRouteWaveTokens = 2048;  // batches of up to 256 experts that may take a whole wave a token
 struct RouteParams {
   const void* logits;  // [T, ld] of dtype (moe_dtype)
   const float* bias;   // [E] or NULL

@@ -11,12 +11,11 @@
 //
 // Precision.  The order of two experts is decided by v in binary64: a
 // prefill batch compares millions of neighbouring values, and in binary32
-// (2^-24 around 1) some of them change places.  A candidate's key is the
-// order-preserving pattern of the binary64 value with its lowest 10 bits
-// replaced by the expert (1023 - e), so values nearer than 2^-42 of their
-// size count as equal.  Without a bias v has the logits' order and the key is
-// made of the logit itself.  Group scores are binary64 sums.  The k weights of
-// a token are formed in binary64 and rounded once to binary32.
+// (2^-24 around 1) some of them change places.  Ten bits of a candidate hold
+// the expert, so values nearer than 2^-42 of their size count as equal.
+// Without a bias v has the logits' order and the candidate is made of the
+// logit itself.  Group scores are binary64 sums.  The k weights of a token are
+// formed in binary64 and rounded once to binary32.
 //
 // Work.  The bytes are T * E logits, read once; what bounds the kernel is
 // vector work: with a bias (or groups by two values) one binary64
@@ -40,24 +39,68 @@ __device__ __forceinline__ float load_logit(const void* p, int dtype, int64_t i)
   if (dtype == MOE_F32) return F32::get(p, i);
   return dtype == MOE_BF16 ? Bf16::get(p, i) : F16::get(p, i);
 }
+// Logits gl, gl + L, ... of a row (past the end: the last one again).
+template <typename T, int KPL, int L>
+__device__ __forceinline__ void load_row(float (&v)[KPL], const void* p, int64_t row, int gl, int E) {
+#pragma unroll
+  for (int i = 0; i < KPL; ++i) v[i] = T::get(p, row + min(gl + L * i, E - 1));
+}
 
 // NaN counts as masked, +inf as the largest finite value.
 __device__ __forceinline__ float clean(float v) { return v >= kNegInf ? fminf(v, kF32Max) : kNegInf; }
 
-__device__ __forceinline__ double sigmoid64(float v) { return 1.0 / (1.0 + exp(-static_cast<double>(v))); }
+// exp(x) in binary64 to 2^-47 of it: x = n ln 2 + r with |r| <= ln 2 / 2, e^r by
+// its series to r^11 (the rest is below r^12 / 12!).  0 far below -745; above
+// 709 the value there.
+__device__ __forceinline__ double exp64(double x) {
+  x = fmin(fmax(x, -1200.0), 709.0);
+  const double n = __builtin_rint(x * 1.4426950408889634);
+  const double r = __builtin_fma(n, -1.9082149292705877e-10, __builtin_fma(n, -0.693147180369123816490, x));
+  double p = 1.0 / 39916800.0;
+  p = __builtin_fma(p, r, 1.0 / 3628800.0);
+  p = __builtin_fma(p, r, 1.0 / 362880.0);
+  p = __builtin_fma(p, r, 1.0 / 40320.0);
+  p = __builtin_fma(p, r, 1.0 / 5040.0);
+  p = __builtin_fma(p, r, 1.0 / 720.0);
+  p = __builtin_fma(p, r, 1.0 / 120.0);
+  p = __builtin_fma(p, r, 1.0 / 24.0);
+  p = __builtin_fma(p, r, 1.0 / 6.0);
+  p = __builtin_fma(p, r, 0.5);
+  p = __builtin_fma(p, r, 1.0);
+  p = __builtin_fma(p, r, 1.0);
+  return __builtin_amdgcn_ldexp(p, static_cast<int>(n));
+}
+// 1 / d for d >= 1, finite: the hardware's reciprocal and two Newton steps.
+__device__ __forceinline__ double recip64(double d) {
+  double y = __builtin_amdgcn_rcp(d);
+  y = __builtin_fma(__builtin_fma(-d, y, 1.0), y, y);
+  return __builtin_fma(__builtin_fma(-d, y, 1.0), y, y);
+}
 
-// Key of a binary64 value: its order-preserving pattern, the expert in the
-// lowest 10 bits.  Finite values have a nonzero high word.
-__device__ __forceinline__ uint64_t value_key(double v, int e) {
-  uint64_t u = static_cast<uint64_t>(__double_as_longlong(v + 0.0));
-  u = (u >> 63) ? ~u : (u | 0x8000000000000000ull);
-  return (u & ~1023ull) | static_cast<uint64_t>(1023 - e);
+// A candidate as one binary64 number: the value with its lowest 10 bits
+// replaced so that of equal values the lower expert's number is the larger.
+// Its order is the numbers' own, so a comparator of the sort is one maximum
+// and one minimum.  Masked experts come behind every value (|value| <= 2
+// FLT_MAX), by index.
+constexpr double kMasked = -0x1p1000;
+__device__ __forceinline__ double candidate(double v, int e) {
+  const uint64_t u = static_cast<uint64_t>(__double_as_longlong(v + 0.0));
+  const uint32_t low = (u >> 63) ? static_cast<uint32_t>(e) : static_cast<uint32_t>(1023 - e);
+  return __longlong_as_double(static_cast<long long>((u & ~1023ull) | low));
+}
+__device__ __forceinline__ int candidate_expert(double c) {
+  const uint64_t u = static_cast<uint64_t>(__double_as_longlong(c));
+  const int low = static_cast<int>(u & 1023);
+  return (u >> 63) ? low : 1023 - low;
 }
 
 template <int CTRL>
 __device__ __forceinline__ double dpp_f64(double v) {
   const uint64_t u = static_cast<uint64_t>(__double_as_longlong(v));
-  const uint64_t lo = dpp_u32<CTRL>(static_cast<uint32_t>(u)), hi = dpp_u32<CTRL>(static_cast<uint32_t>(u >> 32));
+  // (every lane has a source under these controls: no value to keep)
+  const uint64_t lo = static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(u), CTRL, 0xF, 0xF, true));
+  const uint64_t hi =
+      static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(u >> 32), CTRL, 0xF, 0xF, true));
   return __longlong_as_double(static_cast<long long>((hi << 32) | lo));
 }
 __device__ __forceinline__ double row16_sum64(double v) {
@@ -89,6 +132,65 @@ __device__ __forceinline__ float token_max(float v) {
   else return row16_max(v);
 }
 
+template <bool WAVE>
+__device__ __forceinline__ double token_max64(double v) {
+  v = fmax(v, dpp_f64<kDppXor1>(v));
+  v = fmax(v, dpp_f64<kDppXor2>(v));
+  v = fmax(v, dpp_f64<kDppRor4>(v));
+  v = fmax(v, dpp_f64<kDppRor8>(v));
+  if constexpr (WAVE) {
+    v = fmax(v, __shfl_xor(v, 16, kWave));
+    v = fmax(v, __shfl_xor(v, 32, kWave));
+  }
+  return v;
+}
+
+// Batcher's odd-even merge sort (see route.hpp), largest first.  Its passes and
+// the selection's rounds are template steps: a loop that the compiler leaves
+// rolled indexes the list by chains of selects.
+template <int N, int P, int D>
+__device__ __forceinline__ void sort_pass(double (&c)[N]) {
+#pragma unroll
+  for (int a = D % P; a + D < N; ++a) {
+    if ((a - D % P) / D % 2 == 0 && a / (2 * P) == (a + D) / (2 * P)) {
+      const double hi = fmax(c[a], c[a + D]), lo = fmin(c[a], c[a + D]);
+      c[a] = hi;
+      c[a + D] = lo;
+    }
+  }
+  if constexpr (D > 1) sort_pass<N, P, D / 2>(c);
+  else if constexpr (2 * P < N) sort_pass<N, 2 * P, 2 * P>(c);
+}
+template <int N>
+__device__ __forceinline__ void sort_desc64(double (&c)[N]) {
+  if constexpr (N > 1) sort_pass<N, 1, 1>(c);
+}
+
+// The k selection rounds over the lanes' sorted lists, as select_rounds in
+// route.hpp: lane j keeps round j's candidate.
+template <int N, int KMAX, bool WAVE, int J>
+__device__ __forceinline__ void select_round(double (&c)[N], int k, int gl, double& mine) {
+  if (J < k) {
+    const double best = token_max64<WAVE>(c[0]);
+    mine = gl == J ? best : mine;
+    const bool pop = c[0] == best;
+    constexpr int kShift = N < KMAX - 1 - J ? N : KMAX - 1 - J;  // entries that can still become a head
+#pragma unroll
+    for (int i = 0; i < kShift; ++i) c[i] = pop ? (i + 1 < N ? c[i + 1] : 2.0 * kMasked) : c[i];
+    if constexpr (J + 1 < KMAX) select_round<N, KMAX, WAVE, J + 1>(c, k, gl, mine);
+  }
+}
+template <int N, int KMAX, bool WAVE>
+__device__ __forceinline__ double select64(double (&c)[N], int k, int gl) {
+  double mine = kMasked;
+  select_round<N, KMAX, WAVE, 0>(c, k, gl, mine);
+  return mine;
+}
+
+// Orders a wave's own LDS writes before its reads (a token's lanes are in one
+// wave; LDS works in order).
+__device__ __forceinline__ void wave_lds_fence() { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront"); }
+
 // (best, second) of two such pairs
 __device__ __forceinline__ void merge_best(double& a1, double& a2, double b1, double b2) {
   const double lo = fmin(a1, b1);
@@ -99,149 +201,172 @@ __device__ __forceinline__ void merge_best(double& a1, double& a2, double b1, do
 }  // namespace
 
 // Lanes of one token: 16 (four tokens a wave) or the wave; lane gl holds
-// experts gl, gl + L, ... (KPL of them).
-template <int KPL, bool WAVE>
+// experts gl, gl + L, ... (KPL of them).  BIAS: ranked by value, else by logit.
+// A masked expert's value is -inf from the point where it is known to be.
+template <int KPL, bool WAVE, bool BIAS>
 __global__ __launch_bounds__(256) void moe_route_scores_kernel(RouteParams q) {
   constexpr int L = WAVE ? kWave : 16;
   constexpr int kTok = 256 / L;
-  extern __shared__ double s_route[];  // [kTok][E] values and [kTok][kMaxRouteGroups] group scores (G > 1)
+  constexpr double kNegInf64 = -__builtin_inf();
+  extern __shared__ double s_route[];  // [kTok][E + G] values and [kTok][kMaxRouteGroups] group scores (G > 1)
   const int lane = threadIdx.x & (kWave - 1), gl = lane & (L - 1), lt = threadIdx.x / L;
   const int E = q.E, k = q.k, G = q.groups;
   const int64_t t_own = static_cast<int64_t>(blockIdx.x) * kTok + lt;
   const int64_t t = min(t_own, static_cast<int64_t>(q.T) - 1);  // past the end: the last token again, not stored
   const bool softmax = q.score == MOE_SCORE_SOFTMAX;
-  const bool has_bias = q.bias != nullptr;
 
   float v[KPL];
+  if (q.dtype == MOE_F32) load_row<F32, KPL, L>(v, q.logits, t * q.ld, gl, E);
+  else if (q.dtype == MOE_BF16) load_row<Bf16, KPL, L>(v, q.logits, t * q.ld, gl, E);
+  else load_row<F16, KPL, L>(v, q.logits, t * q.ld, gl, E);
+  float b[BIAS ? KPL : 1];
+  if constexpr (BIAS) {
 #pragma unroll
-  for (int i = 0; i < KPL; ++i) v[i] = load_logit(q.logits, q.dtype, t * q.ld + min(gl + L * i, E - 1));
-  uint32_t open = 0;  // bit i: expert gl + L i may be chosen
-#pragma unroll
-  for (int i = 0; i < KPL; ++i) {
-    v[i] = gl + L * i < E ? clean(v[i]) : kNegInf;
-    open |= (v[i] > kNegInf ? 1u : 0u) << i;
+    for (int i = 0; i < KPL; ++i) b[i] = q.bias[min(gl + L * i, E - 1)];
   }
-  float m = v[0];
 #pragma unroll
-  for (int i = 1; i < KPL; ++i) m = fmaxf(m, v[i]);
-  m = token_max<WAVE>(m);
-  if (!(m > kNegInf)) m = 0.0f;  // no expert at all: every exponential below is 0
+  for (int i = 0; i < KPL; ++i) v[i] = gl + L * i < E ? clean(v[i]) : kNegInf;
+  float m = 0.0f;  // the largest logit; 0 without any, where every exponential is 0
+  if (softmax) {
+    m = v[0];
+#pragma unroll
+    for (int i = 1; i < KPL; ++i) m = fmaxf(m, v[i]);
+    m = token_max<WAVE>(m);
+    m = m > kNegInf ? m : 0.0f;
+  }
 
-  // values in binary64 where the order or the groups need them
-  const bool values = has_bias || (G > 1 && q.group_best == 2);
+  // What the experts (BIAS) and groups are ranked by: values in binary64, or
+  // (groups by their largest value without a bias) the logits themselves.
   double val[KPL];
   double z = 0.0;  // the softmax sum, where it is needed
-  if (values) {
+  const bool sums = softmax && (BIAS || !q.renormalize);
+  if (BIAS || (G > 1 && q.group_best == 2)) {
+    if (softmax) {
 #pragma unroll
-    for (int i = 0; i < KPL; ++i)
-      val[i] = softmax ? exp(static_cast<double>(v[i]) - static_cast<double>(m)) : sigmoid64(v[i]);
-    if (softmax && (has_bias || !q.renormalize)) {
+      for (int i = 0; i < KPL; ++i) val[i] = exp64(static_cast<double>(v[i]) - static_cast<double>(m));
+      if (sums) {
 #pragma unroll
-      for (int i = 0; i < KPL; ++i) z += val[i];
-      z = token_sum64<WAVE>(z);
+        for (int i = 0; i < KPL; ++i) z += val[i];
+        z = token_sum64<WAVE>(z);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < KPL; ++i) val[i] = recip64(1.0 + exp64(-static_cast<double>(v[i])));
     }
-    if (has_bias) {
-      const double rz = softmax && z > 0.0 ? 1.0 / z : 1.0;
+    if constexpr (BIAS) {
+      const double rz = softmax ? recip64(fmax(z, 1.0)) : 1.0;  // (z >= 1 where there is any expert)
 #pragma unroll
       for (int i = 0; i < KPL; ++i) {
-        const float b = clean(q.bias[min(gl + L * i, E - 1)]);
-        if (!(b > kNegInf)) open &= ~(1u << i);
-        val[i] = val[i] * rz + static_cast<double>(b);
+        const float bi = clean(b[i]);
+        if (!(bi > kNegInf)) v[i] = kNegInf;
+        val[i] = __builtin_fma(val[i], rz, static_cast<double>(bi));
       }
     }
+#pragma unroll
+    for (int i = 0; i < KPL; ++i) val[i] = v[i] > kNegInf ? val[i] : kNegInf64;
   } else {
-    if (softmax && !q.renormalize) {
+    if (sums) {
       // (binary32 exponentials: they only scale the weights and order nothing)
 #pragma unroll
       for (int i = 0; i < KPL; ++i) z += static_cast<double>(expf(v[i] - m));
       z = token_sum64<WAVE>(z);
     }
 #pragma unroll
-    for (int i = 0; i < KPL; ++i) val[i] = static_cast<double>(v[i]);  // groups by the largest logit
+    for (int i = 0; i < KPL; ++i) val[i] = static_cast<double>(v[i]);
   }
 
   if (G > 1) {
+    // one double between groups, so that they start on different banks
     const int gs = E / G;
-    double* sv = s_route + static_cast<int64_t>(lt) * E;
-    double* sg = s_route + static_cast<int64_t>(kTok) * E + lt * kMaxRouteGroups;
+    const auto group_of = [&](int e) { return static_cast<int>((static_cast<uint32_t>(e) * q.group_magic) >> 20); };
+    double* sv = s_route + static_cast<int64_t>(lt) * (E + G);
+    double* sg = s_route + static_cast<int64_t>(kTok) * (E + G) + lt * kMaxRouteGroups;
 #pragma unroll
-    for (int i = 0; i < KPL; ++i)
-      if (gl + L * i < E) sv[gl + L * i] = (open >> i) & 1 ? val[i] : static_cast<double>(kNegInf);
-    __syncthreads();
+    for (int i = 0; i < KPL; ++i) {
+      const int e = gl + L * i;
+      if (e < E) sv[e + group_of(e)] = val[i];
+    }
+    wave_lds_fence();
     // P lanes a group (a power of two), L / P groups at a time
     int P = L;
     while (P > 1 && P * G > L) P >>= 1;
     const int sub = gl & (P - 1), per = L / P;
     for (int g0 = 0; g0 < G; g0 += per) {
       const int g = g0 + gl / P;
-      double b1 = static_cast<double>(kNegInf), b2 = b1;
-      if (g < G)
-        for (int j = sub; j < gs; j += P) merge_best(b1, b2, sv[g * gs + j], static_cast<double>(kNegInf));
+      double b1 = kNegInf64, b2 = kNegInf64;
+      if (g < G) {
+        const double* own = sv + g * (gs + 1);
+        for (int j = sub; j < gs; j += 4 * P) {  // four reads in flight; past the end: not counted
+          double x[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) x[u] = own[min(j + u * P, gs - 1)];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) merge_best(b1, b2, j + u * P < gs ? x[u] : kNegInf64, kNegInf64);
+        }
+      }
       for (int d = 1; d < P; d <<= 1) {
         const double o1 = __shfl_xor(b1, d, kWave), o2 = __shfl_xor(b2, d, kWave);
         merge_best(b1, b2, o1, o2);
       }
-      if (g < G && sub == 0)
-        sg[g] = q.group_best == 2 && b2 > static_cast<double>(kNegInf) ? b1 + b2 : b1;
+      if (g < G && sub == 0) sg[g] = q.group_best == 2 && b2 > kNegInf64 ? b1 + b2 : b1;
     }
-    __syncthreads();
+    wave_lds_fence();
     uint64_t kept = 0;
     for (int g0 = 0; g0 < G; g0 += L) {
       const int g = g0 + gl;
-      const double mine = g < G ? sg[g] : static_cast<double>(kNegInf);
+      const double mine = g < G ? sg[g] : kNegInf64;
       int rank = 0;
-      for (int h = 0; h < G; ++h) {
-        const double o = sg[h];
-        rank += (o > mine || (o == mine && h < g)) ? 1 : 0;
+      for (int h0 = 0; h0 < G; h0 += 4) {
+        double o[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) o[u] = sg[min(h0 + u, G - 1)];
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          rank += h0 + u < G && (o[u] > mine || (o[u] == mine && h0 + u < g)) ? 1 : 0;
       }
-      const uint64_t b = __ballot(g < G && rank < q.top_groups);
-      kept |= WAVE ? b : (((b >> (lane & 48)) & 0xFFFFull) << g0);
+      const uint64_t ballot = __ballot(g < G && rank < q.top_groups);
+      kept |= WAVE ? ballot : (((ballot >> (lane & 48)) & 0xFFFFull) << g0);
     }
 #pragma unroll
     for (int i = 0; i < KPL; ++i) {
-      const int e = min(gl + L * i, E - 1);
-      const int g = static_cast<int>((static_cast<uint32_t>(e) * q.group_magic) >> 20);  // e / gs
-      if (!((kept >> g) & 1)) open &= ~(1u << i);
+      if (!((kept >> group_of(min(gl + L * i, E - 1))) & 1)) {
+        v[i] = kNegInf;
+        val[i] = kNegInf64;
+      }
     }
   }
 
-  // keys: closed experts have a zero high word and go by index
-  uint64_t cand[KPL];
+  double cand[KPL];
 #pragma unroll
   for (int i = 0; i < KPL; ++i) {
     const int e = gl + L * i;
-    const uint64_t key = has_bias ? value_key(val[i], e) : route_key(v[i], e);
-    const uint64_t last = has_bias ? static_cast<uint64_t>(2047 - e) : static_cast<uint32_t>(~e);
-    cand[i] = e < E ? ((open >> i) & 1 ? key : last) : 0ull;
+    const double rank = BIAS ? val[i] : static_cast<double>(v[i]);
+    cand[i] = e < E ? candidate(v[i] > kNegInf ? rank : kMasked, e) : 2.0 * kMasked;
   }
-  sort_keys_desc<KPL>(cand);
-  uint64_t mine = 0, top = 0;
-  if (k <= 8)
-    select_rounds<KPL, 8, WAVE>(cand, k, gl, mine, top);
-  else
-    select_rounds<KPL, kMaxTopK, WAVE>(cand, k, gl, mine, top);
+  sort_desc64<KPL>(cand);
+  const double mine = k <= 8 ? select64<KPL, 8, WAVE>(cand, k, gl) : select64<KPL, kMaxTopK, WAVE>(cand, k, gl);
 
   // slot gl < k
-  const int id = gl >= k ? 0 : has_bias ? 1023 - static_cast<int>(mine & 1023) : key_expert(mine);
-  const bool on = gl < k && (mine >> 32) != 0;
+  const int id = gl < k ? candidate_expert(mine) : 0;
+  const bool on = gl < k && mine > 0.5 * kMasked;
   const float lv = on ? clean(load_logit(q.logits, q.dtype, t * q.ld + id)) : kNegInf;
-  double w;
-  if (softmax) {
-    // normalized over the k: relative to their own largest, which may lie far
-    // below the row's where a bias or the groups decide
-    float ref = m;
-    if (q.renormalize) {
-      ref = row16_max(lv);
-      if (!(ref > kNegInf)) ref = 0.0f;
-    }
-    w = exp(static_cast<double>(lv) - static_cast<double>(ref));
-    if (!q.renormalize && z > 0.0) w /= z;
-  } else {
-    w = on ? sigmoid64(lv) : 0.0;
+  // Weights.  Normalized over the k they are formed relative to the largest of
+  // their logits (softmax) or, below 0, of their scores (sigmoid): with c that
+  // logit, e^-c / (1 + e^-l) = 1 / (e^c + e^(c - l)), so that they are exact
+  // however far below the row's largest the k lie.
+  float ref = softmax ? m : 0.0f;
+  if (q.renormalize) {
+    const float most = row16_max(lv);
+    ref = most > kNegInf ? (softmax ? most : fminf(most, 0.0f)) : 0.0f;
   }
+  const double c = static_cast<double>(ref), l = static_cast<double>(lv);
+  double w = softmax ? exp64(l - c) : recip64(exp64(c) + exp64(c - l));
+  w = on ? w : 0.0;
   if (q.renormalize) {
     const double sum = row16_sum64(w);
     if (sum > 0.0) w /= sum;
+  } else if (softmax && z > 0.0) {
+    w /= z;
   }
   if (gl < k && t_own < q.T) {
     q.ids[t * k + gl] = id;
@@ -252,15 +377,19 @@ __global__ __launch_bounds__(256) void moe_route_scores_kernel(RouteParams q) {
 template <int KPL, bool WAVE>
 static void launch_scores(const RouteParams& q, hipStream_t s) {
   constexpr int kTok = 256 / (WAVE ? kWave : 16);
-  const size_t lds = q.groups > 1 ? static_cast<size_t>(kTok) * (q.E + kMaxRouteGroups) * sizeof(double) : 0;
-  moe_route_scores_kernel<KPL, WAVE><<<static_cast<unsigned>((q.T + kTok - 1) / kTok), 256, lds, s>>>(q);
+  const size_t lds = q.groups > 1 ? static_cast<size_t>(kTok) * (q.E + q.groups + kMaxRouteGroups) * sizeof(double) : 0;
+  const unsigned blocks = static_cast<unsigned>((static_cast<int64_t>(q.T) + kTok - 1) / kTok);
+  if (q.bias) moe_route_scores_kernel<KPL, WAVE, true><<<blocks, 256, lds, s>>>(q);
+  else moe_route_scores_kernel<KPL, WAVE, false><<<blocks, 256, lds, s>>>(q);
 }
 
 hipError_t launch_route_scores(const RouteParams& q, hipStream_t s) {
-  if (q.E > 256 || q.T <= kRouteWaveTokens) {
-    if (q.E <= 64) launch_scores<1, true>(q, s);
-    else if (q.E <= 128) launch_scores<2, true>(q, s);
-    else if (q.E <= 256) launch_scores<4, true>(q, s);
+  // A whole wave a token where 16 lanes would hold many experts each and the
+  // batch does not fill the chip (256 experts in groups with a bias: 1 token
+  // 5.2 us, with 16 lanes 7.8; 2048: 6.8 and 8.4; 4096: 9.4 and 8.6).
+  if (q.E > 256 || (q.E > 128 && q.T <= kRouteWaveTokens)) {
+    if (q.E <= 256) launch_scores<4, true>(q, s);
+    else if (q.E <= 320) launch_scores<5, true>(q, s);
     else if (q.E <= 512) launch_scores<8, true>(q, s);
     else launch_scores<16, true>(q, s);
   } else {

@@ -55,6 +55,10 @@ def route(logits, k, score="softmax", bias=None, groups=1, top_groups=1, group_b
             if score == "softmax" and on.any():  # the same ratio where the k lie far below the largest
                 lk = l[t, order]
                 w = np.where(on, np.exp(np.where(on, lk - lk[on].max(), -np.inf)), 0.0)
+            elif on.any():  # e^-c / (1 + e^-l) = 1 / (e^c + e^(c - l)): the same ratios for scores far below 1
+                lk = np.where(on, l[t, order], 0.0)
+                c = min(lk[on].max(), 0.0)
+                w = np.where(on, 1.0 / (np.exp(c) + np.exp(np.minimum(c - lk, 709.0))), 0.0)
             w = w / w.sum() if w.sum() > 0 else w
         out[t] = scale * w
     return ids, out

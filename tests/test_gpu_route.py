@@ -87,6 +87,7 @@ def test_route_masks(T, E, score, bias):
     l[8, 11] = 300.0
     l[9, 4] = float("nan")
     l[10] = 60.0 + 0.01 * torch.arange(E, device="cuda")
+    l[11] = -2000.0 - torch.arange(E, device="cuda")
     b = _bias(E) if bias else None
     if bias:
         b[2], b[E - 2], b[6] = -inf, float("nan"), 3.0
