@@ -123,7 +123,7 @@ typedef enum moe_score { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_scor
  * weights are formed in binary64 and rounded once.
  * num_groups: 1..64, a divisor of E; top_groups: 1..num_groups, with
  * top_groups * E / num_groups >= k.  num_groups = 1 has no groups (top_groups
- * and group_best are then 1).  scale: finite.
+ * is then 1, group_best without effect).  scale: finite.
  */
 typedef struct moe_router {
   int32_t score;       /* moe_score */
@@ -245,7 +245,9 @@ int int8_linear(const void* x_dev, int32_t dtype, int64_t ld_x, const void* w_de
                 void* workspace_dev, int64_t workspace_bytes, void* out_dev, int32_t out_dtype, int64_t ldo,
                 void* stream);
 
-/* Bytes of int8_linear's workspace for M tokens of K columns.  Host-only. */
+/* Bytes of int8_linear's workspace for M tokens of K columns (0 for a single
+ * token of at most 32768 columns: its codes stay in the kernel, and the
+ * workspace may be NULL).  Host-only. */
 int int8_linear_workspace(int64_t M, int64_t K, int64_t* bytes);
 
 /* ---------------------------------------------------------------------- */

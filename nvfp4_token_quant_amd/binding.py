@@ -256,14 +256,13 @@ def token_ceiling(max_prefill, piecewise_max, graph_max_bs, spec_draft_tokens) -
 # belong to the stream it ran on.  These calls serve single tokens, whose
 # kernels take a few microseconds: what surrounds the launch is kept short.
 
-def _raw_stream(device):
-    """The handle of the device's current stream."""
-    return torch._C._cuda_getCurrentRawStream(device.index)
+_raw_stream = torch._C._cuda_getCurrentRawStream  # device index -> handle of its current stream
+_current = torch._C._cuda_getDevice
 
 
 def _elsewhere(device, stream):
     """Whether a call has to switch to another device or stream."""
-    return stream is not None or device.index != torch.cuda.current_device()
+    return stream is not None or device.index != _current()
 
 
 def _switched(device, stream):
@@ -287,15 +286,16 @@ def _matrix(t, name, dtypes=DTYPES):
 
 
 def _vector(t, name, n, dtype, device):
+    """Checks a contiguous vector of n values; its address."""
     if not isinstance(t, torch.Tensor) or t.device != device:
         raise ValueError(f"{name} must be a tensor on {device}")
-    if t.dtype is not dtype or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+    if t.dtype is not dtype or t.shape != (n,) or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of {n} values, got {t.dtype} {tuple(t.shape)}")
     return t.data_ptr()
 
 
 def _same(t, name, shape, device):
-    if t.device != device or t.shape != torch.Size(shape):
+    if t.device != device or t.shape != shape:
         raise ValueError(f"{name} must be {tuple(shape)} on {device}, got {tuple(t.shape)} on {t.device}")
 
 
@@ -344,8 +344,8 @@ def route(logits, top_k, router, bias=None, out=None, stream=None):
             _same(t, name, (T, top_k), device)
             if not t.is_contiguous():
                 raise ValueError(f"{name} must be contiguous")
-    _check(lib().moe_route(router.desc, logits.data_ptr(), DTYPES[logits.dtype], T, E, _ld(logits), top_k, b,
-                           ids.data_ptr(), w.data_ptr(), _raw_stream(device)))
+    _check((_lib or lib()).moe_route(router.desc, logits.data_ptr(), DTYPES[logits.dtype], T, E, _ld(logits), top_k, b,
+                           ids.data_ptr(), w.data_ptr(), _raw_stream(device.index)))
     return ids, w
 
 
@@ -372,6 +372,13 @@ class Norm:
 # aligned; quicker to fill)
 _BLOCK_NORM = struct.Struct("@qqiiPqPqPqqiffPPPqPq")
 assert _BLOCK_NORM.size == ctypes.sizeof(MoeBlockNormArgs)
+
+
+def _empty(like, rows, cols, dtype):
+    """A contiguous [rows, cols] of `dtype` beside `like`, of which it has the shape."""
+    if like.dtype is dtype and like.is_contiguous():
+        return torch.empty_like(like)
+    return torch.empty((rows, cols), dtype=dtype, device=like.device)
 
 
 def block_norm(residual, y=None, before=None, after=None, gate=None, gate_sigmoid=False, res_scale=1.0,
@@ -416,14 +423,14 @@ def block_norm(residual, y=None, before=None, after=None, gate=None, gate_sigmoi
     nb = before.desc(H, dtype, device, "before") if before is not None else 0
     r, h = residual_out, h_out
     if r is None and (y is not None or before is None or res_scale != 1.0):
-        r = torch.empty((T, H), dtype=residual.dtype, device=device)
+        r = _empty(residual, T, H, residual.dtype)
     if h is None and before is not None:
-        h = torch.empty((T, H), dtype=dtype, device=device)
-    _check(lib().moe_block_norm(_BLOCK_NORM.pack(
+        h = _empty(residual if y is None else y, T, H, dtype)
+    _check((_lib or lib()).moe_block_norm(_BLOCK_NORM.pack(
         T, H, DTYPES[dtype], DTYPES[residual.dtype], residual.data_ptr(), _ld(residual), yp, ld_y, gp, ld_gate,
         gate_cols, 1 if gate_sigmoid else 0, res_scale, out_scale, na, nb,
         r.data_ptr() if r is not None else 0, _ld(r) if r is not None else 0,
-        h.data_ptr() if h is not None else 0, _ld(h) if h is not None else 0), _raw_stream(device)))
+        h.data_ptr() if h is not None else 0, _ld(h) if h is not None else 0), _raw_stream(device.index)))
     return (residual if r is None else r), h
 
 
@@ -439,8 +446,8 @@ def int8_quantize_per_token(x, stream=None):
     ld = (cols + 15) // 16 * 16
     codes = torch.empty((rows, ld), dtype=torch.int8, device=device)
     scale = torch.empty((rows,), dtype=torch.float32, device=device)
-    _check(lib().int8_quantize_per_token(x.data_ptr(), DTYPES[x.dtype], rows, cols, _ld(x), codes.data_ptr(), ld,
-                                         scale.data_ptr(), _raw_stream(device)))
+    _check((_lib or lib()).int8_quantize_per_token(x.data_ptr(), DTYPES[x.dtype], rows, cols, _ld(x), codes.data_ptr(), ld,
+                                         scale.data_ptr(), _raw_stream(device.index)))
     return (codes[:, :cols] if ld != cols else codes), scale
 
 
@@ -471,9 +478,14 @@ def int8_matmul(codes, scale, w_codes, w_scale, bias=None, out_dtype=torch.bfloa
     b = _vector(bias, "bias", N, torch.float32, device) if bias is not None else None
     lda, ldb = _ld16(codes, "codes"), _ld16(w_codes, "w_codes")
     out = _product_out(out, out_dtype, M, N, device)
-    _check(lib().int8_matmul(codes.data_ptr(), lda, sa, w_codes.data_ptr(), ldb, sb, b, M, N, K, out.data_ptr(),
-                             DTYPES[out.dtype], _ld(out), _raw_stream(device)))
+    _check((_lib or lib()).int8_matmul(codes.data_ptr(), lda, sa, w_codes.data_ptr(), ldb, sb, b, M, N, K, out.data_ptr(),
+                             DTYPES[out.dtype], _ld(out), _raw_stream(device.index)))
     return out
+
+
+def _linear_workspace(M, K):
+    """int8_linear_workspace (a single token of up to 32768 columns needs none)."""
+    return 0 if M == 1 and K <= 32768 else M * ((K + 15) // 16 * 16 + 4)
 
 
 def int8_linear(x, w_codes, w_scale, bias=None, out_dtype=None, out=None, stream=None):
@@ -491,11 +503,11 @@ def int8_linear(x, w_codes, w_scale, bias=None, out_dtype=None, out=None, stream
     b = _vector(bias, "bias", N, torch.float32, device) if bias is not None else None
     ldb = _ld16(w_codes, "w_codes")
     out = _product_out(out, out_dtype or x.dtype, M, N, device)
-    work = M * ((K + 15) // 16 * 16 + 4)  # int8_linear_workspace
-    scratch = torch.empty((work,), dtype=torch.uint8, device=device)
-    _check(lib().int8_linear(x.data_ptr(), DTYPES[x.dtype], _ld(x), w_codes.data_ptr(), ldb, sb, b, M, N, K,
-                             scratch.data_ptr(), work, out.data_ptr(), DTYPES[out.dtype], _ld(out),
-                             _raw_stream(device)))
+    work = _linear_workspace(M, K)
+    scratch = torch.empty((work,), dtype=torch.uint8, device=device) if work else None
+    _check((_lib or lib()).int8_linear(x.data_ptr(), DTYPES[x.dtype], _ld(x), w_codes.data_ptr(), ldb, sb, b, M, N, K,
+                             scratch.data_ptr() if work else None, work, out.data_ptr(), DTYPES[out.dtype], _ld(out),
+                             _raw_stream(device.index)))
     return out
 
 

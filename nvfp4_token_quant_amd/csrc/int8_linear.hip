@@ -7,6 +7,7 @@
 #include <algorithm>
 #include <atomic>
 #include <iterator>
+#include <type_traits>
 
 #include "common.hpp"
 #include "dtype.hpp"
@@ -174,31 +175,24 @@ hipError_t launch_int8_quantize_rows(const void* x, int dtype, int64_t rows, int
 // assigned to lanes in any order that both operands share.
 // ---------------------------------------------------------------------------
 
-// out[m, n]
-__device__ __forceinline__ void store_one(const Int8GemmParams& p, int m, int n, int acc) {
-  float f = static_cast<float>(acc) * (p.sa[m] * p.sb[n]);
-  if (p.bias) f += p.bias[n];
+// The sum times its scales, plus the bias, in binary32: the same steps in every
+// kernel (one rounding of product and bias), so that a token's result does not
+// depend on the batch that it comes with.
+__device__ __forceinline__ float scaled(int acc, float s, bool has_bias, float bias) {
+  const float a = static_cast<float>(acc);
+  return has_bias ? __builtin_fmaf(a, s, bias) : a * s;
+}
+
+// out[m, n]; sa: token m's scale
+__device__ __forceinline__ void store_one(const Int8GemmParams& p, int m, int n, int acc, float sa) {
+  const float f = scaled(acc, sa * p.sb[n], p.bias != nullptr, p.bias ? p.bias[n] : 0.0f);
   const int64_t at = static_cast<int64_t>(m) * p.ldo + n;
   if (p.dtype == MOE_BF16) Bf16::put(p.out, at, f);
   else if (p.dtype == MOE_F16) F16::put(p.out, at, f);
   else F32::put(p.out, at, f);
 }
 
-// 16 bytes of a row at column c, zero from column K on.  The row's last
-// 16-byte piece lies inside its leading dimension.
-__device__ __forceinline__ i32x4 load_k16(const int8_t* row, int c, int K) {
-  i32x4 v = *reinterpret_cast<const i32x4*>(row + min(c, (K - 1) / 16 * 16));
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int left = K - c - 4 * j;  // bytes of this dword before K
-    if (left < 4) v[j] = left <= 0 ? 0 : v[j] & static_cast<int32_t>((1u << (8 * left)) - 1u);
-  }
-  return v;
-}
-
-// One token: a wave a channel, products of four bytes at a time in the vector
-// ALU.  A row's loads are whole kilobytes; kDotLoads of them are in flight
-// together.
+// kDotLoads loads of a whole kilobyte of a channel's row are in flight together.
 constexpr int kDotLoads = 8;
 
 __device__ __forceinline__ int wave_sum_i32(int v) {
@@ -213,26 +207,99 @@ __device__ __forceinline__ int wave_sum_i32(int v) {
   return static_cast<int>(a) + static_cast<int>(b);
 }
 
-__global__ __launch_bounds__(256) void int8_dot_kernel(Int8GemmParams p) {
-  const int lane = threadIdx.x & (kWave - 1);
-  const int n = static_cast<int>(blockIdx.x) * 4 + static_cast<int>(threadIdx.x) / kWave;
-  if (n >= p.N) return;  // whole waves
-  const int8_t* brow = p.b + static_cast<int64_t>(n) * p.ldb;
-  const int last = (p.K - 1) / 16 * 16;  // a row's last piece
-  int acc = 0;
-  for (int c0 = 16 * lane; c0 < p.K; c0 += 1024 * kDotLoads) {
-    i32x4 b[kDotLoads];
+// One token: a wave a channel, products of four bytes at a time in the vector
+// ALU (a tile of matrix instructions would be a sixteenth full).  Every block
+// keeps the row's codes in LDS; with an unquantized row x of type T it makes
+// them itself, behind the loads of its waves' first channels, by the steps of
+// the quantization kernel (two launches cost more than the work: 7168 x 2048
+// 8.1 us in two kernels, 4.5 in one).
+constexpr int kTokenThreads = 512;
+static_assert(kTokenThreads * 8 * 8 == kLinearTokenMaxK, "eight pieces of a row a thread at most");
+
+struct Codes {};  // the row is p.a, its scale p.sa[0]
+
+// Eight codes at column c of the row, 0 from K on.  The row's last 16-byte
+// piece lies inside its leading dimension.
+__device__ __forceinline__ u32x2 load_codes8(const int8_t* row, int c, int K) {
+  u32x2 v = *reinterpret_cast<const u32x2*>(row + min(c, (K + 15) / 16 * 16 - 8));
 #pragma unroll
-    for (int i = 0; i < kDotLoads; ++i) b[i] = *reinterpret_cast<const i32x4*>(brow + min(c0 + 1024 * i, last));
+  for (int j = 0; j < 2; ++j) {
+    const int left = K - c - 4 * j;  // bytes of this dword before K
+    if (left < 4) v[j] = left <= 0 ? 0u : v[j] & ((1u << (8 * left)) - 1u);
+  }
+  return v;
+}
+
+template <typename T, int NC>
+__global__ __launch_bounds__(kTokenThreads) void int8_token_kernel(Int8GemmParams p, const void* __restrict__ x) {
+  extern __shared__ __align__(16) uint8_t s_codes[];  // the row's codes, zeros up to a whole kilobyte
+  __shared__ float s_am[kTokenThreads / kWave];
+  constexpr int W = kTokenThreads / kWave;
+  const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
+  const int last = (p.K - 1) / 16 * 16;
+  int n = static_cast<int>(blockIdx.x) * W + wave;
+  // a chunk: kDotLoads kilobytes of a channel's row (past its end the last
+  // piece again, times zero)
+  const auto load = [&](i32x4 (&b)[kDotLoads], int ch, int c0) {
+    const int8_t* row = p.b + static_cast<int64_t>(min(ch, p.N - 1)) * p.ldb;
 #pragma unroll
-    for (int i = 0; i < kDotLoads; ++i) {
-      const i32x4 a = load_k16(p.a, c0 + 1024 * i, p.K);
+    for (int i = 0; i < kDotLoads; ++i) b[i] = *reinterpret_cast<const i32x4*>(row + min(c0 + 1024 * i + 16 * lane, last));
+  };
+  const int kib = (p.K + 1023) / 1024 * 1024;
+  i32x4 b[kDotLoads];
+  float scale;
+  if constexpr (std::is_same_v<T, Codes>) {
+    u32x2 q[NC];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) acc = __builtin_amdgcn_sdot4(a[j], b[i][j], acc, false);
+    for (int i = 0; i < NC; ++i) q[i] = load_codes8(p.a, 8 * (tid + kTokenThreads * i), p.K);
+    load(b, n, 0);
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const int c = 8 * (tid + kTokenThreads * i);
+      if (c < kib) *reinterpret_cast<u32x2*>(s_codes + c) = q[i];
+    }
+    scale = p.sa[0];
+  } else {
+    float f[NC][8];
+#pragma unroll
+    for (int i = 0; i < NC; ++i) load_piece<T, false>(f[i], x, 8 * (tid + kTokenThreads * i), p.K);
+    load(b, n, 0);
+    float am = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NC; ++i) am = fmaxf(am, amax8(f[i]));
+    am = wave_max(am);
+    if (lane == 0) s_am[wave] = am;
+    lds_barrier();  // (the channels' loads stay in flight)
+#pragma unroll
+    for (int w = 0; w < W; ++w) am = fmaxf(am, s_am[w]);
+    const bool some = am >= kMinAmax;
+    const float inv = some ? 127.0f / am : 0.0f;
+    scale = some ? am / 127.0f : 1.0f;
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const int c = 8 * (tid + kTokenThreads * i);
+      if (c < kib) *reinterpret_cast<u32x2*>(s_codes + c) = pack_codes(f[i], inv);
     }
   }
-  acc = wave_sum_i32(acc);
-  if (lane == 0) store_one(p, 0, n, acc);
+  lds_barrier();
+  for (; n < p.N; n += static_cast<int>(gridDim.x) * W) {
+    int acc = 0;
+    for (int c0 = 0; c0 < p.K; c0 += 1024 * kDotLoads) {
+#pragma unroll
+      for (int i = 0; i < kDotLoads; ++i) {
+        if (c0 + 1024 * i < p.K) {
+          const i32x4 a = *reinterpret_cast<const i32x4*>(s_codes + c0 + 1024 * i + 16 * lane);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc = __builtin_amdgcn_sdot4(a[j], b[i][j], acc, false);
+        }
+      }
+      // the next chunk, of this channel or the next
+      if (c0 + 1024 * kDotLoads < p.K) load(b, n, c0 + 1024 * kDotLoads);
+      else if (n + static_cast<int>(gridDim.x) * W < p.N) load(b, n + static_cast<int>(gridDim.x) * W, 0);
+    }
+    acc = wave_sum_i32(acc);
+    if (lane == 0) store_one(p, 0, n, acc, scale);
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -319,8 +386,7 @@ __device__ __forceinline__ void store_tile(const Int8GemmParams& p, const i32x4 
       float v[kP];
 #pragma unroll
       for (int i = 0; i < kP; ++i) {
-        v[i] = static_cast<float>(acc[f + i / 4][m][i % 4]) * (sa * sb[4 * f + i]);
-        if (p.bias) v[i] += bias[4 * f + i];
+        v[i] = scaled(acc[f + i / 4][m][i % 4], sa * sb[4 * f + i], p.bias != nullptr, bias[4 * f + i]);
       }
       const int n = n0 + 4 * f;
       if (p.vec_out && n + kP <= p.N) {
@@ -663,6 +729,15 @@ static hipError_t launch_tiled(const Int8GemmParams& p, hipStream_t s) {
   return hipGetLastError();
 }
 
+template <typename T>
+static void launch_token(const Int8GemmParams& p, const void* x, hipStream_t s) {
+  // two blocks a CU; a wave takes several channels where there are more
+  const unsigned blocks = static_cast<unsigned>(std::min((p.N + 7) / 8, 512));
+  const size_t lds = static_cast<size_t>((p.K + 1023) / 1024 * 1024);
+  if (p.K <= kLinearTokenMaxK / 4) int8_token_kernel<T, 2><<<blocks, kTokenThreads, lds, s>>>(p, x);
+  else int8_token_kernel<T, 8><<<blocks, kTokenThreads, lds, s>>>(p, x);
+}
+
 // How long `tiles` take where `slots` run at once, in units of one round: the
 // mean of the whole rounds and of the share of work, since the chip's CUs
 // drift apart over several rounds.
@@ -672,10 +747,8 @@ static double rounds(int64_t tiles, int64_t slots) {
 }
 
 hipError_t launch_int8_matmul(const Int8GemmParams& p, hipStream_t s) {
-  // One token and fewer channels than SIMDs: no tile to share (8000 x 1000:
-  // 4.0 us, 16 x 16 tiles 5.4; 7168 x 2048: 6.5 and 5.6).
-  if (p.M == 1 && p.N <= 1024) {
-    int8_dot_kernel<<<static_cast<unsigned>((p.N + 3) / 4), 256, 0, s>>>(p);
+  if (p.M == 1 && p.K <= kLinearTokenMaxK) {
+    launch_token<Codes>(p, nullptr, s);
     return hipGetLastError();
   }
   // Rows far apart: a tile's rows are addressed with 32-bit byte offsets, and
@@ -703,6 +776,13 @@ hipError_t launch_int8_matmul(const Int8GemmParams& p, hipStream_t s) {
     case 6: return launch_ring<2, 4, 4, 2, 1, 2, 2>(p, s);
     default: return launch_tiled<2, 4, 8, 4>(p, s);
   }
+}
+
+hipError_t launch_int8_token(const Int8GemmParams& p, const void* x, int x_dtype, hipStream_t s) {
+  if (x_dtype == MOE_BF16) launch_token<Bf16>(p, x, s);
+  else if (x_dtype == MOE_F16) launch_token<F16>(p, x, s);
+  else launch_token<F32>(p, x, s);
+  return hipGetLastError();
 }
 
 }  // namespace nvfp4

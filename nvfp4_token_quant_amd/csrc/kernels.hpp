@@ -195,6 +195,10 @@ struct Int8GemmParams {
   int vec_out;  // 1: rows of out start at multiples of 16 bytes
 };
 hipError_t launch_int8_matmul(const Int8GemmParams& p, hipStream_t s);
+// One token (M = 1, K <= kLinearTokenMaxK) from its unquantized row x; p.a and
+// p.sa are not read.
+constexpr int kLinearTokenMaxK = 32768;
+hipError_t launch_int8_token(const Int8GemmParams& p, const void* x, int x_dtype, hipStream_t s);
 
 // gemm_kernels.hip
 // Rows per tile and kernel family for a forward of T tokens.

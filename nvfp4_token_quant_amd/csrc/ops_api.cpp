@@ -107,9 +107,9 @@ int check_matmul(const void* a_dev, int64_t lda, const float* scale_a_dev, const
   return NVFP4_OK;
 }
 
-int run_matmul(const void* a_dev, int64_t lda, const float* scale_a_dev, const void* b_dev, int64_t ldb,
-               const float* scale_b_dev, const float* bias_dev, int64_t M, int64_t N, int64_t K, void* out_dev,
-               int32_t dtype, int64_t ldo, void* stream) {
+Int8GemmParams gemm_params(const void* a_dev, int64_t lda, const float* scale_a_dev, const void* b_dev, int64_t ldb,
+                           const float* scale_b_dev, const float* bias_dev, int64_t M, int64_t N, int64_t K,
+                           void* out_dev, int32_t dtype, int64_t ldo) {
   Int8GemmParams p{};
   p.a = static_cast<const int8_t*>(a_dev);
   p.b = static_cast<const int8_t*>(b_dev);
@@ -125,13 +125,22 @@ int run_matmul(const void* a_dev, int64_t lda, const float* scale_a_dev, const v
   p.K = static_cast<int>(K);
   p.dtype = dtype;
   p.vec_out = row_vectors(out_dev, ldo, dtype_bytes(dtype)) ? 1 : 0;
-  hipError_t e = launch_int8_matmul(p, static_cast<hipStream_t>(stream));
+  return p;
+}
+
+int run_matmul(const void* a_dev, int64_t lda, const float* scale_a_dev, const void* b_dev, int64_t ldb,
+               const float* scale_b_dev, const float* bias_dev, int64_t M, int64_t N, int64_t K, void* out_dev,
+               int32_t dtype, int64_t ldo, void* stream) {
+  hipError_t e = launch_int8_matmul(
+      gemm_params(a_dev, lda, scale_a_dev, b_dev, ldb, scale_b_dev, bias_dev, M, N, K, out_dev, dtype, ldo),
+      static_cast<hipStream_t>(stream));
   if (e != hipSuccess) return hip_fail(e, "int8_matmul launch");
   return api_ok();
 }
 
 // int8_linear's workspace: the codes (rows of whole 16-byte pieces), then the
-// scales.
+// scales; none for a single token, which one kernel quantizes and multiplies.
+bool linear_in_one(int64_t M, int64_t K) { return M == 1 && K <= kLinearTokenMaxK; }
 int64_t linear_codes_bytes(int64_t M, int64_t K) { return M * ((K + 15) / 16 * 16); }
 
 }  // namespace
@@ -152,8 +161,6 @@ int check_router(const moe_router* r, int64_t E, int64_t top_k) {
                     r->top_groups, r->num_groups);
   if (r->group_best != 1 && r->group_best != 2)
     return api_fail(NVFP4_ERR_INVALID_ARG, "group_best must be 1 or 2 (got %d)", r->group_best);
-  if (r->num_groups == 1 && r->group_best != 1)
-    return api_fail(NVFP4_ERR_INVALID_ARG, "group_best must be 1 without groups");
   if (r->renormalize != 0 && r->renormalize != 1)
     return api_fail(NVFP4_ERR_INVALID_ARG, "renormalize must be 0 or 1 (got %d)", r->renormalize);
   if (!std::isfinite(r->scale)) return api_fail(NVFP4_ERR_INVALID_ARG, "router scale must be finite");
@@ -321,7 +328,7 @@ int int8_linear_workspace(int64_t M, int64_t K, int64_t* bytes) {
   if (M < 0 || M > INT32_MAX || K < 1 || K > 131071)
     return api_fail(NVFP4_ERR_INVALID_ARG, "M must be in [0, 2^31) and K in [1, 131071] (got %lld, %lld)",
                     (long long)M, (long long)K);
-  *bytes = linear_codes_bytes(M, K) + M * 4;
+  *bytes = linear_in_one(M, K) ? 0 : linear_codes_bytes(M, K) + M * 4;
   return api_ok();
 }
 
@@ -334,27 +341,34 @@ int int8_linear(const void* x_dev, int32_t dtype, int64_t ld_x, const void* w_de
   int64_t need = 0;
   int st = int8_linear_workspace(M, K, &need);
   if (st != NVFP4_OK) return st;
-  const int64_t ldc = (K + 15) / 16 * 16, codes_bytes = linear_codes_bytes(M, K);
-  if (M > 0 && (!workspace_dev || !aligned(workspace_dev, 16) || workspace_bytes < need))
+  const int64_t ldc = (K + 15) / 16 * 16;
+  if (need > 0 && (!workspace_dev || !aligned(workspace_dev, 16) || workspace_bytes < need))
     return api_fail(NVFP4_ERR_INVALID_ARG, "workspace must be 16-byte aligned, of at least %lld bytes (got %lld)",
                     (long long)need, (long long)workspace_bytes);
-  float* scales = reinterpret_cast<float*>(static_cast<char*>(workspace_dev) + codes_bytes);
-  // The product's checks first (nothing is enqueued on an error), with x in
-  // place of the codes where they are about x.
-  st = check_matmul(workspace_dev, ldc, scales, w_dev, ldw, scale_w_dev, bias_dev, M, N, K, out_dev, out_dtype, ldo);
+  // Both steps' checks first (nothing is enqueued on an error); where no codes
+  // are kept, with addresses of their alignment that nothing reads or writes.
+  const bool one = linear_in_one(M, K);
+  char* const codes = one ? reinterpret_cast<char*>(uintptr_t{16}) : static_cast<char*>(workspace_dev);
+  float* const scales = reinterpret_cast<float*>(codes + linear_codes_bytes(M, K));
+  st = check_matmul(codes, ldc, scales, w_dev, ldw, scale_w_dev, bias_dev, M, N, K, out_dev, out_dtype, ldo);
   if (st != NVFP4_OK) return st;
   if (M == 0 || N == 0) return api_ok();
-  st = check_quantize(x_dev, dtype, M, K, ld_x, workspace_dev, ldc, scales);
+  st = check_quantize(x_dev, dtype, M, K, ld_x, codes, ldc, scales);
   if (st != NVFP4_OK) return st;
-  const int64_t no = span(M, ldo, N, ob);
-  if (overlap(out_dev, no, x_dev, span(M, ld_x, K, xb)) ||
-      overlap(workspace_dev, need, w_dev, span(N, ldw, ldc, 1)) || overlap(workspace_dev, need, scale_w_dev, N * 4) ||
-      (bias_dev && overlap(workspace_dev, need, bias_dev, N * 4)))
+  if (overlap(out_dev, span(M, ldo, N, ob), x_dev, span(M, ld_x, K, xb)) ||
+      overlap(codes, need, w_dev, span(N, ldw, ldc, 1)) || overlap(codes, need, scale_w_dev, N * 4) ||
+      (bias_dev && overlap(codes, need, bias_dev, N * 4)))
     return api_fail(NVFP4_ERR_ALIAS, "out or workspace overlaps an input");
-  st = run_quantize(x_dev, dtype, M, K, ld_x, workspace_dev, ldc, scales, stream);
+  if (one) {
+    const Int8GemmParams p = gemm_params(nullptr, ldc, nullptr, w_dev, ldw, scale_w_dev, bias_dev, M, N, K, out_dev,
+                                         out_dtype, ldo);
+    hipError_t e = launch_int8_token(p, x_dev, dtype, static_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return hip_fail(e, "int8_linear launch");
+    return api_ok();
+  }
+  st = run_quantize(x_dev, dtype, M, K, ld_x, codes, ldc, scales, stream);
   if (st != NVFP4_OK) return st;
-  return run_matmul(workspace_dev, ldc, scales, w_dev, ldw, scale_w_dev, bias_dev, M, N, K, out_dev, out_dtype, ldo,
-                    stream);
+  return run_matmul(codes, ldc, scales, w_dev, ldw, scale_w_dev, bias_dev, M, N, K, out_dev, out_dtype, ldo, stream);
 }
 
 }  // extern "C"

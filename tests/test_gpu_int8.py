@@ -98,6 +98,16 @@ def test_product_sizes(M, N, K):
     _check_product(a, sa, b, sb, bias=_randn(N, seed=5), dtype=F16)
 
 
+def test_product_does_not_depend_on_the_batch():
+    """A token's result is the same bit for bit in every batch, and so in every kernel."""
+    K, N = 333, 900
+    a, sa, b, sb = _codes(2600, K, 1), _scales(2600, 3), _codes(N, K, 2), _scales(N, 4)
+    bias = _randn(N, seed=5)
+    whole = binding.int8_matmul(a, sa, b, sb, bias=bias, out_dtype=F32)
+    for M in (1, 2, 17, 40, 100, 300, 700, 1300, 2000):
+        assert torch.equal(binding.int8_matmul(a[:M], sa[:M], b, sb, bias=bias, out_dtype=F32), whole[:M]), M
+
+
 @pytest.mark.parametrize("M", [2, 40, 300])
 def test_product_full_range(M):
     """The largest sum that int32 holds: 131071 products of (-128)^2."""
@@ -158,6 +168,30 @@ def test_linear(M, N, K, dtype):
     other = binding.int8_linear(x, wq, ws, bias=bias, stream=s)
     torch.cuda.synchronize()
     assert torch.equal(other, got)
+
+
+@pytest.mark.parametrize("N,K", [(1, 1), (7, 9), (8, 1024), (2048, 7168), (5000, 640), (300, 8192), (100, 8193),
+                                 (64, 20001), (40, 32768), (33, 32769), (16, 131071)])
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+def test_linear_one_token(N, K, dtype):
+    """One token in one kernel equals the two steps bit for bit, and the reference."""
+    print(f"one token N={N} K={K} {dtype}", flush=True)
+    for c0, seed in ((0, 1), (1, 2)):
+        x = _randn(1, K + c0, seed=seed, dtype=dtype)[:, c0:]
+        if seed == 2:
+            x[0, K // 2] = -90.0
+        w, ws = _codes(N, K, 3), 0.01 * _scales(N, 4)
+        bias = _randn(N, seed=5)
+        got = binding.int8_linear(x, w, ws, bias=bias, out_dtype=F32)
+        q, s = binding.int8_quantize_per_token(x)
+        two = binding.int8_matmul(q, s, w, ws, bias=bias, out_dtype=F32)
+        torch.cuda.synchronize()
+        assert torch.equal(got, two)
+        ops_ref.check_product(got, *ops_ref.int8_product(*ops_ref.int8_rows(x), w.cpu().numpy(), ws.cpu().numpy(),
+                                                         bias.cpu().numpy()))
+    zero = binding.int8_linear(torch.zeros((1, K), dtype=dtype, device="cuda"), w, ws, bias=bias)
+    torch.cuda.synchronize()
+    assert torch.equal(zero, bias.to(dtype)[None])
 
 
 def test_product_refusals_and_empty():

@@ -125,6 +125,7 @@ def test_route_empty_and_outputs():
     s = torch.cuda.Stream()
     s.wait_stream(torch.cuda.current_stream())
     _check(l, 3, stream=s)
+    _check(l, 3, group_best=2)  # without groups it has no effect
     for bad in (dict(groups=3), dict(groups=4, top_groups=1, group_best=2)):
         with pytest.raises(binding.Nvfp4Error):
             binding.route(l, 8, binding.Router(**bad))

@@ -27,7 +27,7 @@ def _route(r=None, logits=1 << 20, dtype=F32, T=4, E=16, ld=16, k=2, bias=0, ids
 
 def test_route_refusals():
     for bad in (dict(score=2), dict(num_groups=0), dict(num_groups=3), dict(num_groups=65, top_groups=65),
-                dict(num_groups=4, top_groups=5), dict(num_groups=4, top_groups=0), dict(group_best=2),
+                dict(num_groups=4, top_groups=5), dict(num_groups=4, top_groups=0), dict(group_best=0),
                 dict(num_groups=4, top_groups=2, group_best=3), dict(renormalize=2), dict(scale=float("inf")),
                 dict(scale=float("nan"))):
         assert _route(_router(**bad)) == 1, bad
@@ -120,6 +120,9 @@ def _linear(x=1 << 20, dtype=BF16, ldx=60, w=1 << 21, ldw=64, sw=1 << 22, bias=0
 def test_int8_linear_refusals():
     n = ctypes.c_int64()
     assert binding.lib().int8_linear_workspace(4, 60, ctypes.byref(n)) == 0 and n.value == 4 * 68
+    for M, K in ((0, 5), (1, 1), (1, 32768), (1, 32769), (1, 131071), (2, 16), (300, 1001)):
+        assert binding.lib().int8_linear_workspace(M, K, ctypes.byref(n)) == 0
+        assert n.value == binding._linear_workspace(M, K)
     assert binding.lib().int8_linear_workspace(4, 0, ctypes.byref(n)) == 1
     assert binding.lib().int8_linear_workspace(-1, 60, ctypes.byref(n)) == 1
     assert binding.lib().int8_linear_workspace(4, 60, None) == 1
@@ -129,6 +132,7 @@ def test_int8_linear_refusals():
     for alias in (dict(out=1 << 20), dict(out=1 << 21), dict(out=1 << 22), dict(out=1 << 23), dict(ws=1 << 20),
                   dict(ws=1 << 21), dict(ws=1 << 22), dict(bias=1 << 23), dict(bias=1 << 24)):
         assert _linear(**alias) == 3, alias
+    assert _linear(M=1, ws=0, wsb=0, x=0) == 1 and _linear(M=1, ws=0, wsb=0, out=1 << 20) == 3
     assert _linear(M=0, x=0, ws=0, wsb=0, out=0) == 0 and _linear(N=0, w=0, sw=0, out=0) == 0
 
 
