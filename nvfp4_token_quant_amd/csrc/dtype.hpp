@@ -6,8 +6,11 @@
 
 namespace nvfp4 {
 
+// Word, value(): an element's bits and its binary32 value.
 struct Bf16 {
   static constexpr int kBytes = 2;
+  using Word = uint16_t;
+  __device__ static float value(Word w) { return __uint_as_float(static_cast<uint32_t>(w) << 16); }
   __device__ static float get(const void* p, int64_t i) {
     return __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(p)[i]) << 16);
   }
@@ -25,6 +28,8 @@ struct Bf16 {
 
 struct F16 {
   static constexpr int kBytes = 2;
+  using Word = _Float16;
+  __device__ static float value(Word w) { return static_cast<float>(w); }
   __device__ static float get(const void* p, int64_t i) {
     return static_cast<float>(static_cast<const _Float16*>(p)[i]);
   }
@@ -41,6 +46,8 @@ struct F16 {
 
 struct F32 {
   static constexpr int kBytes = 4;
+  using Word = float;
+  __device__ static float value(Word w) { return w; }
   __device__ static float get(const void* p, int64_t i) { return static_cast<const float*>(p)[i]; }
   __device__ static void put(void* p, int64_t i, float f) { static_cast<float*>(p)[i] = f; }
 };

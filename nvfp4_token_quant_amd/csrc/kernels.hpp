@@ -153,6 +153,8 @@ struct RouteParams {
   int T, E, k, dtype;
   int score, groups, top_groups, group_best, renormalize;
   float scale;
+  int group_lanes;       // set at the launch: lanes of a token that hold a whole group, 0 if groups do not
+                         // fall on a power of two of whole lanes
   uint32_t group_magic;  // ceil(2^20 * groups / E): (e * magic) >> 20 is e's group (e < 1024)
 };
 hipError_t launch_route_scores(const RouteParams& q, hipStream_t s);

@@ -39,21 +39,27 @@ __device__ __forceinline__ float load_logit(const void* p, int dtype, int64_t i)
   if (dtype == MOE_F32) return F32::get(p, i);
   return dtype == MOE_BF16 ? Bf16::get(p, i) : F16::get(p, i);
 }
-// Logits gl, gl + L, ... of a row (past the end: the last one again).
-template <typename T, int KPL, int L>
-__device__ __forceinline__ void load_row(float (&v)[KPL], const void* p, int64_t row, int gl, int E) {
+// Values first .. first + KPL - 1 of a row of E; past the end the last one again.
+template <typename T, int KPL>
+__device__ __forceinline__ void load_row(float (&v)[KPL], const void* p, int64_t row, int first, int E) {
+  if (first + KPL <= E) {
+    // consecutive: wide loads at any address
+    typename T::Word w[KPL];
+    __builtin_memcpy(w, static_cast<const char*>(p) + (row + first) * T::kBytes, sizeof(w));
 #pragma unroll
-  for (int i = 0; i < KPL; ++i) v[i] = T::get(p, row + min(gl + L * i, E - 1));
+    for (int i = 0; i < KPL; ++i) v[i] = T::value(w[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < KPL; ++i) v[i] = T::get(p, row + min(first + i, E - 1));
+  }
 }
 
 // NaN counts as masked, +inf as the largest finite value.
 __device__ __forceinline__ float clean(float v) { return v >= kNegInf ? fminf(v, kF32Max) : kNegInf; }
 
-// exp(x) in binary64 to 2^-47 of it: x = n ln 2 + r with |r| <= ln 2 / 2, e^r by
-// its series to r^11 (the rest is below r^12 / 12!).  0 far below -745; above
-// 709 the value there.
+// exp(x) in binary64 to 2^-47 of it, x in [-1200, 709]: x = n ln 2 + r with |r| <=
+// ln 2 / 2, e^r by its series to r^11 (the rest is below r^12 / 12!).  0 below -745.
 __device__ __forceinline__ double exp64(double x) {
-  x = fmin(fmax(x, -1200.0), 709.0);
   const double n = __builtin_rint(x * 1.4426950408889634);
   const double r = __builtin_fma(n, -1.9082149292705877e-10, __builtin_fma(n, -0.693147180369123816490, x));
   double p = 1.0 / 39916800.0;
@@ -70,11 +76,17 @@ __device__ __forceinline__ double exp64(double x) {
   p = __builtin_fma(p, r, 1.0);
   return __builtin_amdgcn_ldexp(p, static_cast<int>(n));
 }
-// 1 / d for d >= 1, finite: the hardware's reciprocal and two Newton steps.
+// The same for any x: above 709 the value there.
+__device__ __forceinline__ double exp64_any(double x) { return exp64(fmin(fmax(x, -1200.0), 709.0)); }
+// 1 / d for d >= 1, finite, to 2^-45 of it: the hardware's reciprocal (within
+// 2^-23) and one Newton step.
 __device__ __forceinline__ double recip64(double d) {
-  double y = __builtin_amdgcn_rcp(d);
-  y = __builtin_fma(__builtin_fma(-d, y, 1.0), y, y);
+  const double y = __builtin_amdgcn_rcp(d);
   return __builtin_fma(__builtin_fma(-d, y, 1.0), y, y);
+}
+// sigmoid(v), beyond 709 the value there
+__device__ __forceinline__ double sigmoid64(float v) {
+  return recip64(1.0 + exp64(-static_cast<double>(__builtin_amdgcn_fmed3f(v, -709.0f, 709.0f))));
 }
 
 // A candidate as one binary64 number: the value with its lowest 10 bits
@@ -191,6 +203,11 @@ __device__ __forceinline__ double select64(double (&c)[N], int k, int gl) {
 // wave; LDS works in order).
 __device__ __forceinline__ void wave_lds_fence() { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront"); }
 
+// one more value to (best, second)
+__device__ __forceinline__ void add_best(double& a1, double& a2, double v) {
+  a2 = fmax(a2, fmin(a1, v));
+  a1 = fmax(a1, v);
+}
 // (best, second) of two such pairs
 __device__ __forceinline__ void merge_best(double& a1, double& a2, double b1, double b2) {
   const double lo = fmin(a1, b1);
@@ -201,14 +218,14 @@ __device__ __forceinline__ void merge_best(double& a1, double& a2, double b1, do
 }  // namespace
 
 // Lanes of one token: 16 (four tokens a wave) or the wave; lane gl holds
-// experts gl, gl + L, ... (KPL of them).  BIAS: ranked by value, else by logit.
+// experts KPL gl .. KPL gl + KPL - 1.  BIAS: ranked by value, else by logit.
 // A masked expert's value is -inf from the point where it is known to be.
 template <int KPL, bool WAVE, bool BIAS>
 __global__ __launch_bounds__(256) void moe_route_scores_kernel(RouteParams q) {
   constexpr int L = WAVE ? kWave : 16;
   constexpr int kTok = 256 / L;
   constexpr double kNegInf64 = -__builtin_inf();
-  extern __shared__ double s_route[];  // [kTok][E + G] values and [kTok][kMaxRouteGroups] group scores (G > 1)
+  extern __shared__ double s_route[];  // [kTok][kMaxRouteGroups] group scores, then [kTok][E + L] values (G > 1)
   const int lane = threadIdx.x & (kWave - 1), gl = lane & (L - 1), lt = threadIdx.x / L;
   const int E = q.E, k = q.k, G = q.groups;
   const int64_t t_own = static_cast<int64_t>(blockIdx.x) * kTok + lt;
@@ -216,16 +233,14 @@ __global__ __launch_bounds__(256) void moe_route_scores_kernel(RouteParams q) {
   const bool softmax = q.score == MOE_SCORE_SOFTMAX;
 
   float v[KPL];
-  if (q.dtype == MOE_F32) load_row<F32, KPL, L>(v, q.logits, t * q.ld, gl, E);
-  else if (q.dtype == MOE_BF16) load_row<Bf16, KPL, L>(v, q.logits, t * q.ld, gl, E);
-  else load_row<F16, KPL, L>(v, q.logits, t * q.ld, gl, E);
+  const int first = KPL * gl;
+  if (q.dtype == MOE_F32) load_row<F32, KPL>(v, q.logits, t * q.ld, first, E);
+  else if (q.dtype == MOE_BF16) load_row<Bf16, KPL>(v, q.logits, t * q.ld, first, E);
+  else load_row<F16, KPL>(v, q.logits, t * q.ld, first, E);
   float b[BIAS ? KPL : 1];
-  if constexpr (BIAS) {
+  if constexpr (BIAS) load_row<F32, KPL>(b, q.bias, 0, first, E);
 #pragma unroll
-    for (int i = 0; i < KPL; ++i) b[i] = q.bias[min(gl + L * i, E - 1)];
-  }
-#pragma unroll
-  for (int i = 0; i < KPL; ++i) v[i] = gl + L * i < E ? clean(v[i]) : kNegInf;
+  for (int i = 0; i < KPL; ++i) v[i] = first + i < E ? clean(v[i]) : kNegInf;
   float m = 0.0f;  // the largest logit; 0 without any, where every exponential is 0
   if (softmax) {
     m = v[0];
@@ -243,7 +258,7 @@ __global__ __launch_bounds__(256) void moe_route_scores_kernel(RouteParams q) {
   if (BIAS || (G > 1 && q.group_best == 2)) {
     if (softmax) {
 #pragma unroll
-      for (int i = 0; i < KPL; ++i) val[i] = exp64(static_cast<double>(v[i]) - static_cast<double>(m));
+      for (int i = 0; i < KPL; ++i) val[i] = exp64(fmax(static_cast<double>(v[i]) - static_cast<double>(m), -1200.0));
       if (sums) {
 #pragma unroll
         for (int i = 0; i < KPL; ++i) z += val[i];
@@ -251,7 +266,7 @@ __global__ __launch_bounds__(256) void moe_route_scores_kernel(RouteParams q) {
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < KPL; ++i) val[i] = recip64(1.0 + exp64(-static_cast<double>(v[i])));
+      for (int i = 0; i < KPL; ++i) val[i] = sigmoid64(v[i]);
     }
     if constexpr (BIAS) {
       const double rz = softmax ? recip64(fmax(z, 1.0)) : 1.0;  // (z >= 1 where there is any expert)
@@ -276,45 +291,57 @@ __global__ __launch_bounds__(256) void moe_route_scores_kernel(RouteParams q) {
   }
 
   if (G > 1) {
-    // one double between groups, so that they start on different banks
     const int gs = E / G;
-    const auto group_of = [&](int e) { return static_cast<int>((static_cast<uint32_t>(e) * q.group_magic) >> 20); };
-    double* sv = s_route + static_cast<int64_t>(lt) * (E + G);
-    double* sg = s_route + static_cast<int64_t>(kTok) * (E + G) + lt * kMaxRouteGroups;
+    double* sg = s_route + lt * kMaxRouteGroups;
+    // Best two values of each group.  Where a group is a power of two of whole
+    // lanes they come from the lanes' registers; else from LDS, a lane's
+    // values one double further apart so that lanes start on different banks.
+    if (q.group_lanes > 0) {
+      double b1 = val[0], b2 = kNegInf64;
 #pragma unroll
-    for (int i = 0; i < KPL; ++i) {
-      const int e = gl + L * i;
-      if (e < E) sv[e + group_of(e)] = val[i];
-    }
-    wave_lds_fence();
-    // P lanes a group (a power of two), L / P groups at a time
-    int P = L;
-    while (P > 1 && P * G > L) P >>= 1;
-    const int sub = gl & (P - 1), per = L / P;
-    for (int g0 = 0; g0 < G; g0 += per) {
-      const int g = g0 + gl / P;
-      double b1 = kNegInf64, b2 = kNegInf64;
-      if (g < G) {
-        const double* own = sv + g * (gs + 1);
-        for (int j = sub; j < gs; j += 4 * P) {  // four reads in flight; past the end: not counted
-          double x[4];
-#pragma unroll
-          for (int u = 0; u < 4; ++u) x[u] = own[min(j + u * P, gs - 1)];
-#pragma unroll
-          for (int u = 0; u < 4; ++u) merge_best(b1, b2, j + u * P < gs ? x[u] : kNegInf64, kNegInf64);
-        }
-      }
-      for (int d = 1; d < P; d <<= 1) {
+      for (int i = 1; i < KPL; ++i) add_best(b1, b2, val[i]);
+      for (int d = 1; d < q.group_lanes; d <<= 1) {
         const double o1 = __shfl_xor(b1, d, kWave), o2 = __shfl_xor(b2, d, kWave);
         merge_best(b1, b2, o1, o2);
       }
-      if (g < G && sub == 0) sg[g] = q.group_best == 2 && b2 > kNegInf64 ? b1 + b2 : b1;
+      const int g = gl / q.group_lanes;
+      if (gl % q.group_lanes == 0 && g < G) sg[g] = q.group_best == 2 && b2 > kNegInf64 ? b1 + b2 : b1;
+    } else {
+      double* sv = s_route + kTok * kMaxRouteGroups + static_cast<int64_t>(lt) * (E + L);
+#pragma unroll
+      for (int i = 0; i < KPL; ++i)
+        if (first + i < E) sv[first + i + gl] = val[i];
+      wave_lds_fence();
+      // P lanes a group (a power of two), L / P groups at a time
+      int P = L;
+      while (P > 1 && P * G > L) P >>= 1;
+      const int sub = gl & (P - 1), per = L / P;
+      for (int g0 = 0; g0 < G; g0 += per) {
+        const int g = g0 + gl / P;
+        double b1 = kNegInf64, b2 = kNegInf64;
+        if (g < G) {
+          for (int j = sub; j < gs; j += 4 * P) {  // four reads in flight; past the end: not counted
+            double x[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              const int e = g * gs + min(j + u * P, gs - 1);
+              x[u] = sv[e + e / KPL];
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) add_best(b1, b2, j + u * P < gs ? x[u] : kNegInf64);
+          }
+        }
+        for (int d = 1; d < P; d <<= 1) {
+          const double o1 = __shfl_xor(b1, d, kWave), o2 = __shfl_xor(b2, d, kWave);
+          merge_best(b1, b2, o1, o2);
+        }
+        if (g < G && sub == 0) sg[g] = q.group_best == 2 && b2 > kNegInf64 ? b1 + b2 : b1;
+      }
     }
     wave_lds_fence();
-    uint64_t kept = 0;
-    for (int g0 = 0; g0 < G; g0 += L) {
-      const int g = g0 + gl;
-      const double mine = g < G ? sg[g] : kNegInf64;
+    // a group's rank among all; kept where it is below top_groups
+    const auto kept = [&](int g) {
+      const double mine = sg[g];
       int rank = 0;
       for (int h0 = 0; h0 < G; h0 += 4) {
         double o[4];
@@ -324,14 +351,28 @@ __global__ __launch_bounds__(256) void moe_route_scores_kernel(RouteParams q) {
         for (int u = 0; u < 4; ++u)
           rank += h0 + u < G && (o[u] > mine || (o[u] == mine && h0 + u < g)) ? 1 : 0;
       }
-      const uint64_t ballot = __ballot(g < G && rank < q.top_groups);
-      kept |= WAVE ? ballot : (((ballot >> (lane & 48)) & 0xFFFFull) << g0);
-    }
+      return rank < q.top_groups;
+    };
+    if (q.group_lanes > 0) {
+      const bool keep = kept(min(gl / q.group_lanes, G - 1));  // all of the lane's experts are in one group
 #pragma unroll
-    for (int i = 0; i < KPL; ++i) {
-      if (!((kept >> group_of(min(gl + L * i, E - 1))) & 1)) {
-        v[i] = kNegInf;
-        val[i] = kNegInf64;
+      for (int i = 0; i < KPL; ++i) {
+        v[i] = keep ? v[i] : kNegInf;
+        val[i] = keep ? val[i] : kNegInf64;
+      }
+    } else {
+      uint64_t mask = 0;
+      for (int g0 = 0; g0 < G; g0 += L) {
+        const int g = g0 + gl;
+        const uint64_t ballot = __ballot(g < G && kept(min(g, G - 1)));
+        mask |= WAVE ? ballot : (((ballot >> (lane & 48)) & 0xFFFFull) << g0);
+      }
+#pragma unroll
+      for (int i = 0; i < KPL; ++i) {
+        const int g = static_cast<int>((static_cast<uint32_t>(min(first + i, E - 1)) * q.group_magic) >> 20);  // e / gs
+        const bool keep = (mask >> g) & 1;
+        v[i] = keep ? v[i] : kNegInf;
+        val[i] = keep ? val[i] : kNegInf64;
       }
     }
   }
@@ -339,7 +380,7 @@ __global__ __launch_bounds__(256) void moe_route_scores_kernel(RouteParams q) {
   double cand[KPL];
 #pragma unroll
   for (int i = 0; i < KPL; ++i) {
-    const int e = gl + L * i;
+    const int e = first + i;
     const double rank = BIAS ? val[i] : static_cast<double>(v[i]);
     cand[i] = e < E ? candidate(v[i] > kNegInf ? rank : kMasked, e) : 2.0 * kMasked;
   }
@@ -360,7 +401,7 @@ __global__ __launch_bounds__(256) void moe_route_scores_kernel(RouteParams q) {
     ref = most > kNegInf ? (softmax ? most : fminf(most, 0.0f)) : 0.0f;
   }
   const double c = static_cast<double>(ref), l = static_cast<double>(lv);
-  double w = softmax ? exp64(l - c) : recip64(exp64(c) + exp64(c - l));
+  double w = softmax ? exp64_any(l - c) : recip64(exp64_any(c) + exp64_any(c - l));
   w = on ? w : 0.0;
   if (q.renormalize) {
     const double sum = row16_sum64(w);
@@ -375,12 +416,15 @@ __global__ __launch_bounds__(256) void moe_route_scores_kernel(RouteParams q) {
 }
 
 template <int KPL, bool WAVE>
-static void launch_scores(const RouteParams& q, hipStream_t s) {
-  constexpr int kTok = 256 / (WAVE ? kWave : 16);
-  const size_t lds = q.groups > 1 ? static_cast<size_t>(kTok) * (q.E + q.groups + kMaxRouteGroups) * sizeof(double) : 0;
+static void launch_scores(RouteParams q, hipStream_t s) {
+  constexpr int L = WAVE ? kWave : 16, kTok = 256 / L;
+  const int gs = q.E / q.groups, lanes = gs / KPL;
+  const bool whole = gs % KPL == 0 && (lanes & (lanes - 1)) == 0;
+  q.group_lanes = q.groups > 1 && whole ? lanes : 0;
+  const size_t doubles = q.groups <= 1 ? 0 : kTok * (kMaxRouteGroups + (whole ? 0 : q.E + L));
   const unsigned blocks = static_cast<unsigned>((static_cast<int64_t>(q.T) + kTok - 1) / kTok);
-  if (q.bias) moe_route_scores_kernel<KPL, WAVE, true><<<blocks, 256, lds, s>>>(q);
-  else moe_route_scores_kernel<KPL, WAVE, false><<<blocks, 256, lds, s>>>(q);
+  if (q.bias) moe_route_scores_kernel<KPL, WAVE, true><<<blocks, 256, doubles * sizeof(double), s>>>(q);
+  else moe_route_scores_kernel<KPL, WAVE, false><<<blocks, 256, doubles * sizeof(double), s>>>(q);
 }
 
 hipError_t launch_route_scores(const RouteParams& q, hipStream_t s) {
