@@ -172,7 +172,7 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void block_norm_kernel(Block
   __shared__ float s_red[4][kThreads / kWave];
   const int lt = threadIdx.x % TPR;
   const int cols = p.cols;
-  const int64_t row_own = static_cast<int64_t>(blockIdx.x) * (kThreads / TPR) + threadIdx.x / TPR;
+  const int64_t row_own = block_id() * (kThreads / TPR) + threadIdx.x / TPR;
   const bool active = row_own < p.rows;
   const int64_t row = active ? row_own : p.rows - 1;  // past the end: the last row again, not stored
 
@@ -225,8 +225,7 @@ template <typename T, typename R, bool VEC, int TPR, int NC>
 static void launch_norm_shape(const BlockNormParams& p, hipStream_t s) {
   constexpr int kThreads = TPR > 256 ? TPR : 256;
   constexpr int kRows = kThreads / TPR;
-  block_norm_kernel<T, R, VEC, TPR, NC>
-      <<<static_cast<unsigned>((p.rows + kRows - 1) / kRows), kThreads, 0, s>>>(p);
+  block_norm_kernel<T, R, VEC, TPR, NC><<<grid_of((p.rows + kRows - 1) / kRows), kThreads, 0, s>>>(p);
 }
 
 // One piece a thread up to 8192 columns: the shortest chain for a single row

@@ -74,7 +74,7 @@ __global__ __launch_bounds__(256) void int8_quantize_kernel(const void* __restri
                                                             int64_t ld_codes, float* __restrict__ scales) {
   __shared__ float s_am[4];
   const int lt = threadIdx.x % TPR;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * (256 / TPR) + threadIdx.x / TPR;
+  const int64_t row = block_id() * (256 / TPR) + threadIdx.x / TPR;
   if (row >= rows) return;  // whole waves, and no barrier where a block holds several rows
   const void* xrow = static_cast<const char*>(x) + row * ld * T::kBytes;
   const int cols16 = (cols + 15) / 16 * 16;
@@ -103,11 +103,12 @@ __global__ __launch_bounds__(256) void int8_quantize_kernel(const void* __restri
 
 // Longer rows: one block a row, two passes over it.
 template <typename T, bool VEC>
-__global__ __launch_bounds__(256) void int8_quantize_long_kernel(const void* __restrict__ x, int64_t cols,
-                                                                 int64_t ld, int8_t* __restrict__ codes,
+__global__ __launch_bounds__(256) void int8_quantize_long_kernel(const void* __restrict__ x, int64_t rows,
+                                                                 int64_t cols, int64_t ld, int8_t* __restrict__ codes,
                                                                  int64_t ld_codes, float* __restrict__ scales) {
   __shared__ float s_am[4];
-  const int64_t row = blockIdx.x;
+  const int64_t row = block_id();
+  if (row >= rows) return;
   const void* xrow = static_cast<const char*>(x) + row * ld * T::kBytes;
   const int64_t cols16 = (cols + 15) / 16 * 16;
   float am = 0.0f;
@@ -135,7 +136,7 @@ static void launch_quantize_width(const void* x, int64_t rows, int64_t cols, int
                                   int64_t ld_codes, float* scales, hipStream_t s) {
   const int64_t cols16 = (cols + 15) / 16 * 16;
   const int c = static_cast<int>(cols);
-  const unsigned g1 = static_cast<unsigned>(rows), g4 = static_cast<unsigned>((rows + 3) / 4);
+  const dim3 g1 = grid_of(rows), g4 = grid_of((rows + 3) / 4);
   if (cols16 <= 512)
     int8_quantize_kernel<T, VEC, 64, 1><<<g4, 256, 0, s>>>(x, rows, c, ld, codes, ld_codes, scales);
   else if (cols16 <= 1024)
@@ -149,7 +150,7 @@ static void launch_quantize_width(const void* x, int64_t rows, int64_t cols, int
   else if (cols16 <= 16384)
     int8_quantize_kernel<T, VEC, 256, 8><<<g1, 256, 0, s>>>(x, rows, c, ld, codes, ld_codes, scales);
   else
-    int8_quantize_long_kernel<T, VEC><<<g1, 256, 0, s>>>(x, cols, ld, codes, ld_codes, scales);
+    int8_quantize_long_kernel<T, VEC><<<g1, 256, 0, s>>>(x, rows, cols, ld, codes, ld_codes, scales);
 }
 
 template <typename T>
@@ -327,17 +328,20 @@ constexpr int kAhead = 3;
 template <int FN>
 __device__ __forceinline__ int channel_key(int row) { return (row & 3) | ((row / (4 * FN) & 1) << 2); }
 
-// Origin of this block's tile: each XCD (block % 8) takes a contiguous run of
+// Origin of this block's tile, false past the last: each XCD (block % 8) takes a contiguous run of
 // tiles, ordered in bands of 4 token tiles, so that the blocks that share an
 // L2 share operands.
 template <int BM, int BN>
-__device__ __forceinline__ void tile_origin(int mtiles, int ntiles, int& m0, int& n0) {
-  const int total = mtiles * ntiles, x = blockIdx.x & 7;
-  const int id = x * (total / 8) + min(x, total % 8) + (static_cast<int>(blockIdx.x) >> 3);
+__device__ __forceinline__ bool tile_origin(int mtiles, int ntiles, int& m0, int& n0) {
+  const int total = mtiles * ntiles;
+  if (block_id() >= total) return false;
+  const int block = static_cast<int>(block_id()), x = block & 7;
+  const int id = x * (total / 8) + min(x, total % 8) + (block >> 3);
   const int band = id / (4 * ntiles), in_band = id - band * 4 * ntiles;
   const int bh = min(4, mtiles - 4 * band);
   m0 = (4 * band + in_band % bh) * BM;
   n0 = in_band / bh * BN;
+  return true;
 }
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t code_rsrc(const int8_t* base, int64_t bytes) {
@@ -417,7 +421,7 @@ __attribute__((amdgpu_waves_per_eu(WM * WN / 4, WM * WN / 4))) void int8_tiled_k
   const int r = lane & 15, g = lane >> 4;
 
   int m0, n0;
-  tile_origin<BM, BN>(mtiles, ntiles, m0, n0);
+  if (!tile_origin<BM, BN>(mtiles, ntiles, m0, n0)) return;
 
   // copies: instruction u of this wave fills LDS rows 8 (wave + W u) .. + 7 of
   // the stage (token rows, then channel rows); lane l the piece l % 8 of row
@@ -599,13 +603,13 @@ __attribute__((amdgpu_waves_per_eu(WM * WN * KG * BLOCKS / 4))) void int8_ring_k
   constexpr int kPart = (BM + BN) * kStepBytes, kStage = KG * kPart;
   constexpr int NC = (BM + BN) / 8 / W, NCA = BM / 8 / W;
   static_assert((BM / 8) % W == 0 && (BN / 8) % W == 0 && (FN == 1 || FN % 2 == 0), "whole copies of each operand");
-  static_assert((KG - 1) * BM * BN * 4 <= NS * kStage, "the groups' sums fit the ring");
+  static_assert((NS - 2) * NC < 64 && (KG - 1) * BM * BN * 4 <= NS * kStage, "the groups' sums fit the ring");
   extern __shared__ __align__(1024) uint8_t s_tile[];  // NS * kStage
   const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave % W;
   const int kg = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / (kWave * W));
   const int r = lane & 15, g = lane >> 4;
   int m0, n0;
-  tile_origin<BM, BN>(mtiles, ntiles, m0, n0);
+  if (!tile_origin<BM, BN>(mtiles, ntiles, m0, n0)) return;
 
   // copies and fragments as in the kernel above
   const int K16 = (p.K + 15) / 16 * 16;
@@ -705,13 +709,12 @@ static hipError_t launch_ring(const Int8GemmParams& p, hipStream_t s) {
   constexpr int kLds = NS * KG * (BM + BN) * kStepBytes;
   static_assert(kLds * BLOCKS <= 160 * 1024, "the blocks of a CU share its LDS");
   const int64_t mt = (static_cast<int64_t>(p.M) + BM - 1) / BM, nt = (static_cast<int64_t>(p.N) + BN - 1) / BN;
-  if (mt * nt > UINT32_MAX / (64 * WM * WN * KG)) return hipErrorInvalidConfiguration;
+  if (mt * nt > INT32_MAX) return hipErrorInvalidConfiguration;
   const auto kernel = int8_ring_kernel<WM, WN, FM, FN, KG, NS, BLOCKS>;
   static std::atomic<uint64_t> lds_set{0};
   const hipError_t e = allow_lds(reinterpret_cast<const void*>(kernel), kLds, lds_set);
   if (e != hipSuccess) return e;
-  kernel<<<static_cast<unsigned>(mt * nt), 64 * WM * WN * KG, kLds, s>>>(p, static_cast<int>(mt),
-                                                                         static_cast<int>(nt));
+  kernel<<<grid_of(mt * nt), 64 * WM * WN * KG, kLds, s>>>(p, static_cast<int>(mt), static_cast<int>(nt));
   return hipGetLastError();
 }
 
@@ -720,11 +723,11 @@ static hipError_t launch_tiled(const Int8GemmParams& p, hipStream_t s) {
   constexpr int BM = 16 * FM * WM, BN = 16 * FN * WN;
   constexpr int kLds = 2 * (BM + BN) * kStepBytes;
   const int64_t mt = (static_cast<int64_t>(p.M) + BM - 1) / BM, nt = (static_cast<int64_t>(p.N) + BN - 1) / BN;
-  if (mt * nt > UINT32_MAX / (64 * WM * WN)) return hipErrorInvalidConfiguration;
+  if (mt * nt > INT32_MAX) return hipErrorInvalidConfiguration;
   static std::atomic<uint64_t> lds_set{0};
   const hipError_t e = allow_lds(reinterpret_cast<const void*>(int8_tiled_kernel<WM, WN, FM, FN>), kLds, lds_set);
   if (e != hipSuccess) return e;
-  int8_tiled_kernel<WM, WN, FM, FN><<<static_cast<unsigned>(mt * nt), 64 * WM * WN, kLds, s>>>(
+  int8_tiled_kernel<WM, WN, FM, FN><<<grid_of(mt * nt), 64 * WM * WN, kLds, s>>>(
       p, static_cast<int>(mt), static_cast<int>(nt));
   return hipGetLastError();
 }

@@ -141,6 +141,15 @@ hipError_t launch_quantize_experts(const float* w, int64_t experts, int64_t rows
                                    uint8_t* codes, uint8_t* scales, float* gs, uint32_t* amax_bits,
                                    hipStream_t s);
 
+// Grids of any number of blocks: a launch takes fewer than 2^32 threads in x,
+// so the blocks go on in y; block_id() numbers them, past the last one too.
+constexpr int64_t kGridX = int64_t(1) << 21;
+inline dim3 grid_of(int64_t blocks) {
+  return blocks <= kGridX ? dim3(static_cast<unsigned>(blocks))
+                          : dim3(static_cast<unsigned>(kGridX), static_cast<unsigned>((blocks + kGridX - 1) / kGridX));
+}
+__device__ __forceinline__ int64_t block_id() { return static_cast<int64_t>(blockIdx.y) * kGridX + blockIdx.x; }
+
 // route.hip: the router with scores, bias and groups.
 constexpr int kMaxRouteGroups = 64;
 constexpr int kRouteWaveTokens = 2048;  // batches of up to 256 experts that may take a whole wave a token

@@ -228,7 +228,7 @@ __global__ __launch_bounds__(256) void moe_route_scores_kernel(RouteParams q) {
   extern __shared__ double s_route[];  // [kTok][kMaxRouteGroups] group scores, then [kTok][E + L] values (G > 1)
   const int lane = threadIdx.x & (kWave - 1), gl = lane & (L - 1), lt = threadIdx.x / L;
   const int E = q.E, k = q.k, G = q.groups;
-  const int64_t t_own = static_cast<int64_t>(blockIdx.x) * kTok + lt;
+  const int64_t t_own = block_id() * kTok + lt;
   const int64_t t = min(t_own, static_cast<int64_t>(q.T) - 1);  // past the end: the last token again, not stored
   const bool softmax = q.score == MOE_SCORE_SOFTMAX;
 
@@ -422,7 +422,7 @@ static void launch_scores(RouteParams q, hipStream_t s) {
   const bool whole = gs % KPL == 0 && (lanes & (lanes - 1)) == 0;
   q.group_lanes = q.groups > 1 && whole ? lanes : 0;
   const size_t doubles = q.groups <= 1 ? 0 : kTok * (kMaxRouteGroups + (whole ? 0 : q.E + L));
-  const unsigned blocks = static_cast<unsigned>((static_cast<int64_t>(q.T) + kTok - 1) / kTok);
+  const dim3 blocks = grid_of((static_cast<int64_t>(q.T) + kTok - 1) / kTok);
   if (q.bias) moe_route_scores_kernel<KPL, WAVE, true><<<blocks, 256, doubles * sizeof(double), s>>>(q);
   else moe_route_scores_kernel<KPL, WAVE, false><<<blocks, 256, doubles * sizeof(double), s>>>(q);
 }

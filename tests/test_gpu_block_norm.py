@@ -176,3 +176,16 @@ def test_norm_graph_replay():
         torch.cuda.synchronize()
         want = binding.block_norm(r, y, before=n, after=n)
         assert torch.equal(ro, want[0]) and torch.equal(h, want[1])
+
+
+def test_norm_rows_past_one_grid_dimension():
+    """More rows than a launch has blocks in x (2^21 + 5 of 1100 columns)."""
+    T, H = (1 << 21) + 5, 1100
+    r = torch.zeros((T, H), dtype=BF16, device="cuda")
+    r[-7:] = _randn(7, H, seed=1, dtype=BF16)
+    n, ref = _make_norm(H, BF16, "rms", 0.0, False, 5)
+    _, h = binding.block_norm(r, before=n)
+    torch.cuda.synchronize()
+    _, _, rh, hs = ops_ref.block_norm(r[-7:], None, before=ref)
+    ops_ref.check_norm(h[-7:], rh, hs)
+    assert not h[:-7].any()

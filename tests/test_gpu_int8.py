@@ -227,3 +227,25 @@ def test_linear_graph_replay(M):
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, binding.int8_linear(x, wq, ws))
+
+
+def test_rows_past_one_grid_dimension():
+    """More rows than a launch has blocks in x: quantization and product of 2^21 + 3 and 2^25 + 40 tokens."""
+    x = torch.zeros(((1 << 21) + 3, 600), dtype=BF16, device="cuda")
+    x[-4:] = _randn(4, 600, seed=1, dtype=BF16)
+    q, s = binding.int8_quantize_per_token(x)
+    torch.cuda.synchronize()
+    rq, rs = ops_ref.int8_rows(x[-4:])
+    np.testing.assert_array_equal(q[-4:].cpu().numpy(), rq)
+    np.testing.assert_array_equal(s[-4:].cpu().numpy(), rs)
+    del x, q, s
+    M = (1 << 25) + 40
+    a = torch.zeros((M, 16), dtype=torch.int8, device="cuda")
+    a[-50:] = _codes(50, 16, 1)
+    sa = torch.ones(M, device="cuda")
+    b, sb = _codes(8, 16, 2), _scales(8, 4)
+    got = binding.int8_matmul(a, sa, b, sb, out_dtype=F32)
+    torch.cuda.synchronize()
+    ops_ref.check_product(got[-50:], *ops_ref.int8_product(a[-50:].cpu().numpy(), np.ones(50), b.cpu().numpy(),
+                                                           sb.cpu().numpy()))
+    assert not got[:-50].any()

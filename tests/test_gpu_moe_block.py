@@ -95,6 +95,32 @@ def test_router_bias_in_place_in_a_graph():
     layer.close()
 
 
+@pytest.mark.parametrize("T", [30, 300])
+def test_router_with_the_other_forwards(T):
+    """Handed-over codes give the forward's output bit for bit with a router too; W4A16 takes the same routing."""
+    L = synth.LAYERS[1]
+    x = to_device_bf16(synth.activations(1, T))
+    logits = torch.from_numpy(synth.router_logits(1, T)).cuda()
+    rule, b = dict(score="sigmoid", groups=4, top_groups=3, group_best=2, scale=2.0), _bias(L.E)
+    ids, w = binding.route(logits, L.k, binding.Router(**rule), bias=b)
+    layer = binding.MoeLayer(T, L.H, L.I, L.E, L.k, True)
+    layer.bind(gpu_weights(1))
+    layer.set_router(binding.Router(**rule), b)
+    out = layer.forward(x, logits)
+    again = layer.forward_quantized(*binding.quantize_per_token(x), logits)
+    torch.cuda.synchronize()
+    assert torch.equal(out, again)
+    layer.close()
+    wide = binding.MoeLayer(T, L.H, L.I, L.E, L.k, False, w4a16=True)
+    wide.bind(gpu_weights(1))
+    wide.set_router(binding.Router(**rule), b)
+    wide.forward(x, logits)
+    torch.cuda.synchronize()
+    assert torch.equal(wide.read_buffer("TOPK_IDS", torch.int32, (T, L.k)), ids)
+    assert torch.equal(wide.read_buffer("TOPK_W", torch.float32, (T, L.k)), w)
+    wide.close()
+
+
 def test_masked_tokens_and_shared_expert():
     """A token without any open expert gets only the shared expert's output."""
     L = synth.LAYERS[1]
@@ -155,6 +181,8 @@ def test_block(layer_id, T, residual):
     want, size, wh, whs = ops_ref.block_norm(r, y, before=refs[2], after=refs[1], gate=gate, out_scale=0.5)
     ops_ref.check_norm(out, want, size)
     ops_ref.check_norm(h2, wh, whs)
+    none = block.forward(r[:0], next_before=nxt)
+    assert none[0].shape == (0, L.H) and none[1].shape == (0, L.H)
     # the next block takes the h that this pass gave
     again = block.forward(out, h=h2)
     torch.cuda.synchronize()

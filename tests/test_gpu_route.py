@@ -164,3 +164,16 @@ def test_route_graph_replay(T):
         torch.cuda.synchronize()
         ids, w = binding.route(l, 8, r, bias=b)
         assert torch.equal(ids, out[0]) and torch.equal(w, out[1])
+
+
+def test_route_tokens_past_one_grid_dimension():
+    """More tokens than a launch has blocks in x of 16 tokens each (2^25 + 21)."""
+    T = (1 << 25) + 21
+    l = torch.zeros((T, 4), dtype=torch.bfloat16, device="cuda")
+    l[-30:] = _logits(30, 4, dtype=torch.bfloat16)
+    ids, w = binding.route(l, 2, binding.Router())
+    torch.cuda.synchronize()
+    rids, rw = ops_ref.route(l[-30:], 2)
+    np.testing.assert_array_equal(ids[-30:].cpu().numpy(), rids)
+    np.testing.assert_allclose(w[-30:].double().cpu().numpy(), rw, rtol=TOL_ROUNDED)
+    assert (w[:-30] == 0.5).all() and (ids[:-30, 1] == 1).all()
