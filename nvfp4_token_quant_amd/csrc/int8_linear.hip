@@ -238,11 +238,12 @@ __global__ __launch_bounds__(kTokenThreads) void int8_token_kernel(Int8GemmParam
   constexpr int W = kTokenThreads / kWave;
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
   const int last = (p.K - 1) / 16 * 16;
-  int n = static_cast<int>(blockIdx.x) * W + wave;
+  int64_t n = static_cast<int64_t>(blockIdx.x) * W + wave;
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * W;
   // a chunk: kDotLoads kilobytes of a channel's row (past its end the last
   // piece again, times zero)
-  const auto load = [&](i32x4 (&b)[kDotLoads], int ch, int c0) {
-    const int8_t* row = p.b + static_cast<int64_t>(min(ch, p.N - 1)) * p.ldb;
+  const auto load = [&](i32x4 (&b)[kDotLoads], int64_t ch, int c0) {
+    const int8_t* row = p.b + min(ch, static_cast<int64_t>(p.N) - 1) * p.ldb;
 #pragma unroll
     for (int i = 0; i < kDotLoads; ++i) b[i] = *reinterpret_cast<const i32x4*>(row + min(c0 + 1024 * i + 16 * lane, last));
   };
@@ -283,7 +284,7 @@ __global__ __launch_bounds__(kTokenThreads) void int8_token_kernel(Int8GemmParam
     }
   }
   lds_barrier();
-  for (; n < p.N; n += static_cast<int>(gridDim.x) * W) {
+  for (; n < p.N; n += stride) {
     int acc = 0;
     for (int c0 = 0; c0 < p.K; c0 += 1024 * kDotLoads) {
 #pragma unroll
@@ -296,10 +297,10 @@ __global__ __launch_bounds__(kTokenThreads) void int8_token_kernel(Int8GemmParam
       }
       // the next chunk, of this channel or the next
       if (c0 + 1024 * kDotLoads < p.K) load(b, n, c0 + 1024 * kDotLoads);
-      else if (n + static_cast<int>(gridDim.x) * W < p.N) load(b, n + static_cast<int>(gridDim.x) * W, 0);
+      else if (n + stride < p.N) load(b, n + stride, 0);
     }
     acc = wave_sum_i32(acc);
-    if (lane == 0) store_one(p, 0, n, acc, scale);
+    if (lane == 0) store_one(p, 0, static_cast<int>(n), acc, scale);
   }
 }
 
