@@ -116,7 +116,7 @@ typedef enum moe_score { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_scor
  *           lower index
  *   w_j  =  s_{id_j}, over the sum of the k with renormalize, times scale
  * The order is decided in binary64; values v within 2^-41 of their size may
- * count as equal.  An expert is masked where its logit or its bias is -inf or
+ * count as equal, sigmoid scores below e^-709 count as that.  An expert is masked where its logit or its bias is -inf or
  * NaN (+inf counts as FLT_MAX); masked experts and those of dropped groups
  * come after all others, lower index first, with weight 0, so a token always
  * has k different experts; a token without any has k weights of 0.  The

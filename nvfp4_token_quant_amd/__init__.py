@@ -5,4 +5,4 @@ C-ABI; ``nvfp4_token_quant_amd.binding`` marshals torch tensors into it.
 Importing this package loads nothing; the binding loads the library on first
 use and raises if it is missing.
 """
-__all__ = ["binding", "synth"]
+__all__ = ["binding", "block", "synth"]

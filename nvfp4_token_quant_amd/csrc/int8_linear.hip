@@ -67,7 +67,7 @@ __device__ __forceinline__ float amax8(const float (&f)[8]) {
 // TPR threads a row (64: four rows a block, 256: one), NC pieces of eight
 // columns a thread, held in registers between the maximum and the codes, so
 // that the row is read once.  The codes of a row end on a 16-byte piece,
-// filled with zeros.
+// filled with zeros.  Bound by memory: 16384 x 7168 bf16 67 us (5.3 TB/s).
 template <typename T, bool VEC, int TPR, int NC>
 __global__ __launch_bounds__(256) void int8_quantize_kernel(const void* __restrict__ x, int64_t rows, int cols,
                                                             int64_t ld, int8_t* __restrict__ codes,
@@ -312,11 +312,23 @@ __global__ __launch_bounds__(kTokenThreads) void int8_token_kernel(Int8GemmParam
 // Copies go from global memory straight to LDS, one instruction for 8 rows of
 // 128 bytes (whole lines).  The 16-byte pieces of a row are permuted by a key
 // of the row, so that the eight lanes of an LDS read that take the same piece
-// of different rows touch different banks.  Token fragments are read from LDS
-// kAhead ahead of their MFMAs, across the step's barrier too: the last kAhead
-// fragments of a step are in registers when its buffer is handed back, so
-// their MFMAs run while the next step's first fragments are read and the
-// copies of the step after it start, a whole step before they are needed.
+// of different rows touch different banks (no conflict counted; a 1 KB read
+// takes 4 cycles).  Token fragments are read from LDS kAhead ahead of their
+// MFMAs, across the step's barrier too: the last kAhead fragments of a step are
+// in registers when its buffer is handed back.  A buffer comes back in two
+// parts: behind a barrier in the middle of the step the channel rows and the
+// token rows of the first four groups, which everybody has read by then, and
+// behind its end the rest, so that copies start one and a half steps and one
+// step before they are needed (one buffer at a time, at the end of the step:
+// 8192^3 of zeros 412 us, in two parts 370).
+//
+// What bounds it: on operands like activations and weights the chip's power.
+// 8192^3 takes 449 us (2450 TOP/s; of zeros 370, without the copies 384), 4096 x
+// 7168 x 7168 186 to 212 us from one card to another (448 tiles on 256 CUs), a
+// library's product alone, measured beside it, 462 and 195 to 236.  Four waves of
+// twice the tile each (128 x 128) took 576 us of zeros: one wave a SIMD hides
+// nothing.  Bands of 4 token tiles an XCD: 1% over 8; tiles in block order
+// instead: 5% slower.
 //
 // Fragment f of a wave's channels holds channels 4 FN (r / 4) + 4 f + r % 4
 // (r its row), so a lane ends with 4 FN consecutive channels of a token and
@@ -492,8 +504,12 @@ __attribute__((amdgpu_waves_per_eu(WM * WN / 4, WM * WN / 4))) void int8_tiled_k
   const auto mma = [&](int i) {
     const int m = group_of(i);
 #pragma unroll
-    for (int f = 0; f < FN; ++f)
+    for (int f0 = 0; f0 < FN; ++f0) {
+      // there and back, so that two MFMAs in a row always share an operand
+      // (the chip's power bounds this kernel: 8192^3 454 -> 449 us)
+      const int f = i % 2 ? FN - 1 - f0 : f0;
       acc[f][m] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[half_of(i)][f], x[i % (kAhead + 1)], acc[f][m], 0, 0, 0);
+    }
   };
   static_assert(NI == 16 && NI % (kAhead + 1) == 0 && kAhead <= 4, "the window's slots repeat every step");
   // Copies of the rows that are read by the middle of a step (all channel

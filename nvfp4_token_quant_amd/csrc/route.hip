@@ -19,10 +19,13 @@
 //
 // Work.  The bytes are T * E logits, read once; what bounds the kernel is
 // vector work: with a bias (or groups by two values) one binary64
-// exponential for every logit (about the issue rate of binary32 on this
-// chip, two registers a value), the sort of each lane's keys, and k rounds of
-// a maximum over a token's lanes.  16 lanes share a token (four tokens a
-// wave) or, for few tokens or more than 256 experts, the whole wave.
+// exponential for every logit, the sort of each lane's candidates, and k
+// rounds of a maximum over a token's lanes.  16 lanes share a token (four
+// tokens a wave) or, for few tokens or more than 256 experts, the whole wave; a
+// lane's experts are consecutive, so that groups of whole lanes are reduced in
+// registers (through LDS: 2.7 us more of the 18.5).  16384 tokens of 256 experts
+// take 15.7 us with bias and groups (1960 vector instructions for four tokens),
+// 7.9 without (floor of the bytes: 3.7); one token of 128 experts 3.0 us.
 #include "common.hpp"
 #include "dtype.hpp"
 #include "kernels.hpp"
