@@ -391,20 +391,23 @@ def block_norm(residual, y=None, before=None, after=None, gate=None, gate_sigmoi
     is of its dtype); y [T, H] bf16, f16 or f32; gate None, [H] for each
     channel, [T, 1] for each token or [T, H].  residual_out / h_out: outputs
     to write, residual and y themselves allowed."""
-    (T, H), device = _matrix(residual, "residual")
+    at = _matrix(residual, "residual")
+    (T, H), device = at
     if _elsewhere(device, stream):
         with _switched(device, stream):
             return block_norm(residual, y, before, after, gate, gate_sigmoid, res_scale, out_scale, residual_out,
                               h_out)
+    rdtype = residual.dtype
     yp = ld_y = gp = ld_gate = gate_cols = 0
     if y is not None:
-        _matrix(y, "y")
-        _same(y, "y", residual.shape, device)
-        dtype, yp, ld_y = y.dtype, y.data_ptr(), _ld(y)
+        if _matrix(y, "y") != at:
+            raise ValueError(f"y must be {(T, H)} on {device}, got {tuple(y.shape)} on {y.device}")
+        dtype, yp = y.dtype, y.data_ptr()
+        ld_y = y.stride(0) if T > 1 else H
     else:
-        dtype = h_out.dtype if h_out is not None else residual.dtype
+        dtype = h_out.dtype if h_out is not None else rdtype
     if gate is not None:
-        if not isinstance(gate, torch.Tensor) or gate.device != device or gate.dtype != dtype:
+        if not isinstance(gate, torch.Tensor) or gate.device != device or gate.dtype is not dtype:
             raise ValueError(f"gate must be {dtype} on {device}")
         if gate.dim() == 1:
             gp, gate_cols = _vector(gate, "gate", H, dtype, device), H
@@ -413,24 +416,33 @@ def block_norm(residual, y=None, before=None, after=None, gate=None, gate_sigmoi
             if gate.shape[0] != T or gate.shape[1] not in (1, H):
                 raise ValueError(f"gate must be [{H}], [{T}, 1] or [{T}, {H}], got {tuple(gate.shape)}")
             gp, gate_cols, ld_gate = gate.data_ptr(), gate.shape[1], _ld(gate)
-    for t, name, want in ((residual_out, "residual_out", residual.dtype), (h_out, "h_out", dtype)):
-        if t is not None:
-            _matrix(t, name, (want,))
-            _same(t, name, residual.shape, device)
-    if h_out is not None and before is None:
-        raise ValueError("h_out needs a norm (before)")
     na = after.desc(H, dtype, device, "after") if after is not None else 0
     nb = before.desc(H, dtype, device, "before") if before is not None else 0
     r, h = residual_out, h_out
-    if r is None and (y is not None or before is None or res_scale != 1.0):
-        r = _empty(residual, T, H, residual.dtype)
-    if h is None and before is not None:
+    rp = hp = 0
+    ld_r = ld_h = H
+    if r is not None:
+        if _matrix(r, "residual_out", (rdtype,)) != at:
+            raise ValueError(f"residual_out must be {(T, H)} on {device}, got {tuple(r.shape)} on {r.device}")
+        ld_r = _ld(r)
+    elif y is not None or before is None or res_scale != 1.0:
+        r = _empty(residual, T, H, rdtype)
+    if r is not None:
+        rp = r.data_ptr()
+    if h is not None:
+        if before is None:
+            raise ValueError("h_out needs a norm (before)")
+        if _matrix(h, "h_out", (dtype,)) != at:
+            raise ValueError(f"h_out must be {(T, H)} on {device}, got {tuple(h.shape)} on {h.device}")
+        ld_h = _ld(h)
+    elif before is not None:
         h = _empty(residual if y is None else y, T, H, dtype)
+    if h is not None:
+        hp = h.data_ptr()
     _check((_lib or lib()).moe_block_norm(_BLOCK_NORM.pack(
-        T, H, DTYPES[dtype], DTYPES[residual.dtype], residual.data_ptr(), _ld(residual), yp, ld_y, gp, ld_gate,
-        gate_cols, 1 if gate_sigmoid else 0, res_scale, out_scale, na, nb,
-        r.data_ptr() if r is not None else 0, _ld(r) if r is not None else 0,
-        h.data_ptr() if h is not None else 0, _ld(h) if h is not None else 0), _raw_stream(device.index)))
+        T, H, DTYPES[dtype], DTYPES[rdtype], residual.data_ptr(), residual.stride(0) if T > 1 else H, yp, ld_y, gp,
+        ld_gate, gate_cols, 1 if gate_sigmoid else 0, res_scale, out_scale, na, nb, rp, ld_r, hp, ld_h),
+        _raw_stream(device.index)))
     return (residual if r is None else r), h
 
 
@@ -472,8 +484,9 @@ def int8_matmul(codes, scale, w_codes, w_scale, bias=None, out_dtype=torch.bfloa
     if _elsewhere(device, stream):
         with _switched(device, stream):
             return int8_matmul(codes, scale, w_codes, w_scale, bias, out_dtype, out)
-    (N, _), _ = _matrix(w_codes, "w_codes", _CODES)
-    _same(w_codes, "w_codes", (N, K), device)
+    (N, Kw), where = _matrix(w_codes, "w_codes", _CODES)
+    if Kw != K or where != device:
+        raise ValueError(f"w_codes must be {(N, K)} on {device}, got {(N, Kw)} on {where}")
     sa, sb = _vector(scale, "scale", M, torch.float32, device), _vector(w_scale, "w_scale", N, torch.float32, device)
     b = _vector(bias, "bias", N, torch.float32, device) if bias is not None else None
     lda, ldb = _ld16(codes, "codes"), _ld16(w_codes, "w_codes")
@@ -497,8 +510,9 @@ def int8_linear(x, w_codes, w_scale, bias=None, out_dtype=None, out=None, stream
     if _elsewhere(device, stream):
         with _switched(device, stream):
             return int8_linear(x, w_codes, w_scale, bias, out_dtype, out)
-    (N, _), _ = _matrix(w_codes, "w_codes", _CODES)
-    _same(w_codes, "w_codes", (N, K), device)
+    (N, Kw), where = _matrix(w_codes, "w_codes", _CODES)
+    if Kw != K or where != device:
+        raise ValueError(f"w_codes must be {(N, K)} on {device}, got {(N, Kw)} on {where}")
     sb = _vector(w_scale, "w_scale", N, torch.float32, device)
     b = _vector(bias, "bias", N, torch.float32, device) if bias is not None else None
     ldb = _ld16(w_codes, "w_codes")
