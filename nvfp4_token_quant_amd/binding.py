@@ -10,7 +10,6 @@ from __future__ import annotations
 import ctypes
 import os
 import re
-import struct
 
 import torch
 
@@ -34,7 +33,6 @@ BUF = dict(XQ_CODES=0, XQ_SCALES=1, XQ_GSCALE=2, TOPK_IDS=3, TOPK_W=4, COUNTS=5,
            PERM=7, INV=8, ACT=9, A2_CODES=10, A2_SCALES=11, A2_GSCALE=12, A2_16=13)
 
 
-DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 SCORES = {"softmax": 0, "sigmoid": 1}
 NORM_KINDS = {"rms": 0, "layer": 1}
 
@@ -253,64 +251,32 @@ def token_ceiling(max_prefill, piecewise_max, graph_max_bs, spec_draft_tokens) -
 #
 # Each works on its tensors' device, which need not be the current one, on
 # `stream` (default: that device's current stream).  Tensors a call makes
-# belong to the stream it ran on.  These calls serve single tokens, whose
-# kernels take a few microseconds: what surrounds the launch is kept short.
+# belong to the stream it ran on.  The calls serve single tokens, whose kernels
+# take a few microseconds, so their checks, the allocation of their results and
+# the launch are native code (csrc/torch_calls.cpp).
 
-_raw_stream = torch._C._cuda_getCurrentRawStream  # device index -> handle of its current stream
-_current = torch._C._cuda_getDevice
-
-
-def _elsewhere(device, stream):
-    """Whether a call has to switch to another device or stream."""
-    return stream is not None or device.index != _current()
+_calls = None
 
 
-def _switched(device, stream):
-    """The context in which `stream` (or the device's current stream) is the current one."""
-    if stream is None:
-        return torch.cuda.device(device)
-    if stream.device != device:
-        raise ValueError(f"stream of {stream.device}, tensors on {device}")
+def calls():
+    """The module of the operators' native calls."""
+    global _calls
+    if _calls is None:
+        try:
+            from . import _calls as module
+        except ImportError as e:
+            raise ImportError(f"operators' calls not built: {e} "
+                              "(run __graft_entry__.build() or nvfp4_token_quant_amd/build.py)") from e
+        module.setup(Nvfp4Error, torch._C._cuda_getCurrentRawStream)
+        _calls = module
+    return _calls
+
+
+def _on(stream, t):
+    """The context in which `stream`, which has to be of t's device, is the current one."""
+    if not isinstance(t, torch.Tensor) or stream.device != t.device:
+        raise ValueError(f"stream of {stream.device}, tensors on {getattr(t, 'device', None)}")
     return torch.cuda.stream(stream)
-
-
-def _matrix(t, name, dtypes=DTYPES):
-    """Checks a matrix of unit column stride; its shape and device."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype not in dtypes:
-        raise ValueError(f"{name} must be one of {[str(d) for d in dtypes]}, got {t.dtype}")
-    if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1):
-        raise ValueError(f"{name} must be a matrix with unit column stride")
-    return t.shape, t.device
-
-
-def _vector(t, name, n, dtype, device):
-    """Checks a contiguous vector of n values; its address."""
-    if not isinstance(t, torch.Tensor) or t.device != device:
-        raise ValueError(f"{name} must be a tensor on {device}")
-    if t.dtype is not dtype or t.shape != (n,) or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {n} values, got {t.dtype} {tuple(t.shape)}")
-    return t.data_ptr()
-
-
-def _same(t, name, shape, device):
-    if t.device != device or t.shape != shape:
-        raise ValueError(f"{name} must be {tuple(shape)} on {device}, got {tuple(t.shape)} on {t.device}")
-
-
-def _ld(t):
-    """Elements between two rows (a single row's stride means nothing)."""
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
-
-
-def _ld16(t, name):
-    """The same for 8-bit codes, whose rows start at multiples of 16 bytes."""
-    if t.shape[0] <= 1:
-        return (t.shape[1] + 15) // 16 * 16
-    if t.stride(0) % 16 != 0:
-        raise ValueError(f"{name}: rows must start at multiples of 16 bytes, as int8_quantize_per_token lays them out")
-    return t.stride(0)
 
 
 class Router:
@@ -328,25 +294,10 @@ class Router:
 def route(logits, top_k, router, bias=None, out=None, stream=None):
     """logits [T, E] (bf16, f16 or f32; the row stride may exceed E), bias f32
     [E] -> (ids int32 [T, k], weights f32 [T, k]), into `out` if given."""
-    (T, E), device = _matrix(logits, "logits")
-    if _elsewhere(device, stream):
-        with _switched(device, stream):
+    if stream is not None:
+        with _on(stream, logits):
             return route(logits, top_k, router, bias, out)
-    b = _vector(bias, "bias", E, torch.float32, device) if bias is not None else None
-    if out is None:
-        shape = (T, max(top_k, 0))
-        ids, w = torch.empty(shape, dtype=torch.int32, device=device), torch.empty(shape, device=device,
-                                                                                   dtype=torch.float32)
-    else:
-        ids, w = out
-        for t, name, dtype in ((ids, "ids", torch.int32), (w, "weights", torch.float32)):
-            _require(t, dtype, name)
-            _same(t, name, (T, top_k), device)
-            if not t.is_contiguous():
-                raise ValueError(f"{name} must be contiguous")
-    _check((_lib or lib()).moe_route(router.desc, logits.data_ptr(), DTYPES[logits.dtype], T, E, _ld(logits), top_k, b,
-                           ids.data_ptr(), w.data_ptr(), _raw_stream(device.index)))
-    return ids, w
+    return (_calls or calls()).route(logits, top_k, router, bias, out if out is None else tuple(out))
 
 
 class Norm:
@@ -357,28 +308,7 @@ class Norm:
         if kind not in NORM_KINDS:
             raise ValueError("kind must be 'rms' or 'layer'")
         self.weight, self.bias = weight, bias
-        self._desc = MoeNorm(NORM_KINDS[kind], eps, offset, None, None)
-        self._address = ctypes.addressof(self._desc)
-
-    def desc(self, cols, dtype, device, name):
-        """The address of this norm's moe_norm, of the weight and bias it has now."""
-        w, b, d = self.weight, self.bias, self._desc
-        d.weight = _vector(w, f"{name} weight", cols, dtype, device) if w is not None else None
-        d.bias = _vector(b, f"{name} bias", cols, dtype, device) if b is not None else None
-        return self._address
-
-
-# moe_block_norm_args as bytes (the layout of MoeBlockNormArgs, natively
-# aligned; quicker to fill)
-_BLOCK_NORM = struct.Struct("@qqiiPqPqPqqiffPPPqPq")
-assert _BLOCK_NORM.size == ctypes.sizeof(MoeBlockNormArgs)
-
-
-def _empty(like, rows, cols, dtype):
-    """A contiguous [rows, cols] of `dtype` beside `like`, of which it has the shape."""
-    if like.dtype is dtype and like.is_contiguous():
-        return torch.empty_like(like)
-    return torch.empty((rows, cols), dtype=dtype, device=like.device)
+        self.desc = MoeNorm(NORM_KINDS[kind], eps, offset, None, None)  # each call adds the addresses it needs
 
 
 def block_norm(residual, y=None, before=None, after=None, gate=None, gate_sigmoid=False, res_scale=1.0,
@@ -391,59 +321,12 @@ def block_norm(residual, y=None, before=None, after=None, gate=None, gate_sigmoi
     is of its dtype); y [T, H] bf16, f16 or f32; gate None, [H] for each
     channel, [T, 1] for each token or [T, H].  residual_out / h_out: outputs
     to write, residual and y themselves allowed."""
-    at = _matrix(residual, "residual")
-    (T, H), device = at
-    if _elsewhere(device, stream):
-        with _switched(device, stream):
+    if stream is not None:
+        with _on(stream, residual):
             return block_norm(residual, y, before, after, gate, gate_sigmoid, res_scale, out_scale, residual_out,
                               h_out)
-    rdtype = residual.dtype
-    yp = ld_y = gp = ld_gate = gate_cols = 0
-    if y is not None:
-        if _matrix(y, "y") != at:
-            raise ValueError(f"y must be {(T, H)} on {device}, got {tuple(y.shape)} on {y.device}")
-        dtype, yp = y.dtype, y.data_ptr()
-        ld_y = y.stride(0) if T > 1 else H
-    else:
-        dtype = h_out.dtype if h_out is not None else rdtype
-    if gate is not None:
-        if not isinstance(gate, torch.Tensor) or gate.device != device or gate.dtype is not dtype:
-            raise ValueError(f"gate must be {dtype} on {device}")
-        if gate.dim() == 1:
-            gp, gate_cols = _vector(gate, "gate", H, dtype, device), H
-        else:
-            _matrix(gate, "gate")
-            if gate.shape[0] != T or gate.shape[1] not in (1, H):
-                raise ValueError(f"gate must be [{H}], [{T}, 1] or [{T}, {H}], got {tuple(gate.shape)}")
-            gp, gate_cols, ld_gate = gate.data_ptr(), gate.shape[1], _ld(gate)
-    na = after.desc(H, dtype, device, "after") if after is not None else 0
-    nb = before.desc(H, dtype, device, "before") if before is not None else 0
-    r, h = residual_out, h_out
-    rp = hp = 0
-    ld_r = ld_h = H
-    if r is not None:
-        if _matrix(r, "residual_out", (rdtype,)) != at:
-            raise ValueError(f"residual_out must be {(T, H)} on {device}, got {tuple(r.shape)} on {r.device}")
-        ld_r = _ld(r)
-    elif y is not None or before is None or res_scale != 1.0:
-        r = _empty(residual, T, H, rdtype)
-    if r is not None:
-        rp = r.data_ptr()
-    if h is not None:
-        if before is None:
-            raise ValueError("h_out needs a norm (before)")
-        if _matrix(h, "h_out", (dtype,)) != at:
-            raise ValueError(f"h_out must be {(T, H)} on {device}, got {tuple(h.shape)} on {h.device}")
-        ld_h = _ld(h)
-    elif before is not None:
-        h = _empty(residual if y is None else y, T, H, dtype)
-    if h is not None:
-        hp = h.data_ptr()
-    _check((_lib or lib()).moe_block_norm(_BLOCK_NORM.pack(
-        T, H, DTYPES[dtype], DTYPES[rdtype], residual.data_ptr(), residual.stride(0) if T > 1 else H, yp, ld_y, gp,
-        ld_gate, gate_cols, 1 if gate_sigmoid else 0, res_scale, out_scale, na, nb, rp, ld_r, hp, ld_h),
-        _raw_stream(device.index)))
-    return (residual if r is None else r), h
+    return (_calls or calls()).block_norm(residual, y, before, after, gate, gate_sigmoid, res_scale, out_scale,
+                                          residual_out, h_out)
 
 
 def int8_quantize_per_token(x, stream=None):
@@ -451,54 +334,20 @@ def int8_quantize_per_token(x, stream=None):
     (codes int8 [rows, cols], scale f32 [rows]).  The codes' rows start at
     multiples of 16 bytes, as int8_matmul takes them.  Weights [channels, in]
     give one scale a channel."""
-    (rows, cols), device = _matrix(x, "x")
-    if _elsewhere(device, stream):
-        with _switched(device, stream):
+    if stream is not None:
+        with _on(stream, x):
             return int8_quantize_per_token(x)
-    ld = (cols + 15) // 16 * 16
-    codes = torch.empty((rows, ld), dtype=torch.int8, device=device)
-    scale = torch.empty((rows,), dtype=torch.float32, device=device)
-    _check((_lib or lib()).int8_quantize_per_token(x.data_ptr(), DTYPES[x.dtype], rows, cols, _ld(x), codes.data_ptr(), ld,
-                                         scale.data_ptr(), _raw_stream(device.index)))
-    return (codes[:, :cols] if ld != cols else codes), scale
-
-
-_CODES = (torch.int8,)
-
-
-def _product_out(out, out_dtype, M, N, device):
-    if out is None:
-        if out_dtype not in DTYPES:
-            raise ValueError(f"out_dtype must be one of {[str(d) for d in DTYPES]}, got {out_dtype}")
-        return torch.empty((M, N), dtype=out_dtype, device=device)
-    _matrix(out, "out")
-    _same(out, "out", (M, N), device)
-    return out
+    return (_calls or calls()).quantize(x)
 
 
 def int8_matmul(codes, scale, w_codes, w_scale, bias=None, out_dtype=torch.bfloat16, out=None, stream=None):
     """codes int8 [M, K] and scale f32 [M] of the tokens, w_codes int8 [N, K]
     and w_scale f32 [N] of the channels, bias f32 [N] ->
     scale[m] * w_scale[n] * sum_k codes[m, k] * w_codes[n, k] + bias[n], [M, N]."""
-    (M, K), device = _matrix(codes, "codes", _CODES)
-    if _elsewhere(device, stream):
-        with _switched(device, stream):
+    if stream is not None:
+        with _on(stream, codes):
             return int8_matmul(codes, scale, w_codes, w_scale, bias, out_dtype, out)
-    (N, Kw), where = _matrix(w_codes, "w_codes", _CODES)
-    if Kw != K or where != device:
-        raise ValueError(f"w_codes must be {(N, K)} on {device}, got {(N, Kw)} on {where}")
-    sa, sb = _vector(scale, "scale", M, torch.float32, device), _vector(w_scale, "w_scale", N, torch.float32, device)
-    b = _vector(bias, "bias", N, torch.float32, device) if bias is not None else None
-    lda, ldb = _ld16(codes, "codes"), _ld16(w_codes, "w_codes")
-    out = _product_out(out, out_dtype, M, N, device)
-    _check((_lib or lib()).int8_matmul(codes.data_ptr(), lda, sa, w_codes.data_ptr(), ldb, sb, b, M, N, K, out.data_ptr(),
-                             DTYPES[out.dtype], _ld(out), _raw_stream(device.index)))
-    return out
-
-
-def _linear_workspace(M, K):
-    """int8_linear_workspace (a single token of up to 32768 columns needs none)."""
-    return 0 if M == 1 and K <= 32768 else M * ((K + 15) // 16 * 16 + 4)
+    return (_calls or calls()).matmul(codes, scale, w_codes, w_scale, bias, out_dtype, out)
 
 
 def int8_linear(x, w_codes, w_scale, bias=None, out_dtype=None, out=None, stream=None):
@@ -506,23 +355,10 @@ def int8_linear(x, w_codes, w_scale, bias=None, out_dtype=None, out=None, stream
     channel-quantized weights, as int8_quantize_per_token and int8_matmul
     would; the result is of x's dtype unless out_dtype (or out) says
     otherwise."""
-    (M, K), device = _matrix(x, "x")
-    if _elsewhere(device, stream):
-        with _switched(device, stream):
+    if stream is not None:
+        with _on(stream, x):
             return int8_linear(x, w_codes, w_scale, bias, out_dtype, out)
-    (N, Kw), where = _matrix(w_codes, "w_codes", _CODES)
-    if Kw != K or where != device:
-        raise ValueError(f"w_codes must be {(N, K)} on {device}, got {(N, Kw)} on {where}")
-    sb = _vector(w_scale, "w_scale", N, torch.float32, device)
-    b = _vector(bias, "bias", N, torch.float32, device) if bias is not None else None
-    ldb = _ld16(w_codes, "w_codes")
-    out = _product_out(out, out_dtype or x.dtype, M, N, device)
-    work = _linear_workspace(M, K)
-    scratch = torch.empty((work,), dtype=torch.uint8, device=device) if work else None
-    _check((_lib or lib()).int8_linear(x.data_ptr(), DTYPES[x.dtype], _ld(x), w_codes.data_ptr(), ldb, sb, b, M, N, K,
-                             scratch.data_ptr() if work else None, work, out.data_ptr(), DTYPES[out.dtype], _ld(out),
-                             _raw_stream(device.index)))
-    return out
+    return (_calls or calls()).linear(x, w_codes, w_scale, bias, out_dtype, out)
 
 
 # --- synthetic weights (input generation) --------------------------------------

@@ -133,6 +133,14 @@ def test_route_empty_and_outputs():
         binding.route(l, 2, binding.Router(), bias=torch.zeros(15, device="cuda"))
     with pytest.raises(ValueError):
         binding.route(l.t(), 2, binding.Router())
+    with pytest.raises(TypeError):
+        binding.route(l, 2, binding.Norm())
+    with pytest.raises(TypeError):
+        binding.block_norm(l, before=binding.Router())
+    for k in (0, -1, 17, 1 << 40):
+        with pytest.raises(binding.Nvfp4Error) as e:
+            binding.route(l, k, binding.Router())
+        assert e.value.status == "NVFP4_ERR_INVALID_ARG"
 
 
 def test_route_far_offsets():
