@@ -108,15 +108,16 @@ __device__ __forceinline__ void store8_any(void* p, int64_t i, const float (&f)[
   __builtin_memcpy(static_cast<char*>(p) + i * T::kBytes, &r, sizeof(r));
 }
 
-// Four elements at once (8-byte aligned; binary32: 16-byte).
+// Four elements at any address.
 template <typename T>
-__device__ __forceinline__ void store4(void* p, int64_t i, const float (&f)[4]) {
+__device__ __forceinline__ void store4_any(void* p, int64_t i, const float (&f)[4]) {
   char* d = static_cast<char*>(p) + i * T::kBytes;
-  if constexpr (T::kBytes == 4)
-    *reinterpret_cast<u32x4*>(d) = u32x4{__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
-                                         __float_as_uint(f[3])};
-  else
-    *reinterpret_cast<u32x2*>(d) = u32x2{T::bits(f[0]) | (T::bits(f[1]) << 16), T::bits(f[2]) | (T::bits(f[3]) << 16)};
+  if constexpr (T::kBytes == 4) {
+    __builtin_memcpy(d, f, sizeof(f));
+  } else {
+    const u32x2 w = {T::bits(f[0]) | (T::bits(f[1]) << 16), T::bits(f[2]) | (T::bits(f[3]) << 16)};
+    __builtin_memcpy(d, &w, sizeof(w));
+  }
 }
 
 }  // namespace nvfp4

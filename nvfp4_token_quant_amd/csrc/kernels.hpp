@@ -203,7 +203,6 @@ struct Int8GemmParams {
   void* out;          // [M, ldo] of dtype
   int64_t lda, ldb, ldo;
   int M, N, K, dtype;
-  int vec_out;  // 1: rows of out start at multiples of 16 bytes
 };
 hipError_t launch_int8_matmul(const Int8GemmParams& p, hipStream_t s);
 // One token (M = 1, K <= kLinearTokenMaxK) from its unquantized row x; p.a and

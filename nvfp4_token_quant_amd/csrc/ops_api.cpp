@@ -124,7 +124,6 @@ Int8GemmParams gemm_params(const void* a_dev, int64_t lda, const float* scale_a_
   p.N = static_cast<int>(N);
   p.K = static_cast<int>(K);
   p.dtype = dtype;
-  p.vec_out = row_vectors(out_dev, ldo, dtype_bytes(dtype)) ? 1 : 0;
   return p;
 }
 
