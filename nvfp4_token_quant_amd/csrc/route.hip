@@ -125,12 +125,34 @@ __device__ __forceinline__ double row16_sum64(double v) {
   v += dpp_f64<kDppRor8>(v);
   return v;
 }
-template <bool WAVE>
+// The lanes of a token: a 16-lane row, or the wave, whose rows meet by register
+// swaps (short; the vector ALU does them) or by shuffles through LDS (long;
+// they leave it free).
+enum class Lanes { kRow, kSwap, kShuffle };
+
+// A lane's value and its partner's, 16 or 32 lanes away, in either order.
+template <Lanes LANES, int PAIR>
+__device__ __forceinline__ void lane_pair64(double v, double& a, double& b) {
+  if constexpr (LANES == Lanes::kSwap) {
+    const uint64_t u = static_cast<uint64_t>(__double_as_longlong(v));
+    uint32_t al, bl, ah, bh;
+    lane_pair<PAIR>(static_cast<uint32_t>(u), al, bl);
+    lane_pair<PAIR>(static_cast<uint32_t>(u >> 32), ah, bh);
+    a = __longlong_as_double(static_cast<long long>((static_cast<uint64_t>(ah) << 32) | al));
+    b = __longlong_as_double(static_cast<long long>((static_cast<uint64_t>(bh) << 32) | bl));
+  } else {
+    a = v;
+    b = __shfl_xor(v, PAIR, kWave);
+  }
+}
+template <Lanes LANES>
 __device__ __forceinline__ double token_sum64(double v) {
   v = row16_sum64(v);
-  if constexpr (WAVE) {
-    v += __shfl_xor(v, 16, kWave);
-    v += __shfl_xor(v, 32, kWave);
+  if constexpr (LANES != Lanes::kRow) {
+    double a, b;
+    lane_pair64<LANES, 16>(v, a, b);
+    lane_pair64<LANES, 32>(a + b, a, b);
+    v = a + b;
   }
   return v;
 }
@@ -141,21 +163,23 @@ __device__ __forceinline__ float row16_max(float v) {
   v = fmaxf(v, dpp_f32<kDppRor8>(v));
   return v;
 }
-template <bool WAVE>
+template <Lanes LANES>
 __device__ __forceinline__ float token_max(float v) {
-  if constexpr (WAVE) return wave_max(v);
+  if constexpr (LANES != Lanes::kRow) return wave_max(v);
   else return row16_max(v);
 }
 
-template <bool WAVE>
+template <Lanes LANES>
 __device__ __forceinline__ double token_max64(double v) {
   v = fmax(v, dpp_f64<kDppXor1>(v));
   v = fmax(v, dpp_f64<kDppXor2>(v));
   v = fmax(v, dpp_f64<kDppRor4>(v));
   v = fmax(v, dpp_f64<kDppRor8>(v));
-  if constexpr (WAVE) {
-    v = fmax(v, __shfl_xor(v, 16, kWave));
-    v = fmax(v, __shfl_xor(v, 32, kWave));
+  if constexpr (LANES != Lanes::kRow) {
+    double a, b;
+    lane_pair64<LANES, 16>(v, a, b);
+    lane_pair64<LANES, 32>(fmax(a, b), a, b);
+    v = fmax(a, b);
   }
   return v;
 }
@@ -183,22 +207,22 @@ __device__ __forceinline__ void sort_desc64(double (&c)[N]) {
 
 // The k selection rounds over the lanes' sorted lists, as select_rounds in
 // route.hpp: lane j keeps round j's candidate.
-template <int N, int KMAX, bool WAVE, int J>
+template <int N, int KMAX, Lanes LANES, int J>
 __device__ __forceinline__ void select_round(double (&c)[N], int k, int gl, double& mine) {
   if (J < k) {
-    const double best = token_max64<WAVE>(c[0]);
+    const double best = token_max64<LANES>(c[0]);
     mine = gl == J ? best : mine;
     const bool pop = c[0] == best;
     constexpr int kShift = N < KMAX - 1 - J ? N : KMAX - 1 - J;  // entries that can still become a head
 #pragma unroll
     for (int i = 0; i < kShift; ++i) c[i] = pop ? (i + 1 < N ? c[i + 1] : 2.0 * kMasked) : c[i];
-    if constexpr (J + 1 < KMAX) select_round<N, KMAX, WAVE, J + 1>(c, k, gl, mine);
+    if constexpr (J + 1 < KMAX) select_round<N, KMAX, LANES, J + 1>(c, k, gl, mine);
   }
 }
-template <int N, int KMAX, bool WAVE>
+template <int N, int KMAX, Lanes LANES>
 __device__ __forceinline__ double select64(double (&c)[N], int k, int gl) {
   double mine = kMasked;
-  select_round<N, KMAX, WAVE, 0>(c, k, gl, mine);
+  select_round<N, KMAX, LANES, 0>(c, k, gl, mine);
   return mine;
 }
 
@@ -217,14 +241,41 @@ __device__ __forceinline__ void merge_best(double& a1, double& a2, double b1, do
   a1 = fmax(a1, b1);
   a2 = fmax(fmax(a2, b2), lo);
 }
+template <int CTRL>
+__device__ __forceinline__ void merge_dpp(double& a1, double& a2) {
+  merge_best(a1, a2, dpp_f64<CTRL>(a1), dpp_f64<CTRL>(a2));
+}
+template <Lanes LANES, int PAIR>
+__device__ __forceinline__ void merge_pair(double& a1, double& a2) {
+  double x1, y1, x2, y2;
+  lane_pair64<LANES, PAIR>(a1, x1, y1);
+  lane_pair64<LANES, PAIR>(a2, x2, y2);
+  merge_best(x1, x2, y1, y2);
+  a1 = x1;
+  a2 = x2;
+}
+// The pairs of P consecutive lanes (a power of two) merged in each of them.  The
+// mirrors reach a lane of the other half, where every lane has the same pair.
+template <Lanes LANES>
+__device__ __forceinline__ void merge_lanes(double& a1, double& a2, int P) {
+  if (P > 1) merge_dpp<kDppXor1>(a1, a2);
+  if (P > 2) merge_dpp<kDppXor2>(a1, a2);
+  if (P > 4) merge_dpp<kDppHalfMirror>(a1, a2);
+  if (P > 8) merge_dpp<kDppMirror>(a1, a2);
+  if constexpr (LANES != Lanes::kRow) {
+    if (P > 16) merge_pair<LANES, 16>(a1, a2);
+    if (P > 32) merge_pair<LANES, 32>(a1, a2);
+  }
+}
 
 }  // namespace
 
 // Lanes of one token: 16 (four tokens a wave) or the wave; lane gl holds
 // experts KPL gl .. KPL gl + KPL - 1.  BIAS: ranked by value, else by logit.
 // A masked expert's value is -inf from the point where it is known to be.
-template <int KPL, bool WAVE, bool BIAS>
+template <int KPL, Lanes LANES, bool BIAS>
 __global__ __launch_bounds__(256) void moe_route_scores_kernel(RouteParams q) {
+  constexpr bool WAVE = LANES != Lanes::kRow;
   constexpr int L = WAVE ? kWave : 16;
   constexpr int kTok = 256 / L;
   constexpr double kNegInf64 = -__builtin_inf();
@@ -249,7 +300,7 @@ __global__ __launch_bounds__(256) void moe_route_scores_kernel(RouteParams q) {
     m = v[0];
 #pragma unroll
     for (int i = 1; i < KPL; ++i) m = fmaxf(m, v[i]);
-    m = token_max<WAVE>(m);
+    m = token_max<LANES>(m);
     m = m > kNegInf ? m : 0.0f;
   }
 
@@ -265,7 +316,7 @@ __global__ __launch_bounds__(256) void moe_route_scores_kernel(RouteParams q) {
       if (sums) {
 #pragma unroll
         for (int i = 0; i < KPL; ++i) z += val[i];
-        z = token_sum64<WAVE>(z);
+        z = token_sum64<LANES>(z);
       }
     } else {
 #pragma unroll
@@ -287,7 +338,7 @@ __global__ __launch_bounds__(256) void moe_route_scores_kernel(RouteParams q) {
       // (binary32 exponentials: they only scale the weights and order nothing)
 #pragma unroll
       for (int i = 0; i < KPL; ++i) z += static_cast<double>(expf(v[i] - m));
-      z = token_sum64<WAVE>(z);
+      z = token_sum64<LANES>(z);
     }
 #pragma unroll
     for (int i = 0; i < KPL; ++i) val[i] = static_cast<double>(v[i]);
@@ -303,10 +354,7 @@ __global__ __launch_bounds__(256) void moe_route_scores_kernel(RouteParams q) {
       double b1 = val[0], b2 = kNegInf64;
 #pragma unroll
       for (int i = 1; i < KPL; ++i) add_best(b1, b2, val[i]);
-      for (int d = 1; d < q.group_lanes; d <<= 1) {
-        const double o1 = __shfl_xor(b1, d, kWave), o2 = __shfl_xor(b2, d, kWave);
-        merge_best(b1, b2, o1, o2);
-      }
+      merge_lanes<LANES>(b1, b2, q.group_lanes);
       const int g = gl / q.group_lanes;
       if (gl % q.group_lanes == 0 && g < G) sg[g] = q.group_best == 2 && b2 > kNegInf64 ? b1 + b2 : b1;
     } else {
@@ -334,10 +382,7 @@ __global__ __launch_bounds__(256) void moe_route_scores_kernel(RouteParams q) {
             for (int u = 0; u < 4; ++u) add_best(b1, b2, j + u * P < gs ? x[u] : kNegInf64);
           }
         }
-        for (int d = 1; d < P; d <<= 1) {
-          const double o1 = __shfl_xor(b1, d, kWave), o2 = __shfl_xor(b2, d, kWave);
-          merge_best(b1, b2, o1, o2);
-        }
+        merge_lanes<LANES>(b1, b2, P);
         if (g < G && sub == 0) sg[g] = q.group_best == 2 && b2 > kNegInf64 ? b1 + b2 : b1;
       }
     }
@@ -388,7 +433,7 @@ __global__ __launch_bounds__(256) void moe_route_scores_kernel(RouteParams q) {
     cand[i] = e < E ? candidate(v[i] > kNegInf ? rank : kMasked, e) : 2.0 * kMasked;
   }
   sort_desc64<KPL>(cand);
-  const double mine = k <= 8 ? select64<KPL, 8, WAVE>(cand, k, gl) : select64<KPL, kMaxTopK, WAVE>(cand, k, gl);
+  const double mine = k <= 8 ? select64<KPL, 8, LANES>(cand, k, gl) : select64<KPL, kMaxTopK, LANES>(cand, k, gl);
 
   // slot gl < k
   const int id = gl < k ? candidate_expert(mine) : 0;
@@ -418,33 +463,41 @@ __global__ __launch_bounds__(256) void moe_route_scores_kernel(RouteParams q) {
   }
 }
 
-template <int KPL, bool WAVE>
+template <int KPL, Lanes LANES>
 static void launch_scores(RouteParams q, hipStream_t s) {
-  constexpr int L = WAVE ? kWave : 16, kTok = 256 / L;
+  constexpr int L = LANES == Lanes::kRow ? 16 : kWave, kTok = 256 / L;
   const int gs = q.E / q.groups, lanes = gs / KPL;
   const bool whole = gs % KPL == 0 && (lanes & (lanes - 1)) == 0;
   q.group_lanes = q.groups > 1 && whole ? lanes : 0;
   const size_t doubles = q.groups <= 1 ? 0 : kTok * (kMaxRouteGroups + (whole ? 0 : q.E + L));
   const dim3 blocks = grid_of((static_cast<int64_t>(q.T) + kTok - 1) / kTok);
-  if (q.bias) moe_route_scores_kernel<KPL, WAVE, true><<<blocks, 256, doubles * sizeof(double), s>>>(q);
-  else moe_route_scores_kernel<KPL, WAVE, false><<<blocks, 256, doubles * sizeof(double), s>>>(q);
+  if (q.bias) moe_route_scores_kernel<KPL, LANES, true><<<blocks, 256, doubles * sizeof(double), s>>>(q);
+  else moe_route_scores_kernel<KPL, LANES, false><<<blocks, 256, doubles * sizeof(double), s>>>(q);
+}
+
+// Few tokens wait for each step of their chain, many for the vector ALU (300
+// experts, k = 16: 64 tokens 6.0 us by swaps, 7.0 by shuffles; 16384: 34.7 and 31.7).
+template <int KPL>
+static void launch_wave_scores(const RouteParams& q, hipStream_t s) {
+  if (q.T <= kRouteWaveTokens) launch_scores<KPL, Lanes::kSwap>(q, s);
+  else launch_scores<KPL, Lanes::kShuffle>(q, s);
 }
 
 hipError_t launch_route_scores(const RouteParams& q, hipStream_t s) {
   // A whole wave a token where 16 lanes would hold many experts each and the
   // batch does not fill the chip (256 experts in groups with a bias: 1 token
-  // 5.2 us, with 16 lanes 7.8; 2048: 6.8 and 8.4; 4096: 9.4 and 8.6).
+  // 4.5 us, with 16 lanes 7.8; 2048: 6.0 and 8.4; 4096: 9.4 and 8.6).
   if (q.E > 256 || (q.E > 128 && q.T <= kRouteWaveTokens)) {
-    if (q.E <= 256) launch_scores<4, true>(q, s);
-    else if (q.E <= 320) launch_scores<5, true>(q, s);
-    else if (q.E <= 512) launch_scores<8, true>(q, s);
-    else launch_scores<16, true>(q, s);
+    if (q.E <= 256) launch_scores<4, Lanes::kSwap>(q, s);
+    else if (q.E <= 320) launch_wave_scores<5>(q, s);
+    else if (q.E <= 512) launch_wave_scores<8>(q, s);
+    else launch_wave_scores<16>(q, s);
   } else {
-    if (q.E <= 16) launch_scores<1, false>(q, s);
-    else if (q.E <= 32) launch_scores<2, false>(q, s);
-    else if (q.E <= 64) launch_scores<4, false>(q, s);
-    else if (q.E <= 128) launch_scores<8, false>(q, s);
-    else launch_scores<16, false>(q, s);
+    if (q.E <= 16) launch_scores<1, Lanes::kRow>(q, s);
+    else if (q.E <= 32) launch_scores<2, Lanes::kRow>(q, s);
+    else if (q.E <= 64) launch_scores<4, Lanes::kRow>(q, s);
+    else if (q.E <= 128) launch_scores<8, Lanes::kRow>(q, s);
+    else launch_scores<16, Lanes::kRow>(q, s);
   }
   return hipGetLastError();
 }
