@@ -159,7 +159,10 @@ PyObject* pair(const Tensor& a, const Tensor& b) {
   return PyTuple_Pack(2, x.p, y.p);
 }
 
-void arguments(Py_ssize_t n, Py_ssize_t want) { TORCH_CHECK_TYPE(n == want, "takes ", want, " arguments, got ", n); }
+void arguments(Py_ssize_t n, Py_ssize_t want) {
+  TORCH_CHECK_TYPE(n == want, "takes ", want, " arguments, got ", n);
+  TORCH_CHECK(g_error && g_raw_stream, "called before setup(error class, raw stream function)");
+}
 
 // (logits, top_k, router, bias, out)
 PyObject* route(PyObject*, PyObject* const* a, Py_ssize_t n) {
@@ -364,7 +367,7 @@ PyObject* linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
 // (error class, raw_stream)
 PyObject* setup(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
-  arguments(n, 2);
+  TORCH_CHECK_TYPE(n == 2, "takes 2 arguments, got ", n);
   Py_INCREF(a[0]);
   Py_INCREF(a[1]);
   g_error = a[0];
