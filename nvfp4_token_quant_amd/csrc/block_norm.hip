@@ -67,15 +67,19 @@ template <typename T, bool VEC, int TPR, int NC>
 struct Part {
   Raw8<T> piece[NC];
   float rest;
-  __device__ __forceinline__ void load(const void* row, int lt, int cols) {
+  template <bool ALIGNED>
+  __device__ __forceinline__ void load_pieces(const void* row, int lt, int cols) {
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
       const int c = 8 * (lt + TPR * i);
       if (c + 8 <= cols) {
-        if constexpr (VEC) load8<T>(piece[i], row, c);
+        if constexpr (ALIGNED) load8<T>(piece[i], row, c);
         else load8_any<T>(piece[i], row, c);
       }
     }
+  }
+  __device__ __forceinline__ void load(const void* row, int lt, int cols) {
+    load_pieces<VEC>(row, lt, cols);
     if (!VEC && lt < cols % 8) rest = T::get(row, cols / 8 * 8 + lt);
   }
   __device__ __forceinline__ void get(Own<VEC, NC>& f, int lt, int cols) const {
@@ -115,13 +119,44 @@ __device__ __forceinline__ const void* row_at(const void* p, int64_t elements) {
 }
 
 // Up to two pieces a thread, everything a row needs is loaded before its first
-// reduction; with more, the registers hold only the row, and the rest is
-// loaded where it is used (65536 columns, one row: 62 us with all loads first,
-// most of them spilled).
+// reduction (binary32: with two pieces the weights, for which the registers do
+// not reach, where they are used: two rows of 15331 columns 7.2 us, else 10.0).
+// With more the registers hold the row, and the rest is loaded where it is used:
+// two pieces at a time where all of them would spill (1024 rows of 65536 bf16, eight
+// pieces: 294 us, all at a time 516; four pieces of bf16 together are 5% faster
+// than two).
 template <int NC>
-constexpr bool kLoadFirst = NC <= 2;
+constexpr bool kRowFirst = NC <= 2;
+template <typename T, int NC>
+constexpr bool kWeightsFirst = NC * T::kBytes <= 4;
 
-// N(v) in place.  w, b: the loaded weight and bias (kLoadFirst).
+// f(j, x) for each of a thread's columns j with its value x: of a loaded part,
+// or of a row.
+template <bool LOADED, typename T, bool VEC, int TPR, int NC, typename F>
+__device__ __forceinline__ void with_part(const Part<T, VEC, TPR, NC>& part, const void* row, int lt, int cols, F f) {
+  constexpr int N = 8 * NC + (VEC ? 0 : 1);
+  if constexpr (LOADED) {
+    float x[N];
+    part.get(x, lt, cols);
+#pragma unroll
+    for (int j = 0; j < N; ++j) f(j, x[j]);
+  } else {
+    constexpr int kTogether = NC * T::kBytes > 8 ? 2 : NC;
+    Part<T, true, TPR, kTogether> some;
+#pragma unroll
+    for (int i = 0; i < NC; i += kTogether) {
+      float x[8 * kTogether];
+      some.template load_pieces<VEC>(row, lt + TPR * i, cols);
+      some.get(x, lt + TPR * i, cols);
+#pragma unroll
+      for (int j = 0; j < 8 * kTogether; ++j) f(8 * i + j, x[j]);
+      if constexpr (NC > kTogether) __builtin_amdgcn_sched_barrier(0);
+    }
+    if constexpr (!VEC) f(8 * NC, lt < cols % 8 ? T::get(row, cols / 8 * 8 + lt) : 0.0f);
+  }
+}
+
+// N(v) in place.  w, b: the loaded weight and bias (kWeightsFirst).
 template <typename T, bool VEC, int TPR, int NC>
 __device__ __forceinline__ void apply_norm(Own<VEC, NC>& v, const NormParams& n,
                                            Part<T, VEC, TPR, NC>& w, Part<T, VEC, TPR, NC>& b, int lt, int cols,
@@ -143,23 +178,14 @@ __device__ __forceinline__ void apply_norm(Own<VEC, NC>& v, const NormParams& n,
 #pragma unroll
   for (int j = 0; j < N; ++j) q = __builtin_fmaf(v[j], v[j], q);
   const float inv = 1.0f / sqrtf(row_sum<TPR>(q, buf1) * inv_n + n.eps);
+  constexpr bool kLoaded = kWeightsFirst<T, NC>;
   if (n.weight) {
-    float f[N];
-    if constexpr (!kLoadFirst<NC>) w.load(n.weight, lt, cols);
-    w.get(f, lt, cols);
-#pragma unroll
-    for (int j = 0; j < N; ++j) v[j] *= inv * (f[j] + n.offset);
+    with_part<kLoaded>(w, n.weight, lt, cols, [&](int j, float x) { v[j] *= inv * (x + n.offset); });
   } else {
 #pragma unroll
     for (int j = 0; j < N; ++j) v[j] *= inv;
   }
-  if (n.bias) {
-    float f[N];
-    if constexpr (!kLoadFirst<NC>) b.load(n.bias, lt, cols);
-    b.get(f, lt, cols);
-#pragma unroll
-    for (int j = 0; j < N; ++j) v[j] += f[j];
-  }
+  if (n.bias) with_part<kLoaded>(b, n.bias, lt, cols, [&](int j, float x) { v[j] += x; });
 }
 
 __device__ __forceinline__ float sigmoid32(float g) { return 1.0f / (1.0f + expf(-g)); }
@@ -183,33 +209,27 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void block_norm_kernel(Block
   const void* grow = row_at<T>(p.gate, p.gate ? row * p.ld_gate : 0);
   const bool wide_gate = p.gate && p.gate_cols != 1;
   const void* rrow = row_at<R>(p.r, row * p.ld_r);
-  if (kLoadFirst<NC> || !p.y) pr.load(rrow, lt, cols);
+  if (kRowFirst<NC> || !p.y) pr.load(rrow, lt, cols);
   if (p.y) py.load(row_at<T>(p.y, row * p.ld_y), lt, cols);
   float g1 = p.gate && !wide_gate ? T::get(grow, 0) : 1.0f;
-  if constexpr (kLoadFirst<NC>) {
-    if (wide_gate) pg.load(grow, lt, cols);
+  if (kRowFirst<NC> && wide_gate) pg.load(grow, lt, cols);
+  if constexpr (kWeightsFirst<T, NC>) {
     if (p.after.weight) wa.load(p.after.weight, lt, cols);
     if (p.after.bias) ba.load(p.after.bias, lt, cols);
     if (p.before.weight) wb.load(p.before.weight, lt, cols);
     if (p.before.bias) bb.load(p.before.bias, lt, cols);
   }
 
-  float v[N], f[N];
+  float v[N];
   if (p.y) {
     py.get(v, lt, cols);
     if (p.after.kind >= 0) apply_norm<T, VEC, TPR, NC>(v, p.after, wa, ba, lt, cols, s_red[0], s_red[1]);
     if (p.gate && p.gate_sigmoid && !wide_gate) g1 = sigmoid32(g1);
     g1 *= p.out_scale;
-    if (wide_gate) {
-      if constexpr (!kLoadFirst<NC>) pg.load(grow, lt, cols);
-      pg.get(f, lt, cols);
-#pragma unroll
-      for (int j = 0; j < N; ++j) v[j] *= p.gate_sigmoid ? sigmoid32(f[j]) : f[j];
-    }
-    if constexpr (!kLoadFirst<NC>) pr.load(rrow, lt, cols);
-    pr.get(f, lt, cols);
-#pragma unroll
-    for (int j = 0; j < N; ++j) v[j] = p.res_scale * f[j] + g1 * v[j];
+    if (wide_gate)
+      with_part<kRowFirst<NC>>(pg, grow, lt, cols,
+                               [&](int j, float x) { v[j] *= p.gate_sigmoid ? sigmoid32(x) : x; });
+    with_part<kRowFirst<NC>>(pr, rrow, lt, cols, [&](int j, float x) { v[j] = p.res_scale * x + g1 * v[j]; });
   } else {
     pr.get(v, lt, cols);
 #pragma unroll
