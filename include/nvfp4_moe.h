@@ -245,9 +245,9 @@ int int8_linear(const void* x_dev, int32_t dtype, int64_t ld_x, const void* w_de
                 void* workspace_dev, int64_t workspace_bytes, void* out_dev, int32_t out_dtype, int64_t ldo,
                 void* stream);
 
-/* Bytes of int8_linear's workspace for M tokens of K columns (0 for a single
- * token of at most 32768 columns: its codes stay in the kernel, and the
- * workspace may be NULL).  Host-only. */
+/* Bytes of int8_linear's workspace for M tokens of K columns.  0 for one token of
+ * at most 32768 columns, 2 of 8192, 3 or 4 of 4096, 5 to 8 of 2048, 9 to 16 of
+ * 1024: their codes stay in the kernel, and the workspace may be NULL.  Host-only. */
 int int8_linear_workspace(int64_t M, int64_t K, int64_t* bytes);
 
 /* ---------------------------------------------------------------------- */

@@ -49,12 +49,15 @@ __device__ __forceinline__ void load_piece(float (&f)[8], const void* row, int64
   } else if (c + 8 <= cols) {
     load8_any<T>(raw, row, c);
     to_f32<T>(raw, f);
-  } else {
+  } else if (c < cols) {
     // (unconditional loads, in flight together)
 #pragma unroll
     for (int j = 0; j < 8; ++j) f[j] = T::get(row, min(c + j, cols - 1));
 #pragma unroll
     for (int j = 0; j < 8; ++j) f[j] = c + j < cols ? f[j] : 0.0f;
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = 0.0f;
   }
 }
 
@@ -391,7 +394,7 @@ __device__ __forceinline__ void store_tile(const Int8GemmParams& p, const i32x4 
   // 16-byte pieces at any address; value by value 777 x 1003 x 1999 took 10.5 us,
   // so 9.2)
   float sb[4 * FN], bias[4 * FN] = {};
-  if (n0 + 4 * FN <= p.N) {
+  if (n0 <= p.N - 4 * FN) {
     __builtin_memcpy(sb, p.sb + n0, sizeof(sb));
     if (p.bias) __builtin_memcpy(bias, p.bias + n0, sizeof(bias));
   } else {
@@ -604,6 +607,111 @@ __attribute__((amdgpu_waves_per_eu(WM * WN / 4, WM * WN / 4))) void int8_tiled_k
   else store_tile<F32, FM, FN>(p, acc, t0, nl);
 }
 
+// Two to 16 tokens with little to quantize (linear_few_tokens): the product from
+// the unquantized rows in one kernel.  Every block quantizes the rows for itself,
+// by the steps of the quantization kernel, behind the loads of its first tile's
+// weights, and keeps the codes in LDS; its eight waves take every eighth step of a
+// tile of 16 channels, weights straight to registers, and their sums meet in LDS.
+// The quantizing in every block costs what the launch of a second kernel does at
+// about 32768 values (4 x 4096 x 7168: 9.9 us in one, 10.3 in two; 16 x 8192 x 2048
+// 12.0 and 7.9), so the rule is half of that: 8 x 4096 x 2048 4.8 and 6.0, 2 x 4096 x
+// 7168 8.9 and 10.2, 16 x 128 x 1024 4.5 and 5.7, 2 x 65536 x 4096 53 and 60.
+// TWO: a wave quantizes rows `wave` and `wave + 8`; else 4, 2 or 1 of the eight
+// waves share a row.  Rows in LDS are 16 bytes more than a multiple of 128 apart
+// (16 lanes that read the same piece of 16 rows touch all banks).
+constexpr int kFewThreads = 512, kFewWaves = kFewThreads / kWave, kFewPieces = 4;
+constexpr int kFewSteps = kLinearFewMaxK / kStepBytes / kFewWaves;
+static_assert(kLinearFewColumns == kFewThreads * 8 * kFewPieces, "all rows' columns are in the block's pieces");
+
+template <typename T, bool TWO>
+__global__ __launch_bounds__(kFewThreads) void int8_few_kernel(Int8GemmParams p, const void* __restrict__ x,
+                                                               int64_t ldx) {
+  extern __shared__ __align__(16) uint8_t s_codes[];  // [M][ls]
+  __shared__ float s_am[kFewWaves], s_scale[16];
+  __shared__ i32x4 s_sum[kFewWaves - 1][kWave];
+  const int lane = threadIdx.x & (kWave - 1), r = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / kWave);
+  const int S = (p.K + kStepBytes - 1) / kStepBytes, ls = S * kStepBytes + 16;
+  const int last = (p.K - 1) / 16 * 16;
+  const int tiles = static_cast<int>((static_cast<int64_t>(p.N) + 15) / 16);
+  const auto load = [&](i32x4 (&b)[kFewSteps][2], int tile) {  // past K: the last piece again, times zero
+    const int8_t* row = p.b + min(static_cast<int64_t>(tile) * 16 + r, static_cast<int64_t>(p.N) - 1) * p.ldb;
+#pragma unroll
+    for (int i = 0; i < kFewSteps; ++i) {
+      const int c = (wave + kFewWaves * i) * kStepBytes + 16 * g;
+      if (wave + kFewWaves * i < S) {
+        b[i][0] = *reinterpret_cast<const i32x4*>(row + min(c, last));
+        b[i][1] = *reinterpret_cast<const i32x4*>(row + min(c + 64, last));
+      }
+    }
+  };
+
+  const int share = TWO || p.M > 4 ? 1 : p.M > 2 ? 2 : 4;  // waves of a row
+  const auto row_of = [&](int i) { return TWO ? wave + kFewWaves * (i / (kFewPieces / 2)) : wave / share; };
+  const auto col_of = [&](int i) {
+    return 8 * (lane + kWave * (TWO ? i % (kFewPieces / 2) : wave % share + share * i));
+  };
+  float f[kFewPieces][8];
+#pragma unroll
+  for (int i = 0; i < kFewPieces; ++i)
+    load_piece<T, false>(f[i], static_cast<const char*>(x) + min(row_of(i), p.M - 1) * ldx * T::kBytes, col_of(i), p.K);
+  int tile = blockIdx.x;
+  i32x4 b[kFewSteps][2];
+  load(b, tile);
+  float am[2] = {0.0f, 0.0f};
+#pragma unroll
+  for (int i = 0; i < kFewPieces; ++i) {
+    const int u = TWO && i >= kFewPieces / 2 ? 1 : 0;
+    am[u] = fmaxf(am[u], amax8(f[i]));
+  }
+  am[0] = wave_max(am[0]);
+  if constexpr (TWO) {
+    am[1] = wave_max(am[1]);
+  } else {
+    if (lane == 0) s_am[wave] = am[0];
+    lds_barrier();  // (the weights' loads stay in flight)
+    for (int j = 0; j < share; ++j) am[0] = fmaxf(am[0], s_am[wave / share * share + j]);
+  }
+#pragma unroll
+  for (int i = 0; i < kFewPieces; ++i) {
+    const float a = am[TWO && i >= kFewPieces / 2 ? 1 : 0];
+    const bool some = a >= kMinAmax;
+    const float inv = some ? 127.0f / a : 0.0f;
+    const int row = row_of(i), c = col_of(i);
+    if (row < p.M && c < S * kStepBytes) *reinterpret_cast<u32x2*>(s_codes + row * ls + c) = pack_codes(f[i], inv);
+    if (row < p.M && c == 0) s_scale[row] = some ? a / 127.0f : 1.0f;
+  }
+  lds_barrier();
+
+  Int8GemmParams q = p;
+  q.sa = s_scale;
+  const uint8_t* xrow = s_codes + min(r, p.M - 1) * ls + 16 * g;
+  for (; tile < tiles; tile += gridDim.x) {
+    i32x4 acc[1][1] = {{i32x4{0, 0, 0, 0}}};
+#pragma unroll
+    for (int i = 0; i < kFewSteps; ++i) {
+      const int step = wave + kFewWaves * i;
+      if (step < S) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          acc[0][0] = __builtin_amdgcn_mfma_i32_16x16x64_i8(
+              b[i][h], *reinterpret_cast<const i32x4*>(xrow + step * kStepBytes + 64 * h), acc[0][0], 0, 0, 0);
+      }
+    }
+    if (tile + static_cast<int>(gridDim.x) < tiles) load(b, tile + gridDim.x);
+    if (wave > 0) s_sum[wave - 1][lane] = acc[0][0];
+    lds_barrier();
+    if (wave == 0) {
+#pragma unroll
+      for (int w = 0; w < kFewWaves - 1; ++w) acc[0][0] += s_sum[w][lane];
+      if (p.dtype == MOE_BF16) store_tile<Bf16, 1, 1>(q, acc, r, 16 * tile + 4 * g);
+      else if (p.dtype == MOE_F16) store_tile<F16, 1, 1>(q, acc, r, 16 * tile + 4 * g);
+      else store_tile<F32, 1, 1>(q, acc, r, 16 * tile + 4 * g);
+    }
+    lds_barrier();  // the sums may be written again
+  }
+}
+
 // Lets a kernel use `bytes` of dynamic LDS.  The attribute belongs to the
 // current device: set once per device (devices past the mask's 64 set it on
 // every call).
@@ -807,6 +915,21 @@ hipError_t launch_int8_matmul(const Int8GemmParams& p, hipStream_t s) {
     case 6: return launch_ring<2, 4, 4, 2, 1, 2, 2>(p, s);
     default: return launch_tiled<2, 4, 8, 4>(p, s);
   }
+}
+
+template <typename T>
+static void launch_few(const Int8GemmParams& p, const void* x, int64_t ldx, hipStream_t s) {
+  const unsigned blocks = static_cast<unsigned>(std::min((static_cast<int64_t>(p.N) + 15) / 16, int64_t{512}));
+  const size_t lds = static_cast<size_t>(p.M) * ((p.K + kStepBytes - 1) / kStepBytes * kStepBytes + 16);
+  if (p.M > kFewWaves) int8_few_kernel<T, true><<<blocks, kFewThreads, lds, s>>>(p, x, ldx);
+  else int8_few_kernel<T, false><<<blocks, kFewThreads, lds, s>>>(p, x, ldx);
+}
+
+hipError_t launch_int8_few(const Int8GemmParams& p, const void* x, int64_t ldx, int x_dtype, hipStream_t s) {
+  if (x_dtype == MOE_BF16) launch_few<Bf16>(p, x, ldx, s);
+  else if (x_dtype == MOE_F16) launch_few<F16>(p, x, ldx, s);
+  else launch_few<F32>(p, x, ldx, s);
+  return hipGetLastError();
 }
 
 hipError_t launch_int8_token(const Int8GemmParams& p, const void* x, int x_dtype, hipStream_t s) {

@@ -209,6 +209,14 @@ hipError_t launch_int8_matmul(const Int8GemmParams& p, hipStream_t s);
 // p.sa are not read.
 constexpr int kLinearTokenMaxK = 32768;
 hipError_t launch_int8_token(const Int8GemmParams& p, const void* x, int x_dtype, hipStream_t s);
+// The same for 2 to 16 tokens, rows ldx apart, whose number, rounded up to a power
+// of two, times K is at most kLinearFewColumns.
+constexpr int kLinearFewColumns = 16384, kLinearFewMaxK = kLinearFewColumns / 2;
+inline bool linear_few_tokens(int64_t M, int64_t K) {
+  const int64_t rows = M <= 2 ? 2 : M <= 4 ? 4 : M <= 8 ? 8 : 16;
+  return M >= 2 && M <= 16 && K <= kLinearFewColumns / rows;
+}
+hipError_t launch_int8_few(const Int8GemmParams& p, const void* x, int64_t ldx, int x_dtype, hipStream_t s);
 
 // gemm_kernels.hip
 // Rows per tile and kernel family for a forward of T tokens.

@@ -139,7 +139,7 @@ int run_matmul(const void* a_dev, int64_t lda, const float* scale_a_dev, const v
 
 // int8_linear's workspace: the codes (rows of whole 16-byte pieces), then the
 // scales; none for a single token, which one kernel quantizes and multiplies.
-bool linear_in_one(int64_t M, int64_t K) { return M == 1 && K <= kLinearTokenMaxK; }
+bool linear_in_one(int64_t M, int64_t K) { return (M == 1 && K <= kLinearTokenMaxK) || linear_few_tokens(M, K); }
 int64_t linear_codes_bytes(int64_t M, int64_t K) { return M * ((K + 15) / 16 * 16); }
 
 }  // namespace
@@ -361,7 +361,8 @@ int int8_linear(const void* x_dev, int32_t dtype, int64_t ld_x, const void* w_de
   if (one) {
     const Int8GemmParams p = gemm_params(nullptr, ldc, nullptr, w_dev, ldw, scale_w_dev, bias_dev, M, N, K, out_dev,
                                          out_dtype, ldo);
-    hipError_t e = launch_int8_token(p, x_dev, dtype, static_cast<hipStream_t>(stream));
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    const hipError_t e = M == 1 ? launch_int8_token(p, x_dev, dtype, s) : launch_int8_few(p, x_dev, ld_x, dtype, s);
     if (e != hipSuccess) return hip_fail(e, "int8_linear launch");
     return api_ok();
   }

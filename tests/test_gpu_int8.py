@@ -194,6 +194,32 @@ def test_linear_one_token(N, K, dtype):
     assert torch.equal(zero, bias.to(dtype)[None])
 
 
+@pytest.mark.parametrize("M,N,K", [(2, 1, 1), (2, 40, 8192), (2, 20, 8193), (3, 100, 4095), (4, 2048, 4096), (5, 33, 2048),
+                                   (5, 30, 2049), (7, 4096, 130), (7, 4097, 130), (8, 500, 2047), (9, 64, 1024),
+                                   (16, 4096, 1000), (16, 17, 127), (13, 4090, 640), (16, 24, 1025), (17, 24, 512)])
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+def test_linear_few_tokens(M, N, K, dtype):
+    """Few tokens in one kernel (and the next larger sizes in two) equal the two steps bit for bit, and the reference."""
+    print(f"few tokens M={M} N={N} K={K} {dtype}", flush=True)
+    for c0, seed in ((0, 1), (1, 2)):
+        x = _randn(M, K + c0, seed=seed, dtype=dtype)[:, c0:]
+        x[M - 1, K // 2] = -90.0
+        x[M // 2] = 0.0
+        w, ws = _codes(N, K, 3), 0.01 * _scales(N, 4)
+        bias = _randn(N, seed=5) if seed == 1 else None
+        out = torch.full((M + 2, N + 3), 5.0, device="cuda")
+        got = binding.int8_linear(x, w, ws, bias=bias, out=out[1:-1, 2:-1])
+        q, s = binding.int8_quantize_per_token(x)
+        two = binding.int8_matmul(q, s, w, ws, bias=bias, out_dtype=F32)
+        torch.cuda.synchronize()
+        assert torch.equal(got, two)
+        ops_ref.check_product(got, *ops_ref.int8_product(*ops_ref.int8_rows(x), w.cpu().numpy(), ws.cpu().numpy(),
+                                                         None if bias is None else bias.cpu().numpy()))
+        got.fill_(5.0)
+        assert (out == 5.0).all()  # what is beside it stays as it was
+        assert torch.equal(binding.int8_linear(x, w, ws, bias=bias), two.to(dtype))
+
+
 def test_product_refusals_and_empty():
     a, b, sa, sb = _codes(4, 64, 1), _codes(8, 64, 2), _scales(4, 3), _scales(8, 4)
     assert binding.int8_matmul(a[:0], sa[:0], b, sb).shape == (0, 8)
@@ -209,7 +235,7 @@ def test_product_refusals_and_empty():
         binding.int8_matmul(a[:, 8:40], sa, b[:, 8:40], sb)          # rows not 16-byte aligned
 
 
-@pytest.mark.parametrize("M", [1, 48, 600])
+@pytest.mark.parametrize("M", [1, 6, 16, 48, 600])
 def test_linear_graph_replay(M):
     x = _randn(M, 1024, seed=1, dtype=BF16)
     wq, ws = binding.int8_quantize_per_token(_randn(520, 1024, seed=2))

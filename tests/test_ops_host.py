@@ -111,28 +111,30 @@ def test_int8_refusals():
     assert b"" == binding.lib().nvfp4_last_error()
 
 
-def _linear(x=1 << 20, dtype=BF16, ldx=60, w=1 << 21, ldw=64, sw=1 << 22, bias=0, M=4, N=8, K=60, ws=1 << 23,
-            wsb=4 * 68, out=1 << 24, odt=BF16, ldo=8):
+def _linear(x=1 << 20, dtype=BF16, ldx=60, w=1 << 21, ldw=64, sw=1 << 22, bias=0, M=17, N=8, K=60, ws=1 << 23,
+            wsb=17 * 68, out=1 << 24, odt=BF16, ldo=8):
     return binding.lib().int8_linear(P(x), dtype, ldx, P(w), ldw, P(sw), P(bias), M, N, K, P(ws), wsb, P(out), odt, ldo,
                                      None)
 
 
 def test_int8_linear_refusals():
     n = ctypes.c_int64()
-    assert binding.lib().int8_linear_workspace(4, 60, ctypes.byref(n)) == 0 and n.value == 4 * 68
-    for M, K in ((0, 5), (1, 1), (1, 32768), (1, 32769), (1, 131071), (2, 16), (300, 1001)):
+    assert binding.lib().int8_linear_workspace(17, 60, ctypes.byref(n)) == 0 and n.value == 17 * 68
+    none = ((1, 1), (1, 32768), (2, 16), (2, 8192), (3, 4096), (4, 4096), (5, 2048), (8, 2048), (9, 1024), (16, 1024))
+    for M, K in (*none, (0, 5), (1, 32769), (1, 131071), (2, 8193), (3, 4097), (5, 2049), (16, 1025), (17, 16), (300, 1001)):
         assert binding.lib().int8_linear_workspace(M, K, ctypes.byref(n)) == 0
-        assert n.value == (0 if M == 1 and K <= 32768 else M * ((K + 15) // 16 * 16 + 4))
+        assert n.value == (0 if (M, K) in none else M * ((K + 15) // 16 * 16 + 4))
     assert binding.lib().int8_linear_workspace(4, 0, ctypes.byref(n)) == 1
     assert binding.lib().int8_linear_workspace(-1, 60, ctypes.byref(n)) == 1
     assert binding.lib().int8_linear_workspace(4, 60, None) == 1
     assert _linear(dtype=3) == 1 and _linear(odt=3) == 1 and _linear(ldx=59) == 1 and _linear(K=0) == 1
-    assert _linear(ldw=60) == 1 and _linear(wsb=4 * 68 - 1) == 1 and _linear(ws=0) == 1 and _linear(ws=(1 << 23) + 8) == 1
+    assert _linear(ldw=60) == 1 and _linear(wsb=17 * 68 - 1) == 1 and _linear(ws=0) == 1 and _linear(ws=(1 << 23) + 8) == 1
     assert _linear(x=0) == 1 and _linear(w=0) == 1 and _linear(sw=0) == 1 and _linear(out=0) == 1 and _linear(M=-1) == 1
     for alias in (dict(out=1 << 20), dict(out=1 << 21), dict(out=1 << 22), dict(out=1 << 23), dict(ws=1 << 20),
                   dict(ws=1 << 21), dict(ws=1 << 22), dict(bias=1 << 23), dict(bias=1 << 24)):
         assert _linear(**alias) == 3, alias
     assert _linear(M=1, ws=0, wsb=0, x=0) == 1 and _linear(M=1, ws=0, wsb=0, out=1 << 20) == 3
+    assert _linear(M=16, ws=0, wsb=0, x=0) == 1 and _linear(M=16, ws=0, wsb=0, out=1 << 20) == 3
     assert _linear(M=0, x=0, ws=0, wsb=0, out=0) == 0 and _linear(N=0, w=0, sw=0, out=0) == 0
 
 
