@@ -607,7 +607,7 @@ __attribute__((amdgpu_waves_per_eu(WM * WN / 4, WM * WN / 4))) void int8_tiled_k
   else store_tile<F32, FM, FN>(p, acc, t0, nl);
 }
 
-// Two to 16 tokens with little to quantize (linear_few_tokens): the product from
+// Tokens with little to quantize, two to 16 of them (linear_few_tokens): the product from
 // the unquantized rows in one kernel.  Every block quantizes the rows for itself,
 // by the steps of the quantization kernel, behind the loads of its first tile's
 // weights, and keeps the codes in LDS; its eight waves take every eighth step of a
@@ -616,6 +616,9 @@ __attribute__((amdgpu_waves_per_eu(WM * WN / 4, WM * WN / 4))) void int8_tiled_k
 // about 32768 values (4 x 4096 x 7168: 9.9 us in one, 10.3 in two; 16 x 8192 x 2048
 // 12.0 and 7.9), so the rule is half of that: 8 x 4096 x 2048 4.8 and 6.0, 2 x 4096 x
 // 7168 8.9 and 10.2, 16 x 128 x 1024 4.5 and 5.7, 2 x 65536 x 4096 53 and 60.
+// Of more tokens a block takes 16 (linear_few_tiles): 512 x 256 x 512 5.3 us, in two
+// kernels 6.7; with more tiles than fit the chip at once it loses (1024 x 256 x 512
+// 8.9 and 7.3).
 // TWO: a wave quantizes rows `wave` and `wave + 8`; else 4, 2 or 1 of the eight
 // waves share a row.  Rows in LDS are 16 bytes more than a multiple of 128 apart
 // (16 lanes that read the same piece of 16 rows touch all banks).
@@ -631,6 +634,10 @@ __global__ __launch_bounds__(kFewThreads) void int8_few_kernel(Int8GemmParams p,
   __shared__ i32x4 s_sum[kFewWaves - 1][kWave];
   const int lane = threadIdx.x & (kWave - 1), r = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / kWave);
+  const int m0 = 16 * static_cast<int>(blockIdx.y);  // this block's rows
+  x = static_cast<const char*>(x) + m0 * ldx * T::kBytes;
+  p.out = static_cast<char*>(p.out) + m0 * p.ldo * (p.dtype == MOE_F32 ? 4 : 2);
+  p.M = min(p.M - m0, 16);
   const int S = (p.K + kStepBytes - 1) / kStepBytes, ls = S * kStepBytes + 16;
   const int last = (p.K - 1) / 16 * 16;
   const int tiles = static_cast<int>((static_cast<int64_t>(p.N) + 15) / 16);
@@ -920,9 +927,10 @@ hipError_t launch_int8_matmul(const Int8GemmParams& p, hipStream_t s) {
 template <typename T>
 static void launch_few(const Int8GemmParams& p, const void* x, int64_t ldx, hipStream_t s) {
   const unsigned blocks = static_cast<unsigned>(std::min((static_cast<int64_t>(p.N) + 15) / 16, int64_t{512}));
-  const size_t lds = static_cast<size_t>(p.M) * ((p.K + kStepBytes - 1) / kStepBytes * kStepBytes + 16);
-  if (p.M > kFewWaves) int8_few_kernel<T, true><<<blocks, kFewThreads, lds, s>>>(p, x, ldx);
-  else int8_few_kernel<T, false><<<blocks, kFewThreads, lds, s>>>(p, x, ldx);
+  const dim3 grid(blocks, (p.M + 15) / 16);
+  const size_t lds = static_cast<size_t>(std::min(p.M, 16)) * ((p.K + kStepBytes - 1) / kStepBytes * kStepBytes + 16);
+  if (p.M > kFewWaves) int8_few_kernel<T, true><<<grid, kFewThreads, lds, s>>>(p, x, ldx);
+  else int8_few_kernel<T, false><<<grid, kFewThreads, lds, s>>>(p, x, ldx);
 }
 
 hipError_t launch_int8_few(const Int8GemmParams& p, const void* x, int64_t ldx, int x_dtype, hipStream_t s) {

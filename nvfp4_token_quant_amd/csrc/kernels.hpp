@@ -216,6 +216,11 @@ inline bool linear_few_tokens(int64_t M, int64_t K) {
   const int64_t rows = M <= 2 ? 2 : M <= 4 ? 4 : M <= 8 ? 8 : 16;
   return M >= 2 && M <= 16 && K <= kLinearFewColumns / rows;
 }
+// Also for more tokens, sixteen a block, where K is at most 1024 and there are at
+// most two blocks a CU, of one tile of 16 channels each.
+inline bool linear_few_tiles(int64_t M, int64_t N, int64_t K) {
+  return M > 16 && K <= kLinearFewColumns / 16 && ((M + 15) / 16) * ((N + 15) / 16) <= 512;
+}
 hipError_t launch_int8_few(const Int8GemmParams& p, const void* x, int64_t ldx, int x_dtype, hipStream_t s);
 
 // gemm_kernels.hip

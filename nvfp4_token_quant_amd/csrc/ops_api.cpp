@@ -358,7 +358,7 @@ int int8_linear(const void* x_dev, int32_t dtype, int64_t ld_x, const void* w_de
       overlap(codes, need, w_dev, span(N, ldw, ldc, 1)) || overlap(codes, need, scale_w_dev, N * 4) ||
       (bias_dev && overlap(codes, need, bias_dev, N * 4)))
     return api_fail(NVFP4_ERR_ALIAS, "out or workspace overlaps an input");
-  if (one) {
+  if (one || linear_few_tiles(M, N, K)) {
     const Int8GemmParams p = gemm_params(nullptr, ldc, nullptr, w_dev, ldw, scale_w_dev, bias_dev, M, N, K, out_dev,
                                          out_dtype, ldo);
     const hipStream_t s = static_cast<hipStream_t>(stream);

@@ -196,7 +196,8 @@ def test_linear_one_token(N, K, dtype):
 
 @pytest.mark.parametrize("M,N,K", [(2, 1, 1), (2, 40, 8192), (2, 20, 8193), (3, 100, 4095), (4, 2048, 4096), (5, 33, 2048),
                                    (5, 30, 2049), (7, 4096, 130), (7, 4097, 130), (8, 500, 2047), (9, 64, 1024),
-                                   (16, 4096, 1000), (16, 17, 127), (13, 4090, 640), (16, 24, 1025), (17, 24, 512)])
+                                   (16, 4096, 1000), (16, 17, 127), (13, 4090, 640), (16, 24, 1025), (17, 24, 512), (49, 61, 70),
+                                   (33, 500, 1024), (512, 256, 512), (513, 256, 512), (31, 33, 1023), (8191, 7, 20)])
 @pytest.mark.parametrize("dtype", [BF16, F16, F32])
 def test_linear_few_tokens(M, N, K, dtype):
     """Few tokens in one kernel (and the next larger sizes in two) equal the two steps bit for bit, and the reference."""
