@@ -900,18 +900,23 @@ hipError_t launch_int8_matmul(const Int8GemmParams& p, hipStream_t s) {
   // Rows far apart: a tile's rows are addressed with 32-bit byte offsets, and
   // these tiles have the fewest.
   if (p.lda > kMaxTileLd || p.ldb > kMaxTileLd) return launch_ring<1, 1, 1, 2, 4, 3, 2>(p, s);
-  const auto tiles = [&](int bm, int bn) {
-    return ((static_cast<int64_t>(p.M) + bm - 1) / bm) * ((static_cast<int64_t>(p.N) + bn - 1) / bn);
-  };
-  // The measured time of a round of each tile, in microseconds for 128 bytes
-  // of K (where two blocks share a CU: with one, and with both): small tiles
-  // fill the chip when there are few, large ones move fewer bytes.
-  const auto paired = [&](int64_t t, double alone, double both) { return t <= 256 ? alone : both * rounds(t, 512); };
-  const double cost[] = {
-      0.06 * rounds(tiles(16, 16), 256),      paired(tiles(16, 32), 0.085, 0.155),
-      paired(tiles(32, 32), 0.14, 0.20),      0.18 * rounds(tiles(64, 32), 256),
-      0.25 * rounds(tiles(64, 64), 256),      0.62 * rounds(tiles(128, 128), 256),
-      1.09 * rounds(tiles(128, 128), 512),    1.8 * rounds(tiles(256, 256), 256)};
+  // What a round of each tile takes, in microseconds: for each 128 bytes of K and
+  // for the rest (first loads, sums, output), where every tile has a CU to itself
+  // and where they share the chip.  Fitted to 61 sizes of 17 to 16384 tokens;
+  // on 70 others the choice costs 1% over the best of the eight in the mean (with
+  // times for each 128 bytes alone 7% on the 61; 1340 x 7552 x 192 21.6 us for 13.5).
+  static constexpr struct { int bm, bn, slots; double step, rest, step_full, rest_full; } kTiles[] = {
+      {16, 16, 256, 0.026, 0.73, 0.051, 1.8},  {16, 32, 512, 0.05, 0.55, 0.13, 1.45},
+      {32, 32, 512, 0.13, 0.6, 0.186, 1.95},   {64, 32, 256, 0.145, 1.45, 0.163, 2.6},
+      {64, 64, 256, 0.226, 1.4, 0.262, 2.5},   {128, 128, 256, 0.58, 3.7, 0.66, 5.1},
+      {128, 128, 512, 0.70, 1.4, 1.0, 3.5},    {256, 256, 256, 1.27, 5.3, 1.6, 5.3}};
+  const double steps = (p.K + kStepBytes - 1) / kStepBytes;
+  double cost[std::size(kTiles)];
+  for (size_t i = 0; i < std::size(kTiles); ++i) {
+    const auto& t = kTiles[i];
+    const int64_t tiles = ((static_cast<int64_t>(p.M) + t.bm - 1) / t.bm) * ((static_cast<int64_t>(p.N) + t.bn - 1) / t.bn);
+    cost[i] = tiles <= 256 ? steps * t.step + t.rest : (steps * t.step_full + t.rest_full) * rounds(tiles, t.slots);
+  }
   switch (std::min_element(std::begin(cost), std::end(cost)) - std::begin(cost)) {
     case 0: return launch_ring<1, 1, 1, 1, 8, 4, 1>(p, s);
     case 1: return launch_ring<1, 1, 1, 2, 4, 3, 2>(p, s);
