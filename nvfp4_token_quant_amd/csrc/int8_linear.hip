@@ -330,7 +330,7 @@ __global__ __launch_bounds__(kTokenThreads) void int8_token_kernel(Int8GemmParam
 //
 // What bounds it: on operands like activations and weights the chip's power.
 // 8192^3 takes 449 us (2450 TOP/s; of zeros 370, without the copies 384), 4096 x
-// 7168 x 7168 186 to 212 us from one card to another (448 tiles on 256 CUs), a
+// 7168 x 7168 176 to 212 us from one card to another (448 tiles on 256 CUs), a
 // library's product alone, measured beside it, 462 and 195 to 236.  Four waves of
 // twice the tile each (128 x 128) took 576 us of zeros: one wave a SIMD hides
 // nothing.  Bands of 4 token tiles an XCD: 1% over 8; tiles in block order
@@ -902,7 +902,7 @@ hipError_t launch_int8_matmul(const Int8GemmParams& p, hipStream_t s) {
   if (p.lda > kMaxTileLd || p.ldb > kMaxTileLd) return launch_ring<1, 1, 1, 2, 4, 3, 2>(p, s);
   // What a round of each tile takes, in microseconds: for each 128 bytes of K and
   // for the rest (first loads, sums, output), where every tile has a CU to itself
-  // and where they share the chip.  Fitted to 61 sizes of 17 to 16384 tokens;
+  // and (_full) where there are more tiles than CUs.  Fitted to 61 sizes of 17 to 16384 tokens;
   // on 70 others the choice costs 1% over the best of the eight in the mean (with
   // times for each 128 bytes alone 7% on the 61; 1340 x 7552 x 192 21.6 us for 13.5).
   static constexpr struct { int bm, bn, slots; double step, rest, step_full, rest_full; } kTiles[] = {

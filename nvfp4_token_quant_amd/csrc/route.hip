@@ -25,7 +25,8 @@
 // lane's experts are consecutive, so that groups of whole lanes are reduced in
 // registers (through LDS: 2.7 us more of the 18.5).  16384 tokens of 256 experts
 // take 15.7 us with bias and groups (1960 vector instructions for four tokens),
-// 7.9 without (floor of the bytes: 3.7); one token of 128 experts 3.0 us.
+// 7.9 without (floor of the bytes: 3.7); one token of 128 experts 2.9 us, 64 of 256
+// in groups 4.6.
 #include "common.hpp"
 #include "dtype.hpp"
 #include "kernels.hpp"

@@ -1,10 +1,10 @@
 // The operators around the layer, called with torch tensors (module _calls).
 //
-// A single token's kernels take 3 to 6 us, so the host's side decides what a
+// A single token's kernels take 3 to 5 us, so the host's side decides what a
 // call costs.  In Python (attribute reads, struct packing, ctypes, torch.empty)
-// a call took 8.1 to 10.2 us, here 4.8 to 5.3: the checks read the tensors' fields and the
-// results are allocated without Python's argument parsing.  The launch itself
-// is 2.4 us of what remains.
+// a call took 8.1 to 10.2 us, here 4.7 to 5.5: the checks read the tensors'
+// fields, and the results are allocated without Python's argument parsing.  The
+// launch itself is 2.4 us of what remains.
 //
 // Checks of types, shapes, strides and devices stand here and raise ValueError;
 // everything else (ranges, alignment, overlap) is the library's, whose status
