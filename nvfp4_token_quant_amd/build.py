@@ -32,7 +32,7 @@ LIBS = {
 }
 
 CALLS = "_calls.so"
-CXX = os.environ.get("CXX", "g++")
+CXX = "g++"
 
 
 def _calls_compile(obj):

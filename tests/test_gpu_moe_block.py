@@ -1,4 +1,6 @@
 """The layer with its router set, and the operators of a block run together."""
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -202,3 +204,65 @@ def test_block(layer_id, T, residual):
         torch.cuda.synchronize()
         assert torch.equal(cap[0], eager[0]) and torch.equal(cap[1], eager[1])
     layer.close()
+
+
+def test_calls_from_two_threads():
+    """The operators called from two threads at once, each on its own stream, one norm shared by both."""
+    g = torch.Generator().manual_seed(11)
+    x = [torch.randn((5, 640), generator=g).to(torch.bfloat16).cuda() for _ in range(2)]
+    l = [torch.randn((9, 96), generator=g).cuda() for _ in range(2)]
+    w, ws = binding.int8_quantize_per_token(torch.randn((200, 640), generator=g).cuda())
+    n = binding.Norm(torch.randn(640, generator=g).to(torch.bfloat16).cuda())
+    rule = binding.Router(groups=4, top_groups=2)
+
+    def calls(i):
+        return (*binding.block_norm(x[i], x[1 - i], before=n, after=n), *binding.route(l[i], 6, rule),
+                binding.int8_linear(x[i], w, ws), *binding.int8_quantize_per_token(x[i]))
+
+    want = [calls(0), calls(1)]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def run(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(50):
+                    got = calls(i)
+                torch.cuda.current_stream().synchronize()
+            if not all(torch.equal(a, b) for a, b in zip(got, want[i])):
+                wrong.append(f"results of thread {i}")
+        except Exception as e:  # reported below, in the main thread
+            wrong.append(repr(e))
+
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong, wrong
+
+
+def test_results_allocated_under_capture():
+    """A graph whose calls make their own results, replayed with eager calls between."""
+    x = torch.randn((4, 512), generator=torch.Generator().manual_seed(12)).to(torch.bfloat16).cuda()
+    w, ws = binding.int8_quantize_per_token(torch.randn((64, 512), generator=torch.Generator().manual_seed(13)).cuda())
+    n, rule = binding.Norm(kind="layer"), binding.Router(score="sigmoid")
+
+    def chain():
+        r, h = binding.block_norm(x, x, before=n)
+        logits = binding.int8_linear(h, w, ws, out_dtype=torch.float32)
+        q, s = binding.int8_quantize_per_token(h)
+        return r, h, logits, *binding.route(logits, 4, rule), binding.int8_matmul(q, s, w, ws, out_dtype=torch.float32)
+
+    chain()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        made = chain()
+    for i in range(3):
+        x.copy_(torch.randn((4, 512), generator=torch.Generator().manual_seed(20 + i)))
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(made, chain()):
+            assert torch.equal(a, b)
+        assert torch.equal(made[2], made[5])
