@@ -152,7 +152,7 @@ __device__ __forceinline__ int64_t block_id() { return static_cast<int64_t>(bloc
 
 // route.hip: the router with scores, bias and groups.
 constexpr int kMaxRouteGroups = 64;
-constexpr int kRouteWaveTokens = 2048;  // batches of up to 256 experts that may take a whole wave a token
+constexpr int kRouteWaveTokens = 2048;  // batches of more than 128 experts that take a whole wave a token
 struct RouteParams {
   const void* logits;  // [T, ld] of dtype (moe_dtype)
   const float* bias;   // [E] or NULL

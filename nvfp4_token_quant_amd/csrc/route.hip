@@ -21,7 +21,7 @@
 // vector work: with a bias (or groups by two values) one binary64
 // exponential for every logit, the sort of each lane's candidates, and k
 // rounds of a maximum over a token's lanes.  16 lanes share a token (four
-// tokens a wave) or, for few tokens or more than 256 experts, the whole wave; a
+// tokens a wave) or, for few tokens or more than 432 experts, the whole wave; a
 // lane's experts are consecutive, so that groups of whole lanes are reduced in
 // registers (through LDS: 2.7 us more of the 18.5).  16384 tokens of 256 experts
 // take 15.7 us with bias and groups (1960 vector instructions for four tokens),
@@ -476,29 +476,43 @@ static void launch_scores(RouteParams q, hipStream_t s) {
   else moe_route_scores_kernel<KPL, LANES, false><<<blocks, 256, doubles * sizeof(double), s>>>(q);
 }
 
-// Few tokens wait for each step of their chain, many for the vector ALU (300
-// experts, k = 16: 64 tokens 6.0 us by swaps, 7.0 by shuffles; 16384: 34.7 and 31.7).
+// Few tokens wait for each step of their chain, many for the vector ALU (1000
+// experts, k = 16: 64 tokens 7.4 us by swaps, 8.2 by shuffles; 16384: 62.4 and 60.5;
+// 300 experts, a wave a token: 16384 34.7 and 31.7).
 template <int KPL>
 static void launch_wave_scores(const RouteParams& q, hipStream_t s) {
   if (q.T <= kRouteWaveTokens) launch_scores<KPL, Lanes::kSwap>(q, s);
   else launch_scores<KPL, Lanes::kShuffle>(q, s);
 }
 
+// Most experts of which 16 lanes hold a token (their values for the groups,
+// [16][E + 16] doubles, and the group scores within 64 KB of LDS).
+constexpr int kRouteRowExperts = 432;
+static_assert(8 * 16 * (kMaxRouteGroups + kRouteRowExperts + 16) <= 64 * 1024, "a block's groups and values");
+
 hipError_t launch_route_scores(const RouteParams& q, hipStream_t s) {
   // A whole wave a token where 16 lanes would hold many experts each and the
   // batch does not fill the chip (256 experts in groups with a bias: 1 token
-  // 4.5 us, with 16 lanes 7.8; 2048: 6.0 and 8.4; 4096: 9.4 and 8.6).
-  if (q.E > 256 || (q.E > 128 && q.T <= kRouteWaveTokens)) {
+  // 4.5 us, with 16 lanes 7.8; 2048: 6.0 and 8.4; 4096: 9.4 and 8.6.  300, k = 16:
+  // 2048 tokens 8.0 and 8.8, 4096 11.4 and 9.0, 16384 31.5 and 19.2; 384 with a
+  // bias 8.5 and 13.0, 13.3 and 13.3, 39.0 and 35.4).
+  if (q.E > kRouteRowExperts || (q.E > 128 && q.T <= kRouteWaveTokens)) {
     if (q.E <= 256) launch_scores<4, Lanes::kSwap>(q, s);
-    else if (q.E <= 320) launch_wave_scores<5>(q, s);
+    else if (q.E <= 320) launch_scores<5, Lanes::kSwap>(q, s);
     else if (q.E <= 512) launch_wave_scores<8>(q, s);
     else launch_wave_scores<16>(q, s);
   } else {
+    // (16384 tokens of 160 experts in two groups: 10 a lane 10.9 us, 16 a lane 16.0;
+    // 192 in groups with a bias: 12 a lane 13.0, 16 a lane 18.8)
     if (q.E <= 16) launch_scores<1, Lanes::kRow>(q, s);
     else if (q.E <= 32) launch_scores<2, Lanes::kRow>(q, s);
     else if (q.E <= 64) launch_scores<4, Lanes::kRow>(q, s);
     else if (q.E <= 128) launch_scores<8, Lanes::kRow>(q, s);
-    else launch_scores<16, Lanes::kRow>(q, s);
+    else if (q.E <= 160) launch_scores<10, Lanes::kRow>(q, s);
+    else if (q.E <= 192) launch_scores<12, Lanes::kRow>(q, s);
+    else if (q.E <= 256) launch_scores<16, Lanes::kRow>(q, s);
+    else if (q.E <= 320) launch_scores<20, Lanes::kRow>(q, s);
+    else launch_scores<32, Lanes::kRow>(q, s);
   }
   return hipGetLastError();
 }

@@ -41,7 +41,9 @@ def _bias(E, seed=0):
     (1, 1, 1, 1, 1, 1), (3, 8, 8, 1, 1, 1), (5, 16, 4, 4, 2, 2), (1, 128, 8, 1, 1, 1), (64, 256, 8, 8, 4, 2),
     (33, 60, 4, 5, 2, 1), (9, 300, 16, 6, 3, 2), (7, 1024, 16, 64, 9, 2), (2, 1000, 16, 1, 1, 1), (4, 64, 2, 64, 3, 2),
     (1025, 16, 2, 1, 1, 1), (1030, 20, 3, 4, 2, 2), (1100, 64, 6, 8, 3, 1), (1500, 100, 9, 50, 12, 2),
-    (2000, 256, 8, 8, 4, 2), (1201, 256, 16, 64, 5, 1), (1027, 300, 16, 6, 3, 1)])
+    (2000, 256, 8, 8, 4, 2), (1201, 256, 16, 64, 5, 1), (1027, 300, 16, 6, 3, 1),
+    (2100, 160, 8, 8, 4, 2), (2049, 150, 5, 3, 2, 1), (2065, 192, 16, 8, 4, 2), (2100, 300, 16, 6, 3, 2), (2061, 320, 8, 4, 2, 2), (2050, 384, 8, 6, 3, 2), (2077, 384, 5, 8, 4, 1),
+    (2049, 432, 16, 3, 2, 2), (2055, 433, 7, 1, 1, 1), (2060, 510, 9, 6, 3, 2), (2052, 1000, 16, 5, 3, 2)])
 def test_route_sizes(T, E, k, groups, top_groups, best, score, bias):
     print(f"route T={T} E={E} k={k} groups={groups}/{top_groups}/{best} {score} bias={bias}", flush=True)
     for renorm, scale in ((True, 1.0), (False, 2.5)):
