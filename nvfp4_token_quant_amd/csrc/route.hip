@@ -111,19 +111,25 @@ __device__ __forceinline__ int candidate_expert(double c) {
 }
 
 template <int CTRL>
-__device__ __forceinline__ double dpp_f64(double v) {
-  const uint64_t u = static_cast<uint64_t>(__double_as_longlong(v));
+__device__ __forceinline__ uint64_t dpp_u64(uint64_t u) {
   // (every lane has a source under these controls: no value to keep)
   const uint64_t lo = static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(u), CTRL, 0xF, 0xF, true));
   const uint64_t hi =
       static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(u >> 32), CTRL, 0xF, 0xF, true));
-  return __longlong_as_double(static_cast<long long>((hi << 32) | lo));
+  return (hi << 32) | lo;
 }
+template <int CTRL>
+__device__ __forceinline__ double dpp_f64(double v) {
+  return __longlong_as_double(static_cast<long long>(dpp_u64<CTRL>(static_cast<uint64_t>(__double_as_longlong(v)))));
+}
+// The mirrors reach a lane of the other half, where every lane has the same sum:
+// each step adds the same two numbers in both of its lanes, so the sum is the
+// same bits in all 16.
 __device__ __forceinline__ double row16_sum64(double v) {
   v += dpp_f64<kDppXor1>(v);
   v += dpp_f64<kDppXor2>(v);
-  v += dpp_f64<kDppRor4>(v);
-  v += dpp_f64<kDppRor8>(v);
+  v += dpp_f64<kDppHalfMirror>(v);
+  v += dpp_f64<kDppMirror>(v);
   return v;
 }
 // The lanes of a token: a 16-lane row, or the wave, whose rows meet by register
@@ -133,29 +139,50 @@ enum class Lanes { kRow, kSwap, kShuffle };
 
 // A lane's value and its partner's, 16 or 32 lanes away, in either order.
 template <Lanes LANES, int PAIR>
-__device__ __forceinline__ void lane_pair64(double v, double& a, double& b) {
+__device__ __forceinline__ void lane_pair64(uint64_t u, uint64_t& a, uint64_t& b) {
   if constexpr (LANES == Lanes::kSwap) {
-    const uint64_t u = static_cast<uint64_t>(__double_as_longlong(v));
     uint32_t al, bl, ah, bh;
     lane_pair<PAIR>(static_cast<uint32_t>(u), al, bl);
     lane_pair<PAIR>(static_cast<uint32_t>(u >> 32), ah, bh);
-    a = __longlong_as_double(static_cast<long long>((static_cast<uint64_t>(ah) << 32) | al));
-    b = __longlong_as_double(static_cast<long long>((static_cast<uint64_t>(bh) << 32) | bl));
+    a = (static_cast<uint64_t>(ah) << 32) | al;
+    b = (static_cast<uint64_t>(bh) << 32) | bl;
   } else {
-    a = v;
-    b = __shfl_xor(v, PAIR, kWave);
+    a = u;
+    b = __shfl_xor(static_cast<unsigned long long>(u), PAIR, kWave);
   }
 }
-template <Lanes LANES>
-__device__ __forceinline__ double token_sum64(double v) {
-  v = row16_sum64(v);
+template <Lanes LANES, int PAIR>
+__device__ __forceinline__ void lane_pair64(double v, double& a, double& b) {
+  uint64_t x, y;
+  lane_pair64<LANES, PAIR>(static_cast<uint64_t>(__double_as_longlong(v)), x, y);
+  a = __longlong_as_double(static_cast<long long>(x));
+  b = __longlong_as_double(static_cast<long long>(y));
+}
+// The sum of a token's exponentials e, each in [0, 1], as whole multiples of
+// 2^-52 (the lowest bit of 1 + e; at e = 1 the pattern goes on into the next
+// binade).  Whole numbers add up the same in any order, so every lane has the
+// same bits, and so has the same token in another batch, where other lanes hold
+// its experts: experts of equal logits and biases have equal values everywhere.
+// Off by at most 2^-53 a term, 2^-43 of a sum of 1024 (it is at least 1 with any
+// expert).
+template <Lanes LANES, int KPL>
+__device__ __forceinline__ double exp_sum(const double (&e)[KPL]) {
+  constexpr uint64_t kOne = 0x3FF0000000000000ull;
+  uint64_t u = 0;
+#pragma unroll
+  for (int i = 0; i < KPL; ++i) u += static_cast<uint64_t>(__double_as_longlong(1.0 + e[i]));
+  u += dpp_u64<kDppXor1>(u);
+  u += dpp_u64<kDppXor2>(u);
+  u += dpp_u64<kDppHalfMirror>(u);
+  u += dpp_u64<kDppMirror>(u);
   if constexpr (LANES != Lanes::kRow) {
-    double a, b;
-    lane_pair64<LANES, 16>(v, a, b);
+    uint64_t a, b;
+    lane_pair64<LANES, 16>(u, a, b);
     lane_pair64<LANES, 32>(a + b, a, b);
-    v = a + b;
+    u = a + b;
   }
-  return v;
+  u -= kOne * static_cast<uint64_t>(KPL * (LANES == Lanes::kRow ? 16 : kWave));
+  return 0x1p-52 * static_cast<double>(u);
 }
 __device__ __forceinline__ float row16_max(float v) {
   v = fmaxf(v, dpp_f32<kDppXor1>(v));
@@ -314,11 +341,7 @@ __global__ __launch_bounds__(256) void moe_route_scores_kernel(RouteParams q) {
     if (softmax) {
 #pragma unroll
       for (int i = 0; i < KPL; ++i) val[i] = exp64(fmax(static_cast<double>(v[i]) - static_cast<double>(m), -1200.0));
-      if (sums) {
-#pragma unroll
-        for (int i = 0; i < KPL; ++i) z += val[i];
-        z = token_sum64<LANES>(z);
-      }
+      if (sums) z = exp_sum<LANES>(val);
     } else {
 #pragma unroll
       for (int i = 0; i < KPL; ++i) val[i] = sigmoid64(v[i]);
@@ -338,8 +361,8 @@ __global__ __launch_bounds__(256) void moe_route_scores_kernel(RouteParams q) {
     if (sums) {
       // (binary32 exponentials: they only scale the weights and order nothing)
 #pragma unroll
-      for (int i = 0; i < KPL; ++i) z += static_cast<double>(expf(v[i] - m));
-      z = token_sum64<LANES>(z);
+      for (int i = 0; i < KPL; ++i) val[i] = static_cast<double>(expf(v[i] - m));
+      z = exp_sum<LANES>(val);
     }
 #pragma unroll
     for (int i = 0; i < KPL; ++i) val[i] = static_cast<double>(v[i]);
