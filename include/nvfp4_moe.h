@@ -218,7 +218,9 @@ int int8_quantize_per_token(const void* x_dev, int32_t dtype, int64_t rows, int6
 
 /*
  * out[m, n] = scale_a[m] * scale_b[n] * sum_k a[m, k] * b[n, k] + bias[n]
- * The sum is exact (32-bit integers), scaled in binary32, rounded once.
+ * The sum is exact (32-bit integers).  In binary32 it is rounded, multiplied by
+ * the rounded product of the scales (which may lie outside binary32's normal
+ * range) and, in the same rounding, added to the bias; that is rounded to dtype.
  *   a_dev     i8 [M, lda] token rows;  b_dev  i8 [N, ldb] channel rows; 16-byte
  *             aligned, lda and ldb multiples of 16, >= K, <= 2^26; whole 16-byte
  *             pieces are read, bytes behind K have no effect

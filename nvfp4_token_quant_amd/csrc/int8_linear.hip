@@ -185,14 +185,32 @@ hipError_t launch_int8_quantize_rows(const void* x, int dtype, int64_t rows, int
 // The sum times its scales, plus the bias, in binary32: the same steps in every
 // kernel (one rounding of product and bias), so that a token's result does not
 // depend on the batch that it comes with.
-__device__ __forceinline__ float scaled(int acc, float s, bool has_bias, float bias) {
-  const float a = static_cast<float>(acc);
-  return has_bias ? __builtin_fmaf(a, s, bias) : a * s;
+__device__ __forceinline__ float scaled(float acc, float s, bool has_bias, float bias) {
+  return has_bias ? __builtin_fmaf(acc, s, bias) : acc * s;
+}
+// Whether a product of scales is a normal number: its rounding is then half a
+// step, else (smallest rows and channels: 2^-126 x 1e-4) it has lost bits that
+// the result would have.
+__device__ __forceinline__ bool scale_in_range(float s) {
+  return fabsf(s) >= 0x1p-126f && fabsf(s) <= 3.402823466e38f;
+}
+// The factors acc and s = sa * sb where s may be out of range: s of the scales'
+// fractions (with the bits of sa * sb where that is in range), their exponents
+// shared between the two factors.
+__device__ __forceinline__ void factors_far(float& acc, float& s, float sa, float sb) {
+  s = __builtin_amdgcn_frexp_mantf(sa) * __builtin_amdgcn_frexp_mantf(sb);
+  const int e = __builtin_amdgcn_frexp_expf(sa) + __builtin_amdgcn_frexp_expf(sb);
+  const int es = min(max(e, -120), 120);
+  s = ldexpf(s, es);
+  acc = ldexpf(acc, e - es);
 }
 
 // out[m, n]; sa: token m's scale
 __device__ __forceinline__ void store_one(const Int8GemmParams& p, int m, int n, int acc, float sa) {
-  const float f = scaled(acc, sa * p.sb[n], p.bias != nullptr, p.bias ? p.bias[n] : 0.0f);
+  const float sb = p.sb[n];
+  float a = static_cast<float>(acc), s = sa * sb;
+  if (!scale_in_range(s)) factors_far(a, s, sa, sb);
+  const float f = scaled(a, s, p.bias != nullptr, p.bias ? p.bias[n] : 0.0f);
   const int64_t at = static_cast<int64_t>(m) * p.ldo + n;
   if (p.dtype == MOE_BF16) Bf16::put(p.out, at, f);
   else if (p.dtype == MOE_F16) F16::put(p.out, at, f);
@@ -388,28 +406,14 @@ __device__ __forceinline__ void clear_behind(uint8_t* rows, int c0, int K) {
 }
 
 // Lane's part of the result: tokens t0 + 16 m, channels n0 .. n0 + 4 FN - 1.
-template <typename T, int FM, int FN>
-__device__ __forceinline__ void store_tile(const Int8GemmParams& p, const i32x4 (&acc)[FN][FM], int t0, int n0) {
-  // (rows and vectors start anywhere: global memory is read and written in
-  // 16-byte pieces at any address; value by value 777 x 1003 x 1999 took 10.5 us,
-  // so 9.2)
-  float sb[4 * FN], bias[4 * FN] = {};
-  if (n0 <= p.N - 4 * FN) {
-    __builtin_memcpy(sb, p.sb + n0, sizeof(sb));
-    if (p.bias) __builtin_memcpy(bias, p.bias + n0, sizeof(bias));
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4 * FN; ++i) {
-      const int n = min(n0 + i, p.N - 1);
-      sb[i] = p.sb[n];
-      if (p.bias) bias[i] = p.bias[n];
-    }
-  }
+template <typename T, int FM, int FN, bool FAR>
+__device__ __forceinline__ void store_rows(const Int8GemmParams& p, const i32x4 (&acc)[FN][FM], int t0, int n0,
+                                           const float (&sa)[FM], const float (&sb)[4 * FN],
+                                           const float (&bias)[4 * FN]) {
 #pragma unroll
   for (int m = 0; m < FM; ++m) {
     const int t = t0 + 16 * m;
     if (t >= p.M) continue;
-    const float sa = p.sa[t];
     const int64_t row = static_cast<int64_t>(t) * p.ldo;
 #pragma unroll
     for (int f = 0; f < FN; f += 2) {
@@ -417,7 +421,9 @@ __device__ __forceinline__ void store_tile(const Int8GemmParams& p, const i32x4 
       float v[kP];
 #pragma unroll
       for (int i = 0; i < kP; ++i) {
-        v[i] = scaled(acc[f + i / 4][m][i % 4], sa * sb[4 * f + i], p.bias != nullptr, bias[4 * f + i]);
+        float a = static_cast<float>(acc[f + i / 4][m][i % 4]), s = sa[m] * sb[4 * f + i];
+        if constexpr (FAR) factors_far(a, s, sa[m], sb[4 * f + i]);
+        v[i] = scaled(a, s, p.bias != nullptr, bias[4 * f + i]);
       }
       const int n = n0 + 4 * f;
       if (n + kP <= p.N) {
@@ -430,6 +436,44 @@ __device__ __forceinline__ void store_tile(const Int8GemmParams& p, const i32x4 
       }
     }
   }
+}
+
+template <typename T, int FM, int FN>
+__device__ __forceinline__ void store_tile(const Int8GemmParams& p, const i32x4 (&acc)[FN][FM], int t0, int n0) {
+  // (rows and vectors start anywhere: global memory is read and written in
+  // 16-byte pieces at any address; value by value 777 x 1003 x 1999 took 10.5 us,
+  // so 9.2)
+  float sa[FM], sb[4 * FN], bias[4 * FN] = {};
+#pragma unroll
+  for (int m = 0; m < FM; ++m) sa[m] = p.sa[min(t0 + 16 * m, p.M - 1)];
+  if (n0 <= p.N - 4 * FN) {
+    __builtin_memcpy(sb, p.sb + n0, sizeof(sb));
+    if (p.bias) __builtin_memcpy(bias, p.bias + n0, sizeof(bias));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4 * FN; ++i) {
+      const int n = min(n0 + i, p.N - 1);
+      sb[i] = p.sb[n];
+      if (p.bias) bias[i] = p.bias[n];
+    }
+  }
+  // One wave's products of scales are hardly ever out of range, so the question
+  // is asked once, of the smallest and the largest.
+  float a0 = fabsf(sa[0]), a1 = a0, b0 = fabsf(sb[0]), b1 = b0;
+#pragma unroll
+  for (int m = 1; m < FM; ++m) {
+    a0 = fminf(a0, fabsf(sa[m]));
+    a1 = fmaxf(a1, fabsf(sa[m]));
+  }
+#pragma unroll
+  for (int i = 1; i < 4 * FN; ++i) {
+    b0 = fminf(b0, fabsf(sb[i]));
+    b1 = fmaxf(b1, fabsf(sb[i]));
+  }
+  if (__any(!scale_in_range(a0 * b0) || !scale_in_range(a1 * b1)))
+    store_rows<T, FM, FN, true>(p, acc, t0, n0, sa, sb, bias);
+  else
+    store_rows<T, FM, FN, false>(p, acc, t0, n0, sa, sb, bias);
 }
 
 template <int WM, int WN, int FM, int FN>
@@ -639,7 +683,7 @@ __global__ __launch_bounds__(kFewThreads) void int8_few_kernel(Int8GemmParams p,
   p.out = static_cast<char*>(p.out) + m0 * p.ldo * (p.dtype == MOE_F32 ? 4 : 2);
   p.M = min(p.M - m0, 16);
   const int S = (p.K + kStepBytes - 1) / kStepBytes, ls = S * kStepBytes + 16;
-  const int last = (p.K - 1) / 16 * 16;
+  int last = (p.K - 1) / 16 * 16;
   const int tiles = static_cast<int>((static_cast<int64_t>(p.N) + 15) / 16);
   const auto load = [&](i32x4 (&b)[kFewSteps][2], int tile) {  // past K: the last piece again, times zero
     const int8_t* row = p.b + min(static_cast<int64_t>(tile) * 16 + r, static_cast<int64_t>(p.N) - 1) * p.ldb;
@@ -705,6 +749,7 @@ __global__ __launch_bounds__(kFewThreads) void int8_few_kernel(Int8GemmParams p,
               b[i][h], *reinterpret_cast<const i32x4*>(xrow + step * kStepBytes + 64 * h), acc[0][0], 0, 0, 0);
       }
     }
+    asm volatile("" : "+s"(last));  // (the columns formed again here: the store needs the registers)
     if (tile + static_cast<int>(gridDim.x) < tiles) load(b, tile + gridDim.x);
     if (wave > 0) s_sum[wave - 1][lane] = acc[0][0];
     lds_barrier();
