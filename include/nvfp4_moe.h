@@ -205,8 +205,9 @@ int moe_block_norm(const moe_block_norm_args* args, void* stream);
  * weights [channels, in] a row per channel.
  *   scale = RN(amax / 127), code = RNE(RN(x * RN(127 / amax))), amax = max|x|
  *   of the row; a row with amax < 2^-119 has codes 0 and scale 1.
- *   x_dev      dtype [rows, ld_x], aligned to its element, ld_x >= cols; finite
- *              (an inf or NaN gives unspecified codes and scale for its row)
+ *   x_dev      dtype [rows, ld_x], aligned to its element, ld_x >= cols; a row
+ *              with an infinity or a NaN has scale NaN (its codes mean nothing),
+ *              so that its products are NaN
  *   rows       0 <= rows < 2^31 (0: no-op);  1 <= cols <= 2^30
  *   codes_dev  i8 [rows, ld_codes], 16-byte aligned, ld_codes a multiple of 16,
  *              >= cols (written; a row's last 16-byte piece is filled with

@@ -28,7 +28,8 @@ __device__ __forceinline__ u32x2 pack_codes(const float (&f)[8], float inv) {
   u32x2 r = {0u, 0u};
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    // |x inv| <= 127 (1 + 2^-23): the clamp only bounds a row with inf or NaN
+    // |x inv| <= 127 (1 + 2^-23): the clamp only bounds a row with an infinity or a
+    // NaN, whose codes mean nothing
     const int q = static_cast<int>(__builtin_amdgcn_fmed3f(__builtin_rintf(f[j] * inv), -127.0f, 127.0f));
     r[j / 4] |= (static_cast<uint32_t>(q) & 0xFFu) << (8 * (j % 4));
   }
@@ -61,12 +62,37 @@ __device__ __forceinline__ void load_piece(float (&f)[8], const void* row, int64
   }
 }
 
+// The larger of two magnitudes, NaN if one is.
+__device__ __forceinline__ float amax(float a, float b) { return __builtin_elementwise_maximum(a, b); }
 __device__ __forceinline__ float amax8(const float (&f)[8]) {
   float m = 0.0f;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(f[j]));
+  for (int j = 0; j < 8; ++j) m = amax(m, fabsf(f[j]));
   return m;
 }
+// The wave's largest magnitude, NaN if one is: bit patterns of magnitudes are
+// ordered as they are, infinity and NaN last.
+__device__ __forceinline__ float wave_amax(float m) {
+  uint32_t v = __float_as_uint(m) & 0x7FFFFFFFu;
+  v = max(v, dpp_u32<kDppXor1>(v));
+  v = max(v, dpp_u32<kDppXor2>(v));
+  v = max(v, dpp_u32<kDppHalfMirror>(v));
+  v = max(v, dpp_u32<kDppMirror>(v));
+  uint32_t a, b;
+  lane_pair<16>(v, a, b);
+  lane_pair<32>(max(a, b), a, b);
+  return __uint_as_float(max(a, b));
+}
+// A row's factor and scale from its largest magnitude.  A row with an infinity or
+// a NaN has the scale NaN, and so have its products.
+struct RowScale {
+  float inv, scale;
+  __device__ explicit RowScale(float am) {
+    const bool some = am >= kMinAmax && am <= 3.402823466e38f;
+    inv = some ? 127.0f / am : 0.0f;
+    scale = some ? am / 127.0f : am < kMinAmax ? 1.0f : __builtin_nanf("");
+  }
+};
 
 }  // namespace
 
@@ -89,22 +115,21 @@ __global__ __launch_bounds__(256) void int8_quantize_kernel(const void* __restri
   for (int i = 0; i < NC; ++i) load_piece<T, VEC>(f[i], xrow, 8 * (lt + TPR * i), cols);
   float am = 0.0f;
 #pragma unroll
-  for (int i = 0; i < NC; ++i) am = fmaxf(am, amax8(f[i]));
-  am = wave_max(am);
+  for (int i = 0; i < NC; ++i) am = amax(am, amax8(f[i]));
+  am = wave_amax(am);
   if constexpr (TPR > kWave) {
     if ((threadIdx.x & (kWave - 1)) == 0) s_am[threadIdx.x / kWave] = am;
     __syncthreads();
-    am = fmaxf(fmaxf(s_am[0], s_am[1]), fmaxf(s_am[2], s_am[3]));
+    am = amax(amax(s_am[0], s_am[1]), amax(s_am[2], s_am[3]));
   }
-  const bool some = am >= kMinAmax;
-  const float inv = some ? 127.0f / am : 0.0f;
+  const RowScale rs(am);
   int8_t* crow = codes + row * ld_codes;
 #pragma unroll
   for (int i = 0; i < NC; ++i) {
     const int c = 8 * (lt + TPR * i);
-    if (c < cols16) *reinterpret_cast<u32x2*>(crow + c) = pack_codes(f[i], inv);
+    if (c < cols16) *reinterpret_cast<u32x2*>(crow + c) = pack_codes(f[i], rs.inv);
   }
-  if (lt == 0) scales[row] = some ? am / 127.0f : 1.0f;
+  if (lt == 0) scales[row] = rs.scale;
 }
 
 // Longer rows: one block a row, two passes over it.
@@ -121,20 +146,19 @@ __global__ __launch_bounds__(256) void int8_quantize_long_kernel(const void* __r
   for (int64_t c = 8 * static_cast<int64_t>(threadIdx.x); c < cols; c += 8 * 256) {
     float f[8];
     load_piece<T, VEC>(f, xrow, c, cols);
-    am = fmaxf(am, amax8(f));
+    am = amax(am, amax8(f));
   }
-  am = wave_max(am);
+  am = wave_amax(am);
   if ((threadIdx.x & (kWave - 1)) == 0) s_am[threadIdx.x / kWave] = am;
   __syncthreads();
-  am = fmaxf(fmaxf(s_am[0], s_am[1]), fmaxf(s_am[2], s_am[3]));
-  const bool some = am >= kMinAmax;
-  const float inv = some ? 127.0f / am : 0.0f;
+  am = amax(amax(s_am[0], s_am[1]), amax(s_am[2], s_am[3]));
+  const RowScale rs(am);
   for (int64_t c = 8 * static_cast<int64_t>(threadIdx.x); c < cols16; c += 8 * 256) {
     float f[8];
     load_piece<T, VEC>(f, xrow, c, cols);
-    *reinterpret_cast<u32x2*>(codes + row * ld_codes + c) = pack_codes(f, inv);
+    *reinterpret_cast<u32x2*>(codes + row * ld_codes + c) = pack_codes(f, rs.inv);
   }
-  if (threadIdx.x == 0) scales[row] = some ? am / 127.0f : 1.0f;
+  if (threadIdx.x == 0) scales[row] = rs.scale;
 }
 
 template <typename T, bool VEC>
@@ -292,19 +316,18 @@ __global__ __launch_bounds__(kTokenThreads) void int8_token_kernel(Int8GemmParam
     load(b, n, 0);
     float am = 0.0f;
 #pragma unroll
-    for (int i = 0; i < NC; ++i) am = fmaxf(am, amax8(f[i]));
-    am = wave_max(am);
+    for (int i = 0; i < NC; ++i) am = amax(am, amax8(f[i]));
+    am = wave_amax(am);
     if (lane == 0) s_am[wave] = am;
     lds_barrier();  // (the channels' loads stay in flight)
 #pragma unroll
-    for (int w = 0; w < W; ++w) am = fmaxf(am, s_am[w]);
-    const bool some = am >= kMinAmax;
-    const float inv = some ? 127.0f / am : 0.0f;
-    scale = some ? am / 127.0f : 1.0f;
+    for (int w = 0; w < W; ++w) am = amax(am, s_am[w]);
+    const RowScale rs(am);
+    scale = rs.scale;
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
       const int c = 8 * (tid + kTokenThreads * i);
-      if (c < kib) *reinterpret_cast<u32x2*>(s_codes + c) = pack_codes(f[i], inv);
+      if (c < kib) *reinterpret_cast<u32x2*>(s_codes + c) = pack_codes(f[i], rs.inv);
     }
   }
   lds_barrier();
@@ -713,24 +736,22 @@ __global__ __launch_bounds__(kFewThreads) void int8_few_kernel(Int8GemmParams p,
 #pragma unroll
   for (int i = 0; i < kFewPieces; ++i) {
     const int u = TWO && i >= kFewPieces / 2 ? 1 : 0;
-    am[u] = fmaxf(am[u], amax8(f[i]));
+    am[u] = amax(am[u], amax8(f[i]));
   }
-  am[0] = wave_max(am[0]);
+  am[0] = wave_amax(am[0]);
   if constexpr (TWO) {
-    am[1] = wave_max(am[1]);
+    am[1] = wave_amax(am[1]);
   } else {
     if (lane == 0) s_am[wave] = am[0];
     lds_barrier();  // (the weights' loads stay in flight)
-    for (int j = 0; j < share; ++j) am[0] = fmaxf(am[0], s_am[wave / share * share + j]);
+    for (int j = 0; j < share; ++j) am[0] = amax(am[0], s_am[wave / share * share + j]);
   }
 #pragma unroll
   for (int i = 0; i < kFewPieces; ++i) {
-    const float a = am[TWO && i >= kFewPieces / 2 ? 1 : 0];
-    const bool some = a >= kMinAmax;
-    const float inv = some ? 127.0f / a : 0.0f;
+    const RowScale rs(am[TWO && i >= kFewPieces / 2 ? 1 : 0]);
     const int row = row_of(i), c = col_of(i);
-    if (row < p.M && c < S * kStepBytes) *reinterpret_cast<u32x2*>(s_codes + row * ls + c) = pack_codes(f[i], inv);
-    if (row < p.M && c == 0) s_scale[row] = some ? a / 127.0f : 1.0f;
+    if (row < p.M && c < S * kStepBytes) *reinterpret_cast<u32x2*>(s_codes + row * ls + c) = pack_codes(f[i], rs.inv);
+    if (row < p.M && c == 0) s_scale[row] = rs.scale;
   }
   lds_barrier();
 
