@@ -251,7 +251,8 @@ def token_ceiling(max_prefill, piecewise_max, graph_max_bs, spec_draft_tokens) -
 #
 # Each works on its tensors' device, which need not be the current one, on
 # `stream` (default: that device's current stream).  Tensors a call makes
-# belong to the stream it ran on.  The calls serve single tokens, whose kernels
+# belong to the stream it ran on.  None has a gradient: a tensor that requires one
+# is refused where gradients are on.  The calls serve single tokens, whose kernels
 # take a few microseconds, so their checks, the allocation of their results and
 # the launch are native code (csrc/torch_calls.cpp).
 

@@ -6,7 +6,7 @@
 // fields, and the results are allocated without Python's argument parsing.  The
 // launch itself is 2.4 us of what remains.
 //
-// Checks of types, shapes, strides and devices stand here and raise ValueError;
+// Checks of types, shapes, strides, devices and gradients stand here and raise ValueError;
 // everything else (ranges, alignment, overlap) is the library's, whose status
 // becomes the binding's error.  A call runs on its tensors' device and on that
 // device's current stream, and makes its results there.
@@ -16,6 +16,7 @@
 
 #include <ATen/ops/empty.h>
 #include <c10/core/DeviceGuard.h>
+#include <c10/core/GradMode.h>
 
 #include <algorithm>
 #include <climits>
@@ -55,6 +56,9 @@ const Tensor& tensor(PyObject* o, const char* name) {
   TORCH_CHECK_VALUE(THPVariable_Check(o), name, " must be a CUDA tensor");
   const Tensor& t = THPVariable_Unpack(o);
   TORCH_CHECK_VALUE(t.is_cuda() && t.layout() == at::kStrided, name, " must be a CUDA tensor");
+  // (the operators have no gradient: a result would leave the graph unnoticed)
+  TORCH_CHECK_VALUE(!t.requires_grad() || !c10::GradMode::is_enabled(), name,
+                    " requires a gradient, which this operator does not have (torch.no_grad() or detach it)");
   return t;
 }
 
