@@ -235,6 +235,14 @@ int int8_matmul(const void* a_dev, int64_t lda, const float* scale_a_dev, const 
                 int32_t dtype, int64_t ldo, void* stream);
 
 /*
+ * Which of int8_matmul's kernels these sizes take (host-only; for tests and
+ * tuning, the result is the same in each): 0 the one-token kernel, else tiles of
+ * tokens x channels: 1 16 x 16, 2 16 x 32, 3 32 x 32, 4 64 x 32, 5 64 x 64, 6 128 x
+ * 128 by two groups of waves, 7 128 x 128, 8 256 x 256.  M and N >= 1.
+ */
+int int8_matmul_kernel(int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldb, int32_t* kernel);
+
+/*
  * int8_quantize_per_token of x (dtype [M, ld_x], K columns) and int8_matmul
  * with the channel rows w, in one call.  The codes and scales are kept in
  * caller-owned scratch memory: workspace_dev, 16-byte aligned, of at least

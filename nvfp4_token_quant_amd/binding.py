@@ -140,6 +140,8 @@ def lib():
         L.int8_quantize_per_token.argtypes = [_P, _I32, _I64, _I64, _I64, _P, _I64, _P, _P]
         L.int8_matmul.restype = ctypes.c_int
         L.int8_matmul.argtypes = [_P, _I64, _P, _P, _I64, _P, _P, _I64, _I64, _I64, _P, _I32, _I64, _P]
+        L.int8_matmul_kernel.restype = ctypes.c_int
+        L.int8_matmul_kernel.argtypes = [_I64, _I64, _I64, _I64, _I64, ctypes.POINTER(_I32)]
         L.int8_linear.restype = ctypes.c_int
         L.int8_linear.argtypes = [_P, _I32, _I64, _P, _I64, _P, _P, _I64, _I64, _I64, _P, _I64, _P, _I32, _I64, _P]
         L.int8_linear_workspace.restype = ctypes.c_int

@@ -958,14 +958,11 @@ static double rounds(int64_t tiles, int64_t slots) {
   return 0.5 * (static_cast<double>((tiles + slots - 1) / slots) + (t > 1.0 ? t : 1.0));
 }
 
-hipError_t launch_int8_matmul(const Int8GemmParams& p, hipStream_t s) {
-  if (p.M == 1 && p.K <= kLinearTokenMaxK) {
-    launch_token<Codes>(p, nullptr, s);
-    return hipGetLastError();
-  }
+int choose_int8_kernel(int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldb) {
+  if (M == 1 && K <= kLinearTokenMaxK) return 0;
   // Rows far apart: a tile's rows are addressed with 32-bit byte offsets, and
   // these tiles have the fewest.
-  if (p.lda > kMaxTileLd || p.ldb > kMaxTileLd) return launch_ring<1, 1, 1, 2, 4, 3, 2>(p, s);
+  if (lda > kMaxTileLd || ldb > kMaxTileLd) return 2;
   // What a round of each tile takes, in microseconds: for each 128 bytes of K and
   // for the rest (first loads, sums, output), where every tile has a CU to itself
   // and (_full) where there are more tiles than CUs.  Fitted to 61 sizes of 17 to 16384 tokens;
@@ -976,21 +973,26 @@ hipError_t launch_int8_matmul(const Int8GemmParams& p, hipStream_t s) {
       {32, 32, 512, 0.13, 0.6, 0.186, 1.95},   {64, 32, 256, 0.145, 1.45, 0.163, 2.6},
       {64, 64, 256, 0.226, 1.4, 0.262, 2.5},   {128, 128, 256, 0.58, 3.7, 0.66, 5.1},
       {128, 128, 512, 0.70, 1.4, 1.0, 3.5},    {256, 256, 256, 1.27, 5.3, 1.6, 5.3}};
-  const double steps = (p.K + kStepBytes - 1) / kStepBytes;
+  const double steps = static_cast<double>((K + kStepBytes - 1) / kStepBytes);
   double cost[std::size(kTiles)];
   for (size_t i = 0; i < std::size(kTiles); ++i) {
     const auto& t = kTiles[i];
-    const int64_t tiles = ((static_cast<int64_t>(p.M) + t.bm - 1) / t.bm) * ((static_cast<int64_t>(p.N) + t.bn - 1) / t.bn);
+    const int64_t tiles = ((M + t.bm - 1) / t.bm) * ((N + t.bn - 1) / t.bn);
     cost[i] = tiles <= 256 ? steps * t.step + t.rest : (steps * t.step_full + t.rest_full) * rounds(tiles, t.slots);
   }
-  switch (std::min_element(std::begin(cost), std::end(cost)) - std::begin(cost)) {
-    case 0: return launch_ring<1, 1, 1, 1, 8, 4, 1>(p, s);
-    case 1: return launch_ring<1, 1, 1, 2, 4, 3, 2>(p, s);
-    case 2: return launch_ring<1, 1, 2, 2, 4, 2, 2>(p, s);
-    case 3: return launch_ring<2, 1, 2, 2, 4, 3, 1>(p, s);
-    case 4: return launch_ring<2, 2, 2, 2, 2, 4, 1>(p, s);
-    case 5: return launch_ring<2, 2, 4, 4, 2, 2, 1>(p, s);
-    case 6: return launch_ring<2, 4, 4, 2, 1, 2, 2>(p, s);
+  return 1 + static_cast<int>(std::min_element(std::begin(cost), std::end(cost)) - std::begin(cost));
+}
+
+hipError_t launch_int8_matmul(const Int8GemmParams& p, hipStream_t s) {
+  switch (choose_int8_kernel(p.M, p.N, p.K, p.lda, p.ldb)) {
+    case 0: launch_token<Codes>(p, nullptr, s); return hipGetLastError();
+    case 1: return launch_ring<1, 1, 1, 1, 8, 4, 1>(p, s);
+    case 2: return launch_ring<1, 1, 1, 2, 4, 3, 2>(p, s);
+    case 3: return launch_ring<1, 1, 2, 2, 4, 2, 2>(p, s);
+    case 4: return launch_ring<2, 1, 2, 2, 4, 3, 1>(p, s);
+    case 5: return launch_ring<2, 2, 2, 2, 2, 4, 1>(p, s);
+    case 6: return launch_ring<2, 2, 4, 4, 2, 2, 1>(p, s);
+    case 7: return launch_ring<2, 4, 4, 2, 1, 2, 2>(p, s);
     default: return launch_tiled<2, 4, 8, 4>(p, s);
   }
 }

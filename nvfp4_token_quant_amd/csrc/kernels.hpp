@@ -205,6 +205,8 @@ struct Int8GemmParams {
   int M, N, K, dtype;
 };
 hipError_t launch_int8_matmul(const Int8GemmParams& p, hipStream_t s);
+// Which kernel that takes (numbered as in int8_matmul_kernel).
+int choose_int8_kernel(int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldb);
 // One token (M = 1, K <= kLinearTokenMaxK) from its unquantized row x; p.a and
 // p.sa are not read.
 constexpr int kLinearTokenMaxK = 32768;

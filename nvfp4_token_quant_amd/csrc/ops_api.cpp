@@ -74,11 +74,7 @@ int run_quantize(const void* x_dev, int32_t dtype, int64_t rows, int64_t cols, i
   return api_ok();
 }
 
-int check_matmul(const void* a_dev, int64_t lda, const float* scale_a_dev, const void* b_dev, int64_t ldb,
-                 const float* scale_b_dev, const float* bias_dev, int64_t M, int64_t N, int64_t K, const void* out_dev,
-                 int32_t dtype, int64_t ldo) {
-  const int64_t bytes = dtype_bytes(dtype);
-  if (!bytes) return api_fail(NVFP4_ERR_INVALID_ARG, "unknown dtype %d", dtype);
+int check_matmul_sizes(int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldb) {
   // (the last tile's row and channel numbers also stay below 2^31)
   if (M < 0 || N < 0 || M > INT32_MAX - 512 || N > INT32_MAX - 512)
     return api_fail(NVFP4_ERR_INVALID_ARG, "M and N must be in [0, 2^31 - 512) (got %lld, %lld)", (long long)M,
@@ -92,6 +88,16 @@ int check_matmul(const void* a_dev, int64_t lda, const float* scale_a_dev, const
   if (lda > (int64_t(1) << 26) || ldb > (int64_t(1) << 26))
     return api_fail(NVFP4_ERR_INVALID_ARG, "lda and ldb must be <= 2^26 (got %lld, %lld)", (long long)lda,
                     (long long)ldb);
+  return NVFP4_OK;
+}
+
+int check_matmul(const void* a_dev, int64_t lda, const float* scale_a_dev, const void* b_dev, int64_t ldb,
+                 const float* scale_b_dev, const float* bias_dev, int64_t M, int64_t N, int64_t K, const void* out_dev,
+                 int32_t dtype, int64_t ldo) {
+  const int64_t bytes = dtype_bytes(dtype);
+  if (!bytes) return api_fail(NVFP4_ERR_INVALID_ARG, "unknown dtype %d", dtype);
+  const int st = check_matmul_sizes(M, N, K, lda, ldb);
+  if (st != NVFP4_OK) return st;
   if (ldo < N) return api_fail(NVFP4_ERR_INVALID_ARG, "ldo must be >= N (got %lld)", (long long)ldo);
   if (M == 0 || N == 0) return NVFP4_OK;
   if (!a_dev || !b_dev || !scale_a_dev || !scale_b_dev || !out_dev)
@@ -320,6 +326,14 @@ int int8_matmul(const void* a_dev, int64_t lda, const float* scale_a_dev, const 
   if (st != NVFP4_OK) return st;
   if (M == 0 || N == 0) return api_ok();
   return run_matmul(a_dev, lda, scale_a_dev, b_dev, ldb, scale_b_dev, bias_dev, M, N, K, out_dev, dtype, ldo, stream);
+}
+
+int int8_matmul_kernel(int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldb, int32_t* kernel) {
+  const int st = check_matmul_sizes(M, N, K, lda, ldb);
+  if (st != NVFP4_OK) return st;
+  if (M == 0 || N == 0 || !kernel) return api_fail(NVFP4_ERR_INVALID_ARG, "M and N must be >= 1, kernel not NULL");
+  *kernel = choose_int8_kernel(M, N, K, lda, ldb);
+  return api_ok();
 }
 
 int int8_linear_workspace(int64_t M, int64_t K, int64_t* bytes) {
