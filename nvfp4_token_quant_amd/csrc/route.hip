@@ -359,9 +359,8 @@ __global__ __launch_bounds__(256) void moe_route_scores_kernel(RouteParams q) {
     for (int i = 0; i < KPL; ++i) val[i] = v[i] > kNegInf ? val[i] : kNegInf64;
   } else {
     if (sums) {
-      // (binary32 exponentials: they only scale the weights and order nothing)
 #pragma unroll
-      for (int i = 0; i < KPL; ++i) val[i] = static_cast<double>(expf(v[i] - m));
+      for (int i = 0; i < KPL; ++i) val[i] = exp64(fmax(static_cast<double>(v[i]) - static_cast<double>(m), -1200.0));
       z = exp_sum<LANES>(val);
     }
 #pragma unroll
