@@ -115,9 +115,12 @@ typedef enum moe_score { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_scor
  *   ids:    the k best of the experts that stay, best first, ties to the
  *           lower index
  *   w_j  =  s_{id_j}, over the sum of the k with renormalize, times scale
- * The order is decided in binary64; values v within 2^-41 of their size may
- * count as equal, sigmoid scores below e^-709 count as that.  An expert is masked where its logit or its bias is -inf or
- * NaN (+inf counts as FLT_MAX); masked experts and those of dropped groups
+ * The order is decided in binary64: values v that differ by less than 2^-40 of
+ * the larger of score and |bias| may change places (equal logits with equal
+ * biases do not), sigmoid scores below e^-709 count as that, softmax scores below
+ * e^-708 of the row's largest lose bits, below e^-745 they are 0.  A token's ids and weights do not depend on
+ * the batch that it comes with.  An expert is masked where its logit or its bias
+ * is -inf or NaN (+inf counts as FLT_MAX); masked experts and those of dropped groups
  * come after all others, lower index first, with weight 0, so a token always
  * has k different experts; a token without any has k weights of 0.  The
  * weights are formed in binary64 and rounded once.
@@ -226,7 +229,7 @@ int int8_quantize_per_token(const void* x_dev, int32_t dtype, int64_t rows, int6
  *             aligned, lda and ldb multiples of 16, >= K, <= 2^26; whole 16-byte
  *             pieces are read, bytes behind K have no effect
  *   scale_a_dev f32 [M], scale_b_dev f32 [N], bias_dev f32 [N] or NULL
- *   M, N, K   0 <= M, N < 2^31 (0: no-op);  1 <= K <= 131071 (the sum's range)
+ *   M, N, K   0 <= M, N < 2^31 - 512 (0: no-op);  1 <= K <= 131071 (the sum's range)
  *   out_dev   dtype [M, ldo], ldo >= N, aligned to its element; must not
  *             overlap an input (NVFP4_ERR_ALIAS)
  */

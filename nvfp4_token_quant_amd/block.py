@@ -40,8 +40,10 @@ class MoeBlock:
 
     def forward(self, residual, h=None, next_before=None):
         """residual [T, H], bf16 or f32; h bf16 [T, H]: before(residual) if the
-        pass that made the residual gave it already.  -> (r', h'), h' None
-        without `next_before` (a binding.Norm)."""
+        pass that made the residual gave it already (that pass normed the
+        residual before rounding it, so with a bf16 residual the two differ by
+        that rounding).  -> (r', h'), h' None without `next_before` (a
+        binding.Norm)."""
         if h is None:
             h = torch.empty(residual.shape, dtype=torch.bfloat16, device=residual.device)
             _, h = binding.block_norm(residual, before=self.before, h_out=h)

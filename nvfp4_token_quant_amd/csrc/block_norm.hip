@@ -254,8 +254,10 @@ static void launch_norm_shape(const BlockNormParams& p, hipStream_t s) {
 // (7168 columns: 3.8 us with 1024 threads, 4.5 with 256 of four pieces) and as
 // fast with many (16384 rows: 252 and 257 us).  Narrow rows share a block; in
 // large batches a wave takes one of up to 1024 columns by itself, without a
-// barrier (4096 x 1000: 8.8 us, with two waves a row 9.5; 1027 x 1001: 6.3 and
-// 5.8).
+// barrier (RMS, bf16, 1024 columns: 3000 rows 6.3 us, with two waves a row 6.9;
+// 4096 8.0 and 8.7; 512 3.6 and 3.5.  Layer norms, binary32, 1001 columns with an
+// element gate: 1027 rows 8.2 and 7.2, 4096 19.2 and 18.1, from memory 23.2 and
+// 22.9).
 template <typename T, typename R, bool VEC>
 static void launch_norm_width(const BlockNormParams& p, hipStream_t s) {
   const int w = p.cols;

@@ -2,8 +2,9 @@
 //
 //   quantize: s = RN(amax / 127), q = RNE(x * RN(127 / amax)) of a row
 //   product:  out[m, n] = sa[m] sb[n] sum_k a[m, k] b[n, k] + bias[n]
-// The sum is exact in int32 for K < 2^31 / 128^2; it is converted to binary32
-// once, scaled there and rounded once to the output's type.
+// The sum is exact in int32 for K < 2^31 / 128^2.  In binary32 it is rounded,
+// multiplied by the rounded product of its scales and, in one rounding, added to
+// the bias; that is rounded to the output's type.
 #include <algorithm>
 #include <atomic>
 #include <iterator>

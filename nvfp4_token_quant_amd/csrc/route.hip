@@ -12,10 +12,14 @@
 // Precision.  The order of two experts is decided by v in binary64: a
 // prefill batch compares millions of neighbouring values, and in binary32
 // (2^-24 around 1) some of them change places.  Ten bits of a candidate hold
-// the expert, so values nearer than 2^-42 of their size count as equal.
-// Without a bias v has the logits' order and the candidate is made of the
-// logit itself.  Group scores are binary64 sums.  The k weights of a token are
-// formed in binary64 and rounded once to binary32.
+// the expert, which takes 2^-42 of a value's size; scores are off by at most
+// 2^-42 of theirs (exp64, recip64, the sum), so values that differ by less than
+// 2^-40 of the larger of score and bias may change places.  Experts of equal
+// logits and biases have equal values, the same in every batch.  Without a bias
+// v has the logits' order and the candidate is made of the logit itself.  Group
+// scores are binary64 sums.  The k weights of a token are formed in binary64 and
+// rounded once to binary32 (a softmax sum of binary32 exponentials would put them up
+// to 10 roundings off and saves little: 16384 tokens of 256 experts 9.2 us for 10.2).
 //
 // Work.  The bytes are T * E logits, read once; what bounds the kernel is
 // vector work: with a bias (or groups by two values) one binary64
@@ -24,9 +28,9 @@
 // tokens a wave) or, for few tokens or more than 432 experts, the whole wave; a
 // lane's experts are consecutive, so that groups of whole lanes are reduced in
 // registers (through LDS: 2.7 us more of the 18.5).  16384 tokens of 256 experts
-// take 15.7 us with bias and groups (1960 vector instructions for four tokens),
-// 7.9 without (floor of the bytes: 3.7); one token of 128 experts 2.9 us, 64 of 256
-// in groups 4.6.
+// take 15.2 us with bias and groups (1610 vector instructions for four tokens),
+// 7.4 without (floor of the bytes: 3.7); one token of 128 experts 2.9 us, 64 of 256
+// in groups 4.7 (replayed; single calls take 16.1 and 5.0).
 #include "common.hpp"
 #include "dtype.hpp"
 #include "kernels.hpp"
@@ -61,8 +65,11 @@ __device__ __forceinline__ void load_row(float (&v)[KPL], const void* p, int64_t
 // NaN counts as masked, +inf as the largest finite value.
 __device__ __forceinline__ float clean(float v) { return v >= kNegInf ? fminf(v, kF32Max) : kNegInf; }
 
-// exp(x) in binary64 to 2^-47 of it, x in [-1200, 709]: x = n ln 2 + r with |r| <=
-// ln 2 / 2, e^r by its series to r^11 (the rest is below r^12 / 12!).  0 below -745.
+// exp(x) in binary64 to 2^-46 of it, x in [-1200, 709]: x = n ln 2 + r with |r| <=
+// ln 2 / 2, ln 2 subtracted in two parts of which n times the first is exact (W. J.
+// Cody and W. Waite, "Software Manual for the Elementary Functions", 1980), e^r by
+// its series to r^11 (the rest, r^12 / 12!, is below 2^-46.6 of it).  Below -708 with
+// the absolute error of a subnormal number, 0 below -745.
 __device__ __forceinline__ double exp64(double x) {
   const double n = __builtin_rint(x * 1.4426950408889634);
   const double r = __builtin_fma(n, -1.9082149292705877e-10, __builtin_fma(n, -0.693147180369123816490, x));
@@ -499,8 +506,8 @@ static void launch_scores(RouteParams q, hipStream_t s) {
 }
 
 // Few tokens wait for each step of their chain, many for the vector ALU (1000
-// experts, k = 16: 64 tokens 7.4 us by swaps, 8.2 by shuffles; 16384: 62.4 and 60.5;
-// 300 experts, a wave a token: 16384 34.7 and 31.7).
+// experts with a bias, k = 16: 64 tokens 7.2 us by swaps, 8.1 by shuffles; 16384
+// 57.8 and 54.0).
 template <int KPL>
 static void launch_wave_scores(const RouteParams& q, hipStream_t s) {
   if (q.T <= kRouteWaveTokens) launch_scores<KPL, Lanes::kSwap>(q, s);
@@ -515,17 +522,17 @@ static_assert(8 * 16 * (kMaxRouteGroups + kRouteRowExperts + 16) <= 64 * 1024, "
 hipError_t launch_route_scores(const RouteParams& q, hipStream_t s) {
   // A whole wave a token where 16 lanes would hold many experts each and the
   // batch does not fill the chip (256 experts in groups with a bias: 1 token
-  // 4.5 us, with 16 lanes 7.8; 2048: 6.0 and 8.4; 4096: 9.4 and 8.6.  300, k = 16:
-  // 2048 tokens 8.0 and 8.8, 4096 11.4 and 9.0, 16384 31.5 and 19.2; 384 with a
-  // bias 8.5 and 13.0, 13.3 and 13.3, 39.0 and 35.4).
+  // 4.4 us, with 16 lanes 6.3; 2048: 5.9 and 6.9; 4096: 8.7 and 7.0.  300, k = 16:
+  // 2048 tokens 5.7 and 5.8, 4096 8.7 and 5.8, 16384 26.2 and 12.0; 384 in groups
+  // with a bias 7.9 and 12.8, 12.7 and 13.2, 37.7 and 34.2).
   if (q.E > kRouteRowExperts || (q.E > 128 && q.T <= kRouteWaveTokens)) {
     if (q.E <= 256) launch_scores<4, Lanes::kSwap>(q, s);
     else if (q.E <= 320) launch_scores<5, Lanes::kSwap>(q, s);
     else if (q.E <= 512) launch_wave_scores<8>(q, s);
     else launch_wave_scores<16>(q, s);
   } else {
-    // (16384 tokens of 160 experts in two groups: 10 a lane 10.9 us, 16 a lane 16.0;
-    // 192 in groups with a bias: 12 a lane 13.0, 16 a lane 18.8)
+    // (16384 tokens of 160 experts in two groups, k = 16: 10 a lane 10.9 us, 16 a lane
+    // 16.0; 192 in groups with a bias: 12 a lane 12.4, 16 a lane 18.8)
     if (q.E <= 16) launch_scores<1, Lanes::kRow>(q, s);
     else if (q.E <= 32) launch_scores<2, Lanes::kRow>(q, s);
     else if (q.E <= 64) launch_scores<4, Lanes::kRow>(q, s);
