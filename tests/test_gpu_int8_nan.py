@@ -2,7 +2,9 @@
 import pytest
 import torch
 
-from nvfp4_token_quant_amd import binding
+from nvfp4_token_quant_amd import binding, synth
+from nvfp4_token_quant_amd.block import MoeBlock
+from tests.layer_fixtures import gpu_weights
 
 pytestmark = pytest.mark.gpu
 
@@ -47,3 +49,28 @@ def test_linear_keeps_broken_rows(M, N, K, dtype):
         torch.cuda.synchronize()
         assert torch.isnan(got[bad]).all()
         assert torch.equal(got[~bad], want[~bad])
+
+
+@pytest.mark.parametrize("T", [6, 100])
+@pytest.mark.parametrize("score", [None, "sigmoid"])
+def test_block_keeps_a_broken_row_to_itself(T, score):
+    """A NaN in one token's residual: its router logits are NaN, its output is NaN, and no other token's changes."""
+    print(f"block with a broken row T={T} router {score}", flush=True)
+    L = synth.LAYERS[1]
+    g = torch.Generator().manual_seed(T)
+    layer = binding.MoeLayer(T, L.H, L.I, L.E, L.k, True)
+    layer.bind(gpu_weights(1))
+    if score:
+        layer.set_router(binding.Router(score=score, groups=4, top_groups=2))
+    wg, sg = binding.int8_quantize_per_token((torch.randn((L.E, L.H), generator=g) * L.H ** -0.5).cuda())
+    n = binding.Norm((1 + 0.2 * torch.randn(L.H, generator=g)).to(BF16).cuda())
+    block = MoeBlock(layer, wg, sg, n)
+    r = torch.randn((T, L.H), generator=g).to(BF16).cuda()
+    want, wh = block.forward(r, next_before=n)
+    r[T // 2, 3] = float("nan")
+    got, gh = block.forward(r, next_before=n)
+    torch.cuda.synchronize()
+    rest = torch.arange(T, device="cuda") != T // 2
+    assert torch.equal(got[rest], want[rest]) and torch.equal(gh[rest], wh[rest])
+    assert torch.isnan(got[T // 2, 3]) and torch.isnan(gh[T // 2]).all()
+    layer.close()
