@@ -265,6 +265,128 @@ int int8_linear(const void* x_dev, int32_t dtype, int64_t ld_x, const void* w_de
 int int8_linear_workspace(int64_t M, int64_t K, int64_t* bytes);
 
 /* ---------------------------------------------------------------------- */
+/* The attention half of a block: a key-value cache in 8 bits, new tokens into */
+/* it, attention over it, its values, and sequences that continue others       */
+/* ---------------------------------------------------------------------- */
+
+/*
+ * The cache of one layer, in caller-owned device memory that is zero before the
+ * first append.  A page holds page_size tokens of one sequence for all kv heads.
+ * When the last token of a page arrives, the page's keys and its values of each
+ * head are quantized, each with one scale:
+ *   scale = RN(amax / 127), code = RNE(RN(x * RN(127 / amax))), amax = max|x|;
+ *   amax < 2^-119: codes and scale 0; an infinity or a NaN: scale NaN, so that
+ *   all of it is NaN.
+ * The tokens of a sequence's last, incomplete page are held as they came, in its
+ * slot (bf16 and fp16 values exactly, except values under 2^-29 of their token's
+ * largest, which are within 2^-40 of it; a token with an infinity or a NaN is NaN
+ * throughout its head).  So every value is rounded once, from what was given; the
+ * cache's contents do not depend on how a sequence's tokens were split over calls;
+ * and full pages never change: sequences may share them.
+ *   num_pages    1 .. 2^31 - 1         num_slots  1 .. 2^31 - 1
+ *   kv_heads     1 .. 1024             head_dim   64, 128, 192 or 256
+ *   page_size    16, 32, 64 or 128
+ *   codes_dev        u8  [num_pages, 2, kv_heads, page_size * head_dim]
+ *   scales_dev       f32 [num_pages, 2, kv_heads]
+ *   tails_dev        u16 [num_slots, 2, kv_heads, page_size * head_dim]
+ *   tail_scales_dev  f32 [num_slots, 2, kv_heads, page_size]
+ * 16-byte aligned.  Keys come first, then values; the order inside a page is the
+ * kernels' (kv_read gives the values).
+ */
+typedef struct kv_cache {
+  int64_t num_pages, num_slots;
+  int32_t kv_heads, head_dim, page_size;
+  void* codes_dev;
+  float* scales_dev;
+  void* tails_dev;
+  float* tail_scales_dev;
+} kv_cache;
+
+/*
+ * A step of a batch: sequence i had lens[i] tokens and now gets the call's tokens
+ * cu[i] .. cu[i + 1] - 1 (with cu_dev NULL: token i, tokens = entries), at the
+ * positions from lens[i] on.  All calls of a step take the same batch.
+ *   table_dev  i32 [entries, ld_table]: the pages of each sequence in order;
+ *              table_width of them, ld_table >= table_width, are the call's
+ *   lens_dev, slots_dev   i32 [entries];  cu_dev   i32 [entries + 1] or NULL
+ *   entries, tokens >= 0 (either 0: no-op), table_width * page_size <= 2^30
+ * These are read on the device, so that a captured step follows their new values.
+ * An entry whose slot or length is negative is padding: it has no tokens.  Numbers
+ * outside the cache or the call's tensors are never followed: an entry whose slot,
+ * length or first token is outside is padding too, tokens behind the table's last
+ * page or the call's last token are dropped, a page outside the cache keeps nothing
+ * and holds nothing that attention sees (kv_read gives 0).  The outputs of tokens that belong
+ * to no entry are left as they were.  cu has to be ascending; entries of an append
+ * have different slots, and pages that they complete are theirs alone.
+ */
+typedef struct kv_batch {
+  int64_t entries, tokens;
+  const int32_t* table_dev;
+  int64_t table_width, ld_table;
+  const int32_t* lens_dev;
+  const int32_t* slots_dev;
+  const int32_t* cu_dev;
+} kv_batch;
+
+/*
+ * The step's keys and values into the cache.
+ *   k_dev, v_dev  dtype (MOE_BF16 or MOE_F16) [tokens, kv_heads, head_dim], tokens
+ *                 ld_k / ld_v and heads ld_k_head / ld_v_head elements apart
+ *                 (multiples of 8), 16-byte aligned
+ * They must not overlap the cache (NVFP4_ERR_ALIAS).
+ */
+int kv_append(const kv_cache* cache, const kv_batch* batch, const void* k_dev, int64_t ld_k, int64_t ld_k_head,
+              const void* v_dev, int64_t ld_v, int64_t ld_v_head, int32_t dtype, void* stream);
+
+/*
+ * Attention of the step's tokens over the cache, which holds their own keys and
+ * values already: with t at position p of its sequence and kv head h / (heads / kv_heads),
+ *   out[t, h] = sum_j softmax_j(scale q[t, h] . k_j) v_j,   p - window < j <= p
+ * (window 0: j <= p); a token that sees no key has output 0.  k_j, v_j: the values that the
+ * cache holds.  Scores, maxima and sums are binary32; a softmax weight is rounded to
+ * 11 bits before it multiplies a value; the result is rounded to dtype once.
+ * Scores beyond binary32's range, and q with an infinity or a NaN, give NaN.
+ *   q_dev    dtype (MOE_BF16 or MOE_F16) [tokens, heads, head_dim], strides as in kv_append
+ *   heads    a multiple of kv_heads, at most 64 times as many
+ *   scale    finite;  window >= 0
+ *   workspace_dev  16-byte aligned, of at least kv_attention_workspace bytes (may be
+ *            NULL for 0), used by one call at a time (calls on one stream may share
+ *            it, calls that overlap and graphs that replay together may not)
+ *   out_dev  dtype [tokens, heads, head_dim], strides as in kv_append; overlaps nothing
+ *            else (NVFP4_ERR_ALIAS)
+ * A long sequence's keys are cut into pieces by the lengths of all entries, so the last
+ * bits of a token's result can depend on the batch; equal calls give equal bits.
+ */
+int kv_attention(const kv_cache* cache, const kv_batch* batch, const void* q_dev, int64_t ld_q, int64_t ld_q_head,
+                 int32_t heads, int32_t dtype, float scale, int64_t window, void* workspace_dev, int64_t workspace_bytes,
+                 void* out_dev, int64_t ld_out, int64_t ld_out_head, void* stream);
+
+/* Bytes of kv_attention's workspace (its pointers are not read).  Host-only. */
+int kv_attention_workspace(const kv_cache* cache, const kv_batch* batch, int32_t heads, int64_t* bytes);
+
+/*
+ * The step's keys and values as the cache holds them: code * scale, or the tail's
+ * value, rounded to dtype (MOE_BF16, MOE_F16 or MOE_F32).  The batch's tokens are the
+ * last ones of their sequences.
+ *   k_out_dev, v_out_dev   dtype [tokens, kv_heads, head_dim], dense, 16-byte aligned;
+ *                          overlap nothing else (NVFP4_ERR_ALIAS)
+ */
+int kv_read(const kv_cache* cache, const kv_batch* batch, void* k_out_dev, void* v_out_dev, int32_t dtype, void* stream);
+
+/*
+ * For each of `pairs` pairs: entry dst continues what entry src holds (the lengths in
+ * lens; cu and tokens are not read).  Full pages are shared: the first
+ * lens[src] / page_size entries of src's table row are copied to dst's row, the others
+ * stay; lens[dst] becomes lens[src]; the tokens of an incomplete page are copied from
+ * src's slot to dst's.  table_dev and lens_dev are written.
+ *   src_dev, dst_dev   i32 [pairs]; a pair with a number outside the entries, or with
+ *            src = dst, does nothing; no dst is another pair's src or dst, and its slot is
+ *            no other entry's
+ */
+int kv_fork(const kv_cache* cache, const kv_batch* batch, const int32_t* src_dev, const int32_t* dst_dev, int64_t pairs,
+            void* stream);
+
+/* ---------------------------------------------------------------------- */
 /* MoE layer                                                               */
 /* ---------------------------------------------------------------------- */
 

@@ -85,6 +85,18 @@ class MoeBlockNormArgs(ctypes.Structure):
                 ("h", ctypes.c_void_p), ("ld_h", ctypes.c_int64)]
 
 
+class KvCacheDesc(ctypes.Structure):
+    _fields_ = [("num_pages", ctypes.c_int64), ("num_slots", ctypes.c_int64), ("kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("page_size", ctypes.c_int32), ("codes", ctypes.c_void_p),
+                ("scales", ctypes.c_void_p), ("tails", ctypes.c_void_p), ("tail_scales", ctypes.c_void_p)]
+
+
+class KvBatchDesc(ctypes.Structure):
+    _fields_ = [("entries", ctypes.c_int64), ("tokens", ctypes.c_int64), ("table", ctypes.c_void_p),
+                ("table_width", ctypes.c_int64), ("ld_table", ctypes.c_int64), ("lens", ctypes.c_void_p),
+                ("slots", ctypes.c_void_p), ("cu", ctypes.c_void_p)]
+
+
 _lib = None
 _synth = None
 _P = ctypes.c_void_p
@@ -146,6 +158,18 @@ def lib():
         L.int8_linear.argtypes = [_P, _I32, _I64, _P, _I64, _P, _P, _I64, _I64, _I64, _P, _I64, _P, _I32, _I64, _P]
         L.int8_linear_workspace.restype = ctypes.c_int
         L.int8_linear_workspace.argtypes = [_I64, _I64, ctypes.POINTER(_I64)]
+        cache, batch = ctypes.POINTER(KvCacheDesc), ctypes.POINTER(KvBatchDesc)
+        L.kv_append.restype = ctypes.c_int
+        L.kv_append.argtypes = [cache, batch, _P, _I64, _I64, _P, _I64, _I64, _I32, _P]
+        L.kv_attention.restype = ctypes.c_int
+        L.kv_attention.argtypes = [cache, batch, _P, _I64, _I64, _I32, _I32, ctypes.c_float, _I64, _P, _I64, _P, _I64,
+                                   _I64, _P]
+        L.kv_attention_workspace.restype = ctypes.c_int
+        L.kv_attention_workspace.argtypes = [cache, batch, _I32, ctypes.POINTER(_I64)]
+        L.kv_read.restype = ctypes.c_int
+        L.kv_read.argtypes = [cache, batch, _P, _P, _I32, _P]
+        L.kv_fork.restype = ctypes.c_int
+        L.kv_fork.argtypes = [cache, batch, _P, _P, _I64, _P]
         _lib = L
     return _lib
 
@@ -362,6 +386,87 @@ def int8_linear(x, w_codes, w_scale, bias=None, out_dtype=None, out=None, stream
         with _on(stream, x):
             return int8_linear(x, w_codes, w_scale, bias, out_dtype, out)
     return (_calls or calls()).linear(x, w_codes, w_scale, bias, out_dtype, out)
+
+
+# --- the attention half of a block ----------------------------------------------
+#
+# A step of a batch is described by the same four tensors in every call: table int32
+# [B, W] (the pages of each sequence in order), lens int32 [B] (tokens that it had
+# before the step), slots int32 [B] (where the tokens of its last, incomplete page
+# are kept) and cu int32 [B + 1], or None where each sequence gets one token: the
+# call's tokens cu[i] .. cu[i + 1] - 1 are sequence i's, at its positions from
+# lens[i] on.  They are read on the device: a captured step follows their values.
+# Entries with a negative slot or length are padding (kv_batch).
+
+class KvCache:
+    """A layer's key-value cache (kv_cache): `num_pages` pages of `page_size`
+    tokens for `kv_heads` heads of `head_dim` channels, full pages in 8 bits with
+    one scale for the keys and one for the values of each head, and
+    `num_slots` places for the tokens of sequences' last, incomplete pages.
+    Which page and slot is whose is the caller's to say."""
+
+    def __init__(self, num_pages, num_slots, kv_heads, head_dim, page_size=64, device="cuda"):
+        for name, v, least, most in (("num_pages", num_pages, 1, 2 ** 31 - 1), ("num_slots", num_slots, 1, 2 ** 31 - 1),
+                                     ("kv_heads", kv_heads, 1, 1024)):
+            if not least <= v <= most:
+                raise ValueError(f"{name} must be in [{least}, {most}], got {v}")
+        if head_dim not in (64, 128, 192, 256):
+            raise ValueError(f"head_dim must be 64, 128, 192 or 256, got {head_dim}")
+        if page_size not in (16, 32, 64, 128):
+            raise ValueError(f"page_size must be 16, 32, 64 or 128, got {page_size}")
+        self.num_pages, self.num_slots, self.kv_heads = num_pages, num_slots, kv_heads
+        self.head_dim, self.page_size = head_dim, page_size
+        n = page_size * head_dim
+        self.codes = torch.zeros((num_pages, 2, kv_heads, n), dtype=torch.uint8, device=device)
+        self.scales = torch.zeros((num_pages, 2, kv_heads), dtype=torch.float32, device=device)
+        self.tails = torch.zeros((num_slots, 2, kv_heads, n), dtype=torch.float16, device=device)
+        self.tail_scales = torch.zeros((num_slots, 2, kv_heads, page_size), dtype=torch.float32, device=device)
+        self.desc = KvCacheDesc(num_pages, num_slots, kv_heads, head_dim, page_size, self.codes.data_ptr(),
+                                self.scales.data_ptr(), self.tails.data_ptr(), self.tail_scales.data_ptr())
+
+
+def kv_append(cache, k, v, table, lens, slots, cu=None, stream=None):
+    """The step's keys and values, [tokens, kv_heads, head_dim] bf16 or f16 (any
+    strides of tokens and heads that are multiples of 8), into the cache."""
+    if stream is not None:
+        with _on(stream, k):
+            return kv_append(cache, k, v, table, lens, slots, cu)
+    return (_calls or calls()).append(cache, k, v, table, lens, slots, cu)
+
+
+def kv_attention(cache, q, table, lens, slots, cu=None, scale=None, window=0, out=None, stream=None):
+    """Causal attention of the step's queries q [tokens, heads, head_dim] over the
+    cache, which holds the step's keys and values already, -> [tokens, heads,
+    head_dim].  heads: a multiple of kv_heads (consecutive query heads share a kv
+    head); scale: 1 / sqrt(head_dim) by default; window: how many of the last
+    tokens, its own included, a token sees (0: all)."""
+    if stream is not None:
+        with _on(stream, q):
+            return kv_attention(cache, q, table, lens, slots, cu, scale, window, out)
+    if scale is None:
+        scale = cache.head_dim ** -0.5
+    return (_calls or calls()).attention(cache, q, table, lens, slots, cu, scale, window, out)
+
+
+def kv_read(cache, table, lens, slots, cu=None, tokens=None, dtype=torch.bfloat16, out=None, stream=None):
+    """(k, v) [tokens, kv_heads, head_dim] of the step's tokens, the last ones of their
+    sequences, as the cache holds them.  tokens: how many they are (cu[-1]);
+    rows behind cu[-1] are left as they were."""
+    if stream is not None:
+        with _on(stream, table):
+            return kv_read(cache, table, lens, slots, cu, tokens, dtype, out)
+    return (_calls or calls()).read(cache, table, lens, slots, cu, tokens, dtype, out if out is None else tuple(out))
+
+
+def kv_fork(cache, table, lens, slots, src, dst, stream=None):
+    """For each pair, entry dst[j] of the batch continues what entry src[j] holds: it
+    shares its full pages (table is written), has its length (lens is written)
+    and its own copy of the incomplete page's tokens.  src, dst int32; no dst may
+    be another pair's src or dst."""
+    if stream is not None:
+        with _on(stream, table):
+            return kv_fork(cache, table, lens, slots, src, dst)
+    return (_calls or calls()).fork(cache, table, lens, slots, src, dst)
 
 
 # --- synthetic weights (input generation) --------------------------------------

@@ -27,7 +27,8 @@ FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-Wall",
 
 LIBS = {
     "libnvfp4moe.so": ["quantize.hip", "moe_kernels.hip", "gemm_kernels.hip", "route.hip", "block_norm.hip",
-                      "int8_linear.hip", "moe_api.cpp", "ops_api.cpp", "noalloc.hip"],
+                      "int8_linear.hip", "kv_cache.hip", "kv_attention.hip", "moe_api.cpp", "ops_api.cpp", "kv_api.cpp",
+                      "noalloc.hip"],
     "libnvfp4synth.so": ["synth_weights.hip"],
 }
 

@@ -31,7 +31,7 @@ using at::Tensor;
 
 PyObject* g_error = nullptr;       // Nvfp4Error(status, message)
 PyObject* g_raw_stream = nullptr;  // device index -> handle of its current stream
-PyObject *g_weight, *g_bias, *g_desc;  // attribute names
+PyObject *g_weight, *g_bias, *g_desc, *g_codes;  // attribute names
 
 [[noreturn]] void raised() {
   python_error e;
@@ -134,7 +134,7 @@ S structure(PyObject* o) {
   bool fits = view.len == sizeof(S);
   if (fits) std::memcpy(&s, view.buf, sizeof(S));
   PyBuffer_Release(&view);
-  TORCH_CHECK_TYPE(fits, "a Router (for routing) or a Norm (for a norm) is expected");
+  TORCH_CHECK_TYPE(fits, "a Router (for routing), a Norm (for a norm) or a KvCache is expected");
   return s;
 }
 
@@ -368,6 +368,153 @@ PyObject* linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+// --- the attention half of a block
+
+// A tensor [tokens, heads, D] of unit stride in D, heads or D of 0: any number.
+const Tensor& heads_of(PyObject* o, const char* name, int64_t tokens, int64_t heads, int64_t D, c10::Device device,
+                       ScalarType type = ScalarType::Undefined) {
+  const Tensor& t = tensor(o, name);
+  TORCH_CHECK_VALUE(type == ScalarType::Undefined ? t.scalar_type() == ScalarType::BFloat16 || t.scalar_type() == ScalarType::Half
+                                                  : t.scalar_type() == type,
+                    name, " must be ", type == ScalarType::Undefined ? "bfloat16 or float16" : c10::toString(type), ", got ",
+                    t.scalar_type());
+  TORCH_CHECK_VALUE(t.dim() == 3 && t.device() == device && (tokens < 0 || t.size(0) == tokens) &&
+                        (heads < 0 || t.size(1) == heads) && t.size(2) == D && t.stride(2) == 1,
+                    name, " must be [tokens, heads, ", D, "] on ", device, " with unit stride in its last dimension",
+                    tokens >= 0 ? " and match the other tensors" : "", ", got ", t.sizes(), " on ", t.device());
+  return t;
+}
+
+int64_t token_stride(const Tensor& t) { return t.size(0) > 1 ? t.stride(0) : 0; }
+int64_t head_stride(const Tensor& t) { return t.size(1) > 1 ? t.stride(1) : 0; }
+
+// A KvCache's structure, and the device of its memory.
+kv_cache cache_of(PyObject* o, c10::Device& device) {
+  kv_cache c = structure<kv_cache>(o);
+  Ref codes(PyObject_GetAttr(o, g_codes));
+  device = tensor(codes.p, "the cache's memory").device();
+  return c;
+}
+
+// tokens: of the call, or -1 where it is for cu to say.
+kv_batch batch_of(PyObject* table_o, PyObject* lens, PyObject* slots, PyObject* cu, int64_t tokens, c10::Device device) {
+  const Tensor& table = matrix(table_o, "table", ScalarType::Int);
+  TORCH_CHECK_VALUE(table.device() == device, "table must be a tensor on ", device);
+  kv_batch b{};
+  b.entries = table.size(0);
+  b.tokens = tokens < 0 ? b.entries : tokens;
+  b.table_dev = static_cast<const int32_t*>(table.data_ptr());
+  b.table_width = table.size(1);
+  b.ld_table = row_stride(table);
+  TORCH_CHECK_VALUE(lens != Py_None && slots != Py_None, "lens and slots must be tensors");
+  b.lens_dev = static_cast<const int32_t*>(vector(lens, "lens", b.entries, ScalarType::Int, device));
+  b.slots_dev = static_cast<const int32_t*>(vector(slots, "slots", b.entries, ScalarType::Int, device));
+  b.cu_dev = static_cast<const int32_t*>(vector(cu, "cu", b.entries + 1, ScalarType::Int, device));
+  return b;
+}
+
+// (cache, k, v, table, lens, slots, cu)
+PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  arguments(n, 7);
+  c10::Device device(c10::kCUDA);
+  const kv_cache c = cache_of(a[0], device);
+  const Tensor& k = heads_of(a[1], "k", -1, c.kv_heads, c.head_dim, device);
+  const Tensor& v = heads_of(a[2], "v", k.size(0), c.kv_heads, c.head_dim, device, k.scalar_type());
+  const kv_batch b = batch_of(a[3], a[4], a[5], a[6], k.size(0), device);
+  c10::DeviceGuard guard(device);
+  void* stream = stream_of(device);
+  call([&] {
+    return kv_append(&c, &b, k.data_ptr(), token_stride(k), head_stride(k), v.data_ptr(), token_stride(v), head_stride(v),
+                     code_of(k.scalar_type()), stream);
+  });
+  Py_RETURN_NONE;
+  END_HANDLE_TH_ERRORS
+}
+
+// (cache, q, table, lens, slots, cu, scale, window, out)
+PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  arguments(n, 9);
+  c10::Device device(c10::kCUDA);
+  const kv_cache c = cache_of(a[0], device);
+  const Tensor& q = heads_of(a[1], "q", -1, -1, c.head_dim, device);
+  const int64_t T = q.size(0), heads = q.size(1);
+  TORCH_CHECK_VALUE(heads <= INT_MAX, "q has too many heads");
+  const kv_batch b = batch_of(a[2], a[3], a[4], a[5], T, device);
+  const float scale = number(a[6]);
+  const long long window = PyLong_AsLongLong(a[7]);
+  if (window == -1 && PyErr_Occurred()) raised();
+  c10::DeviceGuard guard(device);
+  int64_t bytes = 0;
+  call([&] { return kv_attention_workspace(&c, &b, static_cast<int32_t>(heads), &bytes); });
+  Tensor out = a[8] == Py_None ? empty({T, heads, c.head_dim}, q.scalar_type(), device)
+                               : heads_of(a[8], "out", T, heads, c.head_dim, device, q.scalar_type());
+  Tensor work;
+  if (bytes) work = empty({bytes}, ScalarType::Byte, device);
+  void* stream = stream_of(device);
+  call([&] {
+    return kv_attention(&c, &b, q.data_ptr(), token_stride(q), head_stride(q), static_cast<int32_t>(heads),
+                        code_of(q.scalar_type()), scale, window, bytes ? work.data_ptr() : nullptr, bytes, out.data_ptr(),
+                        token_stride(out), head_stride(out), stream);
+  });
+  return THPVariable_Wrap(out);
+  END_HANDLE_TH_ERRORS
+}
+
+// (cache, table, lens, slots, cu, tokens, dtype, out)
+PyObject* read(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  arguments(n, 8);
+  c10::Device device(c10::kCUDA);
+  const kv_cache c = cache_of(a[0], device);
+  int64_t T = -1;
+  if (a[5] != Py_None) {
+    T = PyLong_AsLongLong(a[5]);
+    if (T == -1 && PyErr_Occurred()) raised();
+    TORCH_CHECK_VALUE(T >= 0, "tokens must be >= 0");
+  }
+  TORCH_CHECK_VALUE(a[4] == Py_None || T >= 0, "tokens (how many cu has in all) must be given with cu");
+  const kv_batch b = batch_of(a[1], a[2], a[3], a[4], T, device);
+  c10::DeviceGuard guard(device);
+  Tensor k, v;
+  if (a[7] == Py_None) {
+    const ScalarType type = type_of(a[6], "dtype");
+    k = empty({b.tokens, c.kv_heads, c.head_dim}, type, device);
+    v = empty({b.tokens, c.kv_heads, c.head_dim}, type, device);
+  } else {
+    TORCH_CHECK_VALUE(PyTuple_Check(a[7]) && PyTuple_GET_SIZE(a[7]) == 2, "out must be (k, v)");
+    const Tensor& first = tensor(PyTuple_GET_ITEM(a[7], 0), "k out");
+    TORCH_CHECK_VALUE(code_of(first.scalar_type()) >= 0, "out must be bfloat16, float16 or float32");
+    k = heads_of(PyTuple_GET_ITEM(a[7], 0), "k out", b.tokens, c.kv_heads, c.head_dim, device, first.scalar_type());
+    v = heads_of(PyTuple_GET_ITEM(a[7], 1), "v out", b.tokens, c.kv_heads, c.head_dim, device, first.scalar_type());
+    TORCH_CHECK_VALUE(k.is_contiguous() && v.is_contiguous(), "out must be contiguous");
+  }
+  void* stream = stream_of(device);
+  call([&] { return kv_read(&c, &b, k.data_ptr(), v.data_ptr(), code_of(k.scalar_type()), stream); });
+  return pair(k, v);
+  END_HANDLE_TH_ERRORS
+}
+
+// (cache, table, lens, slots, src, dst)
+PyObject* fork_(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  arguments(n, 6);
+  c10::Device device(c10::kCUDA);
+  const kv_cache c = cache_of(a[0], device);
+  const kv_batch b = batch_of(a[1], a[2], a[3], Py_None, -1, device);
+  const Tensor& src = tensor(a[4], "src");
+  const int64_t pairs = src.dim() == 1 ? src.size(0) : 0;
+  TORCH_CHECK_VALUE(a[5] != Py_None, "dst must be a tensor");
+  auto* s = static_cast<const int32_t*>(vector(a[4], "src", pairs, ScalarType::Int, device));
+  auto* d = static_cast<const int32_t*>(vector(a[5], "dst", pairs, ScalarType::Int, device));
+  c10::DeviceGuard guard(device);
+  void* stream = stream_of(device);
+  call([&] { return kv_fork(&c, &b, s, d, pairs, stream); });
+  Py_RETURN_NONE;
+  END_HANDLE_TH_ERRORS
+}
+
 // (error class, raw_stream)
 PyObject* setup(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
@@ -382,7 +529,7 @@ PyObject* setup(PyObject*, PyObject* const* a, Py_ssize_t n) {
 
 #define CALL(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(f)), METH_FASTCALL, nullptr}
 PyMethodDef g_methods[] = {CALL(route), CALL(block_norm), CALL(quantize), CALL(matmul),
-                           CALL(linear), CALL(setup), {nullptr, nullptr, 0, nullptr}};
+                           CALL(linear), CALL(append), CALL(attention), CALL(read), {"fork", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(fork_)), METH_FASTCALL, nullptr}, CALL(setup), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace
@@ -391,5 +538,6 @@ PyMODINIT_FUNC PyInit__calls() {
   g_weight = PyUnicode_InternFromString("weight");
   g_bias = PyUnicode_InternFromString("bias");
   g_desc = PyUnicode_InternFromString("desc");
-  return g_weight && g_bias && g_desc ? PyModule_Create(&g_module) : nullptr;
+  g_codes = PyUnicode_InternFromString("codes");
+  return g_weight && g_bias && g_desc && g_codes ? PyModule_Create(&g_module) : nullptr;
 }
