@@ -347,7 +347,7 @@ int kv_append(const kv_cache* cache, const kv_batch* batch, const void* k_dev, i
  * 11 bits before it multiplies a value; the result is rounded to dtype once.
  * Scores beyond binary32's range, and q with an infinity or a NaN, give NaN.
  *   q_dev    dtype (MOE_BF16 or MOE_F16) [tokens, heads, head_dim], strides as in kv_append
- *   heads    a multiple of kv_heads, at most 64 times as many
+ *   heads    a multiple of kv_heads, at most 64 times as many; tokens * heads / kv_heads <= 2^28
  *   scale    finite;  window >= 0
  *   workspace_dev  16-byte aligned, of at least kv_attention_workspace bytes (may be
  *            NULL for 0), used by one call at a time (calls on one stream may share

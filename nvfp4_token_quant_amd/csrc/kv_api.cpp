@@ -142,8 +142,8 @@ int check_heads(const kv_cache& c, const kv_batch& b, int32_t heads) {
   if (heads < 1 || heads % c.kv_heads != 0 || heads / c.kv_heads > 64)
     return api_fail(NVFP4_ERR_INVALID_ARG, "heads must be a multiple of kv_heads, at most 64 times as many (got %d of %d)",
                     heads, c.kv_heads);
-  if (b.tokens * (heads / c.kv_heads) > (int64_t{1} << 30))
-    return api_fail(NVFP4_ERR_INVALID_ARG, "tokens * heads / kv_heads must be <= 2^30");
+  if (b.tokens * (heads / c.kv_heads) > (int64_t{1} << 28))
+    return api_fail(NVFP4_ERR_INVALID_ARG, "tokens * heads / kv_heads must be <= 2^28");
   return NVFP4_OK;
 }
 

@@ -33,9 +33,14 @@ namespace nvfp4 {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kUnit = 0x1p14f;      // weights are up to this
-constexpr float kLeastUnit = 0x1p-100f;  // and u at least this
 constexpr float kNone = -__builtin_huge_valf();
+// A running maximum is kept while weights stay within 2^4 of its own, so that the
+// output's sums are rescaled a few times instead of at every second step; fp16 holds
+// 2^11 times that.
+constexpr float kSlack = 4.0f;
+constexpr float kUnit = 0x1p11f;
+constexpr float kLeastUnit = 0x1p-100f;   // of u
+constexpr float kLeastScale = 0x1p-126f;  // of a page's scales, as this kernel uses them
 
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
@@ -89,81 +94,192 @@ __device__ __forceinline__ int entry_steps(const AttnParams& a, const KvEntry& e
   return a.window ? min(all, (a.window + BM / a.group) / STEP + 4) : all;
 }
 
+// Tiles of an entry, none if its rows are another kernel's.
+template <int BM>
+__device__ __forceinline__ int entry_tiles(const AttnParams& a, const KvEntry& e) {
+  const int rows = e.n * a.group;
+  return rows > a.rows_above && rows <= a.rows_most ? (rows + BM - 1) / BM : 0;
+}
+
+// Steps of a piece, from the sum of tiles x steps over all entries (binary32, in an order
+// that is every block's; one step more than the quotient covers its rounding).
+__device__ __forceinline__ int steps_of_piece(const AttnParams& a, float total) {
+  const float n = total * static_cast<float>(a.c.heads) / static_cast<float>(a.target) * 1.0001f + 1.0f;
+  return max(a.least_steps, static_cast<int>(fminf(n, 0x1p30f)));
+}
+
+struct Count {
+  uint32_t blocks, cut;  // cut: pieces of cut tiles << 12 | cut tiles; both without the factor of the kv heads
+  int pieces;
+};
+__device__ __forceinline__ Count entry_blocks(const AttnParams& a, int tiles, int steps, int piece_steps) {
+  Count c{0, 0, 1};
+  if (!tiles) return c;
+  if (a.target) c.pieces = (steps + piece_steps - 1) / piece_steps;
+  const uint64_t n = static_cast<uint64_t>(tiles) * c.pieces;
+  c.blocks = static_cast<uint32_t>(min(n, uint64_t{1} << 25));
+  // (with target <= 1024 the pieces of cut tiles are at most 2048 in all)
+  if (c.pieces > 1) c.cut = c.blocks << 12 | static_cast<uint32_t>(tiles);
+  return c;
+}
+
+__device__ __forceinline__ uint32_t wave_scan(uint32_t v) {  // sum over the lanes up to this one
+  v += __builtin_amdgcn_update_dpp(0u, v, 0x111, 0xF, 0xF, false);  // row_shr 1, 2, 4, 8
+  v += __builtin_amdgcn_update_dpp(0u, v, 0x112, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0u, v, 0x114, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0u, v, 0x118, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0u, v, 0x142, 0xA, 0xF, false);  // lane 15 and 47 of the row before
+  v += __builtin_amdgcn_update_dpp(0u, v, 0x143, 0xC, 0xF, false);  // lane 31
+  return v;
+}
+__device__ __forceinline__ float wave_total(float v) {
+#pragma unroll
+  for (int d = 1; d < kWave; d *= 2) v += __shfl_xor(v, d);
+  return v;
+}
+
 // Which work item a block has (false: none).  Every block computes the same cut of
 // the batch: the number of pieces of each entry, and from their sums where its own
-// index falls.  The sums hold blocks, pieces of cut tiles and cut tiles, each without
-// the factor of the kv heads, in 40, 12 and 12 bits: with target <= 1024 there are at
-// most 2048 pieces of cut tiles.
+// index falls.  Up to 256 entries every wave does so by itself, up to four entries a
+// lane, without a barrier; more are the block's together.
 template <int THREADS, int STEP, int BM>
 __device__ __forceinline__ bool find_work(const AttnParams& a, Work& w) {
-  __shared__ uint64_t buf[2][THREADS / kWave];
-  __shared__ int found[4];
   const KvParams& p = a.c;
-  const int per = (p.entries + THREADS - 1) / THREADS;
-  const int i0 = threadIdx.x * per, i1 = min(i0 + per, p.entries);
-  auto tiles_of = [&](const KvEntry& e) {
-    const int64_t rows = int64_t{e.n} * a.group;
-    return rows > a.rows_above && rows <= a.rows_most ? static_cast<int>((rows + BM - 1) / BM) : 0;
-  };
-  uint64_t own = 0, total;
-  if (a.target) {
-    for (int i = i0; i < i1; ++i) {
-      const KvEntry e = kv_entry(p, i);
-      const int t = tiles_of(e);
-      if (t) own += static_cast<uint64_t>(t) * entry_steps<STEP, BM>(a, e);
-    }
-  }
-  int piece_steps = INT_MAX;
-  if (a.target) {
-    block_scan<THREADS>(own, buf[0], total);
-    const uint64_t n = (total * p.heads + a.target - 1) / a.target;
-    piece_steps = uniform(static_cast<int>(min(max(n, static_cast<uint64_t>(a.least_steps)), uint64_t{INT_MAX / 2})));
-  }
-  auto count_of = [&](const KvEntry& e, int tiles) -> uint64_t {
-    if (!tiles) return 0;
-    const int pieces = a.target ? (entry_steps<STEP, BM>(a, e) + piece_steps - 1) / piece_steps : 1;
-    const uint64_t blocks = static_cast<uint64_t>(tiles) * pieces;
-    return blocks << 24 | (pieces > 1 ? blocks << 12 | static_cast<uint64_t>(tiles) : 0);
-  };
-  own = 0;
-  for (int i = i0; i < i1; ++i) {
-    const KvEntry e = kv_entry(p, i);
-    own += count_of(e, tiles_of(e));
-  }
-  if (threadIdx.x == 0) found[0] = -1;
-  uint64_t at = block_scan<THREADS>(own, buf[1], total) - own;
-  // (entries that share tokens can need more blocks than there are: such a call does nothing)
-  const bool fits = (total >> 24) * p.heads <= gridDim.x;
-  if (blockIdx.x == 0 && threadIdx.x == 0 && a.target)
-    *a.join_count = fits ? static_cast<int>(total & 4095) * p.heads : 0;
-  if (!fits) return false;
-  const uint64_t want = blockIdx.x / p.heads;
-  if (want >= at >> 24 && want < (at + own) >> 24) {
-    for (int i = i0; i < i1; ++i) {
-      const KvEntry e = kv_entry(p, i);
-      const uint64_t c = count_of(e, tiles_of(e));
-      if (want < (at + c) >> 24) {
-        found[0] = i;
-        found[1] = static_cast<int>(want - (at >> 24));
-        found[2] = static_cast<int>(at >> 12 & 4095);
-        found[3] = static_cast<int>(at & 4095);
-        break;
-      }
-      at += c;
-    }
-  }
-  __syncthreads();
-  w.entry = uniform(found[0]);
-  if (w.entry < 0) return false;
-  const int index = uniform(found[1]);
-  w.e = kv_entry(p, w.entry);
+  const int lane = threadIdx.x & (kWave - 1);
+  const uint32_t want = blockIdx.x / p.heads;
   w.head = blockIdx.x % p.heads;
-  w.tiles = tiles_of(w.e);
-  w.pieces = a.target ? (entry_steps<STEP, BM>(a, w.e) + piece_steps - 1) / piece_steps : 1;
+  uint32_t total_blocks, total_cut;
+  int index, cut_before;
+  if (p.entries <= 4 * kWave) {
+    const int per = (p.entries + kWave - 1) / kWave;
+    KvEntry e[4];
+    int tiles[4], steps[4];
+    float work = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int i = lane * per + k;
+      e[k] = KvEntry{};
+      tiles[k] = steps[k] = 0;
+      if (k < per && i < p.entries) {
+        e[k] = kv_entry(p, i);
+        tiles[k] = entry_tiles<BM>(a, e[k]);
+        if (tiles[k]) steps[k] = entry_steps<STEP, BM>(a, e[k]);
+        work += static_cast<float>(tiles[k]) * static_cast<float>(steps[k]);
+      }
+    }
+    const int piece_steps = a.target ? steps_of_piece(a, wave_total(work)) : 0;
+    Count c[4];
+    uint32_t blocks = 0, cut = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      c[k] = entry_blocks(a, tiles[k], steps[k], piece_steps);
+      blocks += c[k].blocks;
+      cut += c[k].cut;
+    }
+    uint32_t at = wave_scan(blocks), cut_at = a.target ? wave_scan(cut) : 0;
+    total_blocks = __builtin_amdgcn_readlane(at, kWave - 1);
+    total_cut = __builtin_amdgcn_readlane(cut_at, kWave - 1);
+    at -= blocks;
+    cut_at -= cut;
+    const uint64_t here = __ballot(want - at < blocks);
+    const int from = here ? __builtin_ctzll(here) : 0;
+    w.entry = here ? 0 : -1;
+    // the lane's entry among its four
+    int mine = 0;
+    uint32_t in = want - at;
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      if (mine == k && in >= c[k].blocks) {
+        in -= c[k].blocks;
+        cut_at += c[k].cut;
+        mine = k + 1;
+      }
+    }
+    KvEntry x = e[0];
+    int t = tiles[0], n = c[0].pieces;
+#pragma unroll
+    for (int k = 1; k < 4; ++k)
+      if (mine == k) {
+        x = e[k];
+        t = tiles[k];
+        n = c[k].pieces;
+      }
+    if (here) w.entry = from * per + __builtin_amdgcn_readlane(mine, from);
+    w.e.len = __builtin_amdgcn_readlane(x.len, from);
+    w.e.n = __builtin_amdgcn_readlane(x.n, from);
+    w.e.first = __builtin_amdgcn_readlane(x.first, from);
+    w.e.slot = __builtin_amdgcn_readlane(x.slot, from);
+    w.tiles = __builtin_amdgcn_readlane(t, from);
+    w.pieces = __builtin_amdgcn_readlane(n, from);
+    index = __builtin_amdgcn_readlane(in, from);
+    cut_before = __builtin_amdgcn_readlane(cut_at, from);
+  } else {
+    __shared__ uint64_t buf[2][THREADS / kWave];
+    __shared__ float sum[THREADS / kWave];
+    __shared__ int found[3];
+    const int per = (p.entries + THREADS - 1) / THREADS;
+    const int i0 = threadIdx.x * per, i1 = min(i0 + per, p.entries);
+    int piece_steps = 0;
+    if (a.target) {
+      float work = 0.0f;
+      for (int i = i0; i < i1; ++i) {
+        const KvEntry e = kv_entry(p, i);
+        const int t = entry_tiles<BM>(a, e);
+        if (t) work += static_cast<float>(t) * static_cast<float>(entry_steps<STEP, BM>(a, e));
+      }
+      work = wave_total(work);
+      if (lane == 0) sum[threadIdx.x / kWave] = work;
+      __syncthreads();
+      work = 0.0f;
+      for (int i = 0; i < THREADS / kWave; ++i) work += sum[i];
+      piece_steps = steps_of_piece(a, work);
+    }
+    auto count_of = [&](int i, KvEntry& e, int& t) {
+      e = kv_entry(p, i);
+      t = entry_tiles<BM>(a, e);
+      return entry_blocks(a, t, t ? entry_steps<STEP, BM>(a, e) : 0, piece_steps);
+    };
+    KvEntry e;
+    int t;
+    uint64_t own = 0, total;
+    for (int i = i0; i < i1; ++i) {
+      const Count c = count_of(i, e, t);
+      own += static_cast<uint64_t>(c.blocks) << 24 | c.cut;
+    }
+    if (threadIdx.x == 0) found[0] = -1;
+    uint64_t at = block_scan<THREADS>(own, buf[0], total) - own;
+    total_blocks = static_cast<uint32_t>(min(total >> 24, uint64_t{UINT32_MAX}));
+    total_cut = static_cast<uint32_t>(total & 0xffffff);
+    if (want >= at >> 24 && want < (at + own) >> 24) {
+      for (int i = i0; i < i1; ++i) {
+        const Count c = count_of(i, e, t);
+        if (want < (at >> 24) + c.blocks) {
+          found[0] = i;
+          found[1] = static_cast<int>(want - (at >> 24));
+          found[2] = static_cast<int>(at & 0xffffff);
+          break;
+        }
+        at += static_cast<uint64_t>(c.blocks) << 24 | c.cut;
+      }
+    }
+    __syncthreads();
+    w.entry = uniform(found[0]);
+    index = cut_before = 0;
+    if (w.entry >= 0) {
+      w.pieces = uniform(count_of(w.entry, w.e, w.tiles).pieces);
+      index = uniform(found[1]);
+      cut_before = uniform(found[2]);
+    }
+  }
+  // (entries that share tokens can need more blocks than there are: such a call does nothing)
+  const bool fits = static_cast<uint64_t>(total_blocks) * p.heads <= gridDim.x;
+  if (a.target && blockIdx.x == 0 && threadIdx.x == 0)
+    *a.join_count = fits ? static_cast<int>(total_cut & 4095) * p.heads : 0;
+  if (!fits || w.entry < 0) return false;
   // the last rows see the most keys: their tiles first
   w.tile = w.tiles - 1 - index / w.pieces;
   w.piece = index % w.pieces;
-  w.slot = (uniform(found[2]) + index) * p.heads + w.head;
+  w.slot = ((cut_before >> 12) + index) * p.heads + w.head;
   if (w.pieces > 1 && w.piece == 0 && threadIdx.x == 0) {
     const int r0 = w.tile * BM;
     KvJoin j;
@@ -174,7 +290,7 @@ __device__ __forceinline__ bool find_work(const AttnParams& a, Work& w) {
     j.slot = w.slot;
     j.pieces = w.pieces;
     j.stride = p.heads;
-    a.joins[(found[3] + index / w.pieces) * p.heads + w.head] = j;
+    a.joins[((cut_before & 4095) + index / w.pieces) * p.heads + w.head] = j;
   }
   return true;
 }
@@ -197,6 +313,22 @@ __device__ __forceinline__ float over_groups(float v) {  // over the four lanes 
   return MAX ? fmaxf(__uint_as_float(x), __uint_as_float(y)) : __uint_as_float(x) + __uint_as_float(y);
 }
 
+// The tail's tokens have scales of their own, powers of two.  A block of 16 gets the largest
+// as its scale; the values are brought to it (a token of 2^-28 of the block's largest
+// keeps its 11 bits), so that the products see the same thing as in a page.
+__device__ __forceinline__ float row_max(float v) {  // over 16 lanes (a NaN is none)
+  v = fmaxf(v, __uint_as_float(dpp_u32<kDppXor1>(__float_as_uint(v))));
+  v = fmaxf(v, __uint_as_float(dpp_u32<kDppXor2>(__float_as_uint(v))));
+  v = fmaxf(v, __uint_as_float(dpp_u32<kDppHalfMirror>(__float_as_uint(v))));
+  return fmaxf(v, __uint_as_float(dpp_u32<kDppMirror>(__float_as_uint(v))));
+}
+__device__ __forceinline__ float relative(float scale, float block) {  // 0 for a NaN and for none
+  return scale > 0.0f ? scale / block : 0.0f;
+}
+__device__ __forceinline__ float nan_mark(float k, float v) {  // 0, or NaN if either is
+  return k != k || v != v ? __uint_as_float(0x7fc00000u) : 0.0f;
+}
+
 // A wave's 16 MR rows: operands, running maximum, sum (of the lane's own keys) and
 // output sums (channels 16 f + 4 (lane / 16) + i of row lane % 16).
 template <int D, int MR>
@@ -204,15 +336,19 @@ struct Rows {
   half8 q[MR][D / 32];
   float m[MR], l[MR];
   f32x4 o[MR][D / 16];
-  float u, inv;      // unit, kUnit / u
-  float c;           // scale log2(e) over q's power of two
+  float u, inv;        // unit, kUnit / u
+  float c;             // |scale| log2(e) over q's power of two
   int lo[MR], hi[MR];  // keys that the lane's row sees: lo <= key < hi
   int all_lo, all_hi;  // keys that every row sees
 
-  // Rows [r0, r0 + 16 MR) of the entry, of which `rows` exist.
-  __device__ __forceinline__ void load(const AttnParams& a, const KvEntry& e, int head, int r0, int rows) {
+  struct Raw {
+    u32x4 x[MR][D / 32];
+  };
+
+  // Rows [r0, r0 + 16 MR) of the entry, of which `rows` exist: the loads of q, and what
+  // needs no memory.
+  __device__ __forceinline__ void issue(Raw& raw, const AttnParams& a, const KvEntry& e, int head, int r0, int rows) {
     const int lane = threadIdx.x & (kWave - 1);
-    u32x4 raw[MR][D / 32];
 #pragma unroll
     for (int r = 0; r < MR; ++r) {
       const int row = r0 + 16 * r + lane % 16, token = row / a.group;
@@ -220,7 +356,7 @@ struct Rows {
       const char* p = static_cast<const char*>(a.q) + (at + 16 * (lane / 16)) * 2;
 #pragma unroll
       for (int k = 0; k < D / 32; ++k)
-        raw[r][k] = row < rows ? *reinterpret_cast<const u32x4*>(p + (64 * (k / 2) + 8 * (k % 2)) * 2) : u32x4{};
+        raw.x[r][k] = row < rows ? *reinterpret_cast<const u32x4*>(p + (64 * (k / 2) + 8 * (k % 2)) * 2) : u32x4{};
       hi[r] = e.len + min(token, (rows - 1) / a.group) + 1;
       lo[r] = a.window ? max(0, hi[r] - a.window) : 0;
       m[r] = kNone;
@@ -233,12 +369,12 @@ struct Rows {
     all_lo = a.window ? max(0, e.len + last / a.group + 1 - a.window) : 0;
     u = kLeastUnit;
     inv = kUnit / kLeastUnit;
+  }
+
+  template <typename T>
+  __device__ __forceinline__ void scale_q(const Raw& raw, float scale) {
     // the largest finite magnitude of the tile, as bits
     uint32_t top = 0;
-    auto widen = [&](uint32_t w, float& x, float& y) {
-      if (a.bf16) Bf16::unpack(w, x, y);
-      else F16::unpack(w, x, y);
-    };
 #pragma unroll
     for (int r = 0; r < MR; ++r)
 #pragma unroll
@@ -246,14 +382,16 @@ struct Rows {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           float x, y;
-          widen(raw[r][k][i], x, y);
+          T::unpack(raw.x[r][k][i], x, y);
           const uint32_t bx = __float_as_uint(x) & 0x7fffffffu, by = __float_as_uint(y) & 0x7fffffffu;
           top = max(top, max(bx < 0x7f800000u ? bx : 0u, by < 0x7f800000u ? by : 0u));
         }
     top = __float_as_uint(wave_max(__uint_as_float(top)));
     const int exp = max(static_cast<int>(top >> 23) - 127 - 14, -126);
-    const float mul = __uint_as_float(static_cast<uint32_t>(127 - exp) << 23);
-    c = a.scale * kLog2e * __uint_as_float(static_cast<uint32_t>(127 + exp) << 23);
+    // the scale's sign is q's (the largest score is then the largest product)
+    const float sign = scale < 0.0f ? -1.0f : scale > 0.0f ? 1.0f : 0.0f;
+    const float mul = sign * __uint_as_float(static_cast<uint32_t>(127 - exp) << 23);
+    c = fabsf(scale) * kLog2e * __uint_as_float(static_cast<uint32_t>(127 + exp) << 23);
 #pragma unroll
     for (int r = 0; r < MR; ++r)
 #pragma unroll
@@ -261,21 +399,20 @@ struct Rows {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           float x, y;
-          widen(raw[r][k][i], x, y);
+          T::unpack(raw.x[r][k][i], x, y);
           q[r][k][2 * i] = static_cast<_Float16>(x * mul);
           q[r][k][2 * i + 1] = static_cast<_Float16>(y * mul);
         }
   }
+  __device__ __forceinline__ void prepare(const Raw& raw, const AttnParams& a) {
+    if (a.bf16) scale_q<Bf16>(raw, a.scale);
+    else scale_q<F16>(raw, a.scale);
+  }
 
-  // One step: 16 NB keys from key0 on.  key(b, k): a key operand, value(t, f): a value
-  // operand of 32 keys, ks / vs[b][i]: scales (of a block's four keys of this lane, or
-  // one for the block); ok[b]: whether the block's page is one.  masked: not every
-  // row sees every key.
-  template <int NB, int SC, typename Key, typename Value>
-  __device__ __forceinline__ void step(int key0, bool masked, const float (&ks)[NB][SC], const float (&vs)[NB][SC],
-                                       const bool (&ok)[NB], Key key, Value value) {
-    const int g4 = (threadIdx.x & (kWave - 1)) / 16 * 4;
-    f32x4 s[MR][NB];
+  // One step, 16 NB keys, in three parts.  s: products of q and the keys.  key(b, k): a
+  // key operand, of block b of 16 keys and 32 channels.
+  template <int NB, typename Key>
+  __device__ __forceinline__ void scores(f32x4 (&s)[MR][NB], Key key) const {
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
 #pragma unroll
@@ -287,14 +424,45 @@ struct Rows {
         for (int r = 0; r < MR; ++r) s[r][b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(x, q[r][k], s[r][b], 0, 0, 0);
       }
     }
-    // a larger unit
-    float top = u;
+  }
+
+  // The largest score of a lane's four keys in each block.
+  template <int NB>
+  __device__ __forceinline__ void tops(const f32x4 (&s)[MR][NB], float (&top)[MR][NB]) const {
 #pragma unroll
-    for (int b = 0; b < NB; ++b)
+    for (int r = 0; r < MR; ++r)
 #pragma unroll
-      for (int i = 0; i < SC; ++i) top = fmaxf(top, vs[b][i]);
+      for (int b = 0; b < NB; ++b) top[r][b] = fmaxf(fmaxf(s[r][b][0], s[r][b][1]), fmaxf(s[r][b][2], s[r][b][3]));
+  }
+
+  // Scores out of sight: of keys before or behind what a row sees, of a block whose page is
+  // none (ok[b] false).  mark: 0, or NaN where a key or its value is NaN.  Only for
+  // steps that have such keys.
+  template <int NB>
+  __device__ __forceinline__ void mask(f32x4 (&s)[MR][NB], int key0, const bool (&ok)[NB], const f32x4 (&mark)[NB]) const {
+    const int g4 = (threadIdx.x & (kWave - 1)) / 16 * 4;
+#pragma unroll
+    for (int r = 0; r < MR; ++r)
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int at = key0 + 16 * b + g4 + i;
+          s[r][b][i] = ok[b] && at >= lo[r] && at < hi[r] ? s[r][b][i] + mark[b][i] : kNone;
+        }
+  }
+
+  // w: weights 2^(x - m) s_v kUnit / u of the values' codes; maxima, sums, units.  ks, vs:
+  // the scales of each block of 16 keys.  The values' factor goes into the exponent: a
+  // weight costs one fma, one exponential, one addition and half a conversion, and a
+  // block's weights are divided by their factor in their sum.
+  template <int NB>
+  __device__ __forceinline__ void weights(const f32x4 (&s)[MR][NB], const float (&tops)[MR][NB], half8 (&w)[MR][NB / 2],
+                                          const float (&ks)[NB], const float (&vs)[NB]) {
+    float top = vs[0];
+#pragma unroll
+    for (int b = 1; b < NB; ++b) top = fmaxf(top, vs[b]);
     if (__ballot(top > u)) {
-      top = over_groups<true>(top);
       const float down = u / top;
       u = top;
       inv = kUnit / top;
@@ -303,42 +471,61 @@ struct Rows {
 #pragma unroll
         for (int f = 0; f < D / 16; ++f) o[r][f] *= down;
     }
-    half8 w[MR][NB / 2];
+    // Scales of nothing but zeros, and those far below the unit (2^-60: fp16 has lost
+    // their weights), are raised, so that no factor is zero.
+    const float least = fmaxf(u * 0x1p-60f, kLeastScale);
+    float kc[NB], log_f[NB], one_f[NB];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      const float f = fmaxf(vs[b], least) * inv;
+      kc[b] = fmaxf(ks[b] * c, kLeastScale);
+      log_f[b] = __builtin_amdgcn_logf(f);
+      one_f[b] = __builtin_amdgcn_rcpf(f);
+    }
+    float top_x[MR];
+    bool grows = false;
 #pragma unroll
     for (int r = 0; r < MR; ++r) {
-      float top_x = kNone;
+      top_x[r] = kNone;
 #pragma unroll
-      for (int b = 0; b < NB; ++b)
+      for (int b = 0; b < NB; ++b) top_x[r] = fmaxf(top_x[r], tops[r][b] * kc[b]);
+      grows = grows || top_x[r] > m[r] + kSlack;
+    }
+    if (__ballot(grows)) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float x = s[r][b][i] * (ks[b][SC == 1 ? 0 : i] * c);
-          if (masked) {
-            const int at = key0 + 16 * b + g4 + i;
-            x = ok[b] && at >= lo[r] && at < hi[r] ? x : kNone;
-          }
-          s[r][b][i] = x;
-          top_x = fmaxf(top_x, x);
-        }
-      if (__ballot(top_x > m[r])) {
-        const float now = fmaxf(m[r], over_groups<true>(top_x));
+      for (int r = 0; r < MR; ++r) {
+        const float now = fmaxf(m[r], over_groups<true>(top_x[r]));
         const float down = __builtin_amdgcn_exp2f(m[r] - (now == kNone ? 0.0f : now));
         m[r] = now;
         l[r] *= down;
 #pragma unroll
         for (int f = 0; f < D / 16; ++f) o[r][f] *= down;
       }
+    }
+#pragma unroll
+    for (int r = 0; r < MR; ++r) {
       const float base = m[r] == kNone ? 0.0f : m[r];
 #pragma unroll
-      for (int b = 0; b < NB; ++b)
+      for (int b = 0; b < NB; ++b) {
+        typedef float f32x2 __attribute__((ext_vector_type(2)));
+        const float off = log_f[b] - base;
+        float e[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float e = __builtin_amdgcn_exp2f(s[r][b][i] - base);
-          l[r] += e;
-          float v = e * (vs[b][SC == 1 ? 0 : i] * inv);
-          if (masked) v = s[r][b][i] == kNone ? 0.0f : v;  // (a scale that is NaN stays out of sight)
-          w[r][b / 2][b % 2 * 4 + i] = static_cast<_Float16>(v);
+        for (int i = 0; i < 4; ++i) e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r][b][i], kc[b], off));
+        l[r] += ((e[0] + e[1]) + (e[2] + e[3])) * one_f[b];
+#pragma unroll
+        for (int i = 0; i < 4; i += 2) {
+          const half2v h = __builtin_convertvector((f32x2{e[i], e[i + 1]}), half2v);
+          w[r][b / 2][b % 2 * 4 + i] = h[0];
+          w[r][b / 2][b % 2 * 4 + i + 1] = h[1];
         }
+      }
     }
+  }
+
+  // The weights times the values.  value(t, f): a value operand, of 32 keys and 16 channels.
+  template <int NB, typename Value>
+  __device__ __forceinline__ void outputs(const half8 (&w)[MR][NB / 2], Value value) {
 #pragma unroll
     for (int t = 0; t < NB / 2; ++t)
 #pragma unroll
@@ -361,6 +548,9 @@ struct Rows {
   }
 };
 
+using GlobalBytes = __attribute__((address_space(1))) uint8_t;
+using GlobalPiece = __attribute__((address_space(1))) u32x4;
+
 // Where row r of an entry writes its output.
 __device__ __forceinline__ int64_t out_at(const AttnParams& a, int first, int head, int row) {
   return (first + row / a.group) * a.ldo + (head * a.group + row % a.group) * a.ldo_head;
@@ -372,20 +562,24 @@ __device__ __forceinline__ void put8(const AttnParams& a, int64_t at, const floa
 }
 
 // Few rows: the kernel reads the cache once and is bound by that.  Each of a block's
-// waves takes every fourth step of the piece, its codes straight to registers, the
-// next step's loads in flight while one is computed; the four results meet in LDS.
-constexpr int kStreamWaves = 4, kStreamThreads = kStreamWaves * kWave;
+// NW waves takes every NW-th step of the piece, its codes straight to registers, the
+// next step's loads in flight while one is computed; the results meet in LDS.  Steps are
+// short and their code stands once: a call of one short sequence is bound by the way
+// through memory to instructions and codes, and a CU has twelve waves of loads in flight.
 template <int D, int MR>
-constexpr int stream_blocks_of_step = D * MR <= 128 ? 4 : 2;
+constexpr int stream_blocks_of_step = 2;
+constexpr int stream_waves_of_simd(int D, int MR, int NW) {
+  return NW > 4 ? 2 : D * MR <= 128 ? 3 : D * MR <= 256 ? 2 : 1;
+}
 
-template <int D, int MR>
-__global__ __launch_bounds__(kStreamThreads, D * MR >= 256 ? 1 : 2) void kv_stream_kernel(AttnParams a) {
+template <int D, int MR, int NW>
+__global__ __launch_bounds__(NW * kWave, (stream_waves_of_simd(D, MR, NW))) void kv_stream_kernel(AttnParams a) {
   constexpr int NB = stream_blocks_of_step<D, MR>, STEP = 16 * NB, NU = D / 64, BM = 16 * MR;
   constexpr int kBatch = kWave / NB;  // steps whose pages a wave looks up together
   extern __shared__ __align__(16) float lds[];
   const KvParams& p = a.c;
   Work w;
-  if (!find_work<kStreamThreads, STEP, BM>(a, w)) return;
+  if (!find_work<NW * kWave, STEP, BM>(a, w)) return;
   const KvEntry& e = w.e;
   const int lane = threadIdx.x & (kWave - 1), wave = uniform(threadIdx.x / kWave);
   const int r0 = w.tile * BM, rows = e.n * a.group;
@@ -394,76 +588,94 @@ __global__ __launch_bounds__(kStreamThreads, D * MR >= 256 ? 1 : 2) void kv_stre
   const Steps<STEP> st(e.total(), p.shift);
   piece_steps<STEP>(st, w, lo, hi, s0, s1);
 
-  Rows<D, MR> t;
-  t.load(a, e, w.head, r0, rows);
-
-  struct Codes {
-    u32x4 k[NB][NU], v[NB][NU];
-  };
   const int64_t page_bytes = int64_t{p.P} * p.D;
-  const int mine = wave < s1 - s0 ? (s1 - s0 - wave + kStreamWaves - 1) / kStreamWaves : 0;  // steps of this wave
-  const int of_codes = max(0, min(mine, (min(s1, st.full_steps) - s0 - wave + kStreamWaves - 1) / kStreamWaves));
-  for (int b0 = 0; b0 < of_codes; b0 += kBatch) {
-    // lane NB j + b: block b of this wave's step b0 + j
-    const int key = (s0 + wave + (b0 + lane / NB) * kStreamWaves) * STEP + 16 * (lane % NB);
-    int id = -1;
+  const int mine = wave < s1 - s0 ? (s1 - s0 - wave + NW - 1) / NW : 0;  // steps of this wave
+  const int of_codes = max(0, min(mine, (min(s1, st.full_steps) - s0 - wave + NW - 1) / NW));
+
+  // A batch of steps' pages.  Lane NB j + b: block b of this wave's step b0 + j.
+  int id = -1;
+  float ks_lane = 0.0f, vs_lane = 0.0f;
+  auto look_up = [&](int b0) {
+    const int key = (s0 + wave + (b0 + lane / NB) * NW) * STEP + 16 * (lane % NB);
+    id = -1;
+    ks_lane = vs_lane = 0.0f;
     if (b0 + lane / NB < of_codes && key < st.full_keys) id = kv_page(p, w.entry, key >> p.shift);
-    float ks_lane = 0.0f, vs_lane = 0.0f;
     if (id >= 0) {
       ks_lane = p.scales[kv_page_at(p, id, 0, w.head)];
       vs_lane = p.scales[kv_page_at(p, id, 1, w.head)];
     }
-    auto fetch = [&](Codes& x, int j) {
+  };
+  struct Codes {
+    u32x4 k[NB][NU], v[NB][NU];
+  };
+  auto fetch = [&](Codes& x, int b0, int j) {
 #pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        const int page = max(__builtin_amdgcn_readlane(id, j * NB + b), 0);
-        const int in_page = ((s0 + wave + (b0 + j) * kStreamWaves) * STEP + 16 * b) & (p.P - 1);
-        const uint8_t* k = p.codes + kv_page_at(p, page, 0, w.head) * page_bytes + in_page * D;
-        const uint8_t* v = k + p.heads * page_bytes;
+    for (int b = 0; b < NB; ++b) {
+      const int page = max(__builtin_amdgcn_readlane(id, j * NB + b), 0);
+      const int in_page = ((s0 + wave + (b0 + j) * NW) * STEP + 16 * b) & (p.P - 1);
+      const uint8_t* k = p.codes + kv_page_at(p, page, 0, w.head) * page_bytes + in_page * D;
+      const uint8_t* v = k + p.heads * page_bytes;
 #pragma unroll
-        for (int c = 0; c < NU; ++c) {
-          x.k[b][c] = *reinterpret_cast<const u32x4*>(k + c * 1024 + lane * 16);
-          x.v[b][c] = *reinterpret_cast<const u32x4*>(v + c * 1024 + lane * 16);
-        }
+      for (int c = 0; c < NU; ++c) {
+        x.k[b][c] = *reinterpret_cast<const u32x4*>(k + c * 1024 + lane * 16);
+        x.v[b][c] = *reinterpret_cast<const u32x4*>(v + c * 1024 + lane * 16);
       }
-    };
-    auto compute = [&](const Codes& x, int j) {
-      float ks[NB][1], vs[NB][1];
-      bool ok[NB], all = true;
+    }
+  };
+
+  // q's loads go out first, then the way to the first codes, then q is prepared
+  Rows<D, MR> t;
+  typename Rows<D, MR>::Raw raw;
+  t.issue(raw, a, e, w.head, r0, rows);
+  Codes x;
+  if (of_codes) {
+    look_up(0);
+    fetch(x, 0, 0);
+  }
+  t.prepare(raw, a);
+
+  f32x4 s[MR][NB];
+  float tops[MR][NB];
+  half8 wt[MR][NB / 2];
+  for (int b0 = 0; b0 < of_codes; b0 += kBatch) {
+    if (b0) {
+      look_up(b0);
+      fetch(x, b0, 0);
+    }
+    const int n = min(kBatch, of_codes - b0);
+#pragma unroll 1
+    for (int j = 0; j < n; ++j) {
+      Codes y = x;
+      if (j + 1 < n) fetch(x, b0, j + 1);
+      float ks[NB], vs[NB];
+      f32x4 mark[NB];
+      bool ok[NB], plain = true;
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
         ok[b] = __builtin_amdgcn_readlane(id, j * NB + b) >= 0;
-        all = all && ok[b];
-        ks[b][0] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(ks_lane), j * NB + b));
-        vs[b][0] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(vs_lane), j * NB + b));
+        ks[b] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(ks_lane), j * NB + b));
+        vs[b] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(vs_lane), j * NB + b));
+        mark[b] = f32x4{} + nan_mark(ks[b], vs[b]);
+        plain = plain && ok[b] && nan_mark(ks[b], vs[b]) == 0.0f;
       }
-      const int key0 = (s0 + wave + (b0 + j) * kStreamWaves) * STEP;
-      const bool masked = !all || key0 < t.all_lo || key0 + STEP > t.all_hi;
-      t.template step<NB, 1>(
-          key0, masked, ks, vs, ok,
-          [&](int b, int k) { return kv_codes8(x.k[b][k / 2][k % 2 * 2], x.k[b][k / 2][k % 2 * 2 + 1]); },
-          [&](int h, int f) { return kv_codes8(x.v[2 * h][f / 4][f % 4], x.v[2 * h + 1][f / 4][f % 4]); });
-    };
-    const int n = min(kBatch, of_codes - b0);
-    Codes x, y;
-    fetch(x, 0);
-    int j = 0;
-    for (; j + 2 <= n; j += 2) {
-      fetch(y, j + 1);
-      compute(x, j);
-      if (j + 2 < n) fetch(x, j + 2);
-      compute(y, j + 1);
+      const int key0 = (s0 + wave + (b0 + j) * NW) * STEP;
+      t.template scores<NB>(s, [&](int b, int k) { return kv_codes8(y.k[b][k / 2][k % 2 * 2], y.k[b][k / 2][k % 2 * 2 + 1]); });
+      if (!plain || key0 < t.all_lo || key0 + STEP > t.all_hi) t.template mask<NB>(s, key0, ok, mark);
+      t.template tops<NB>(s, tops);
+      t.template weights<NB>(s, tops, wt, ks, vs);
+      t.template outputs<NB>(wt, [&](int h, int f) { return kv_codes8(y.v[2 * h][f / 4][f % 4], y.v[2 * h + 1][f / 4][f % 4]); });
     }
-    if (j < n) compute(x, j);
   }
 
   // the tail's steps
+#pragma unroll 1
   for (int i = of_codes; i < mine; ++i) {
-    const int s = s0 + wave + i * kStreamWaves, key0 = st.first(s), in_tail = key0 - st.full_keys;
+    const int key0 = st.first(s0 + wave + i * NW), in_tail = key0 - st.full_keys;
     const int64_t at = kv_page_at(p, e.slot, 0, w.head);
     const char* k = reinterpret_cast<const char*>(p.tails + at * page_bytes);
     const char* v = reinterpret_cast<const char*>(p.tails + (at + p.heads) * page_bytes);
-    float ks[NB][4], vs[NB][4];
+    float ks[NB], vs[NB], k_rel[NB];
+    f32x4 v_rel[NB], mark[NB];
     bool ok[NB];
     int unit[NB];  // (a block behind the page is out of sight; its operands are the page's first)
 #pragma unroll
@@ -471,32 +683,49 @@ __global__ __launch_bounds__(kStreamThreads, D * MR >= 256 ? 1 : 2) void kv_stre
       ok[b] = in_tail + 16 * b < p.P;
       const int block = ok[b] ? in_tail / 16 + b : 0;
       unit[b] = block * NU;
-      const f32x4 x = *reinterpret_cast<const f32x4*>(p.tail_scales + at * p.P + block * 16 + lane / 16 * 4);
-      const f32x4 y = *reinterpret_cast<const f32x4*>(p.tail_scales + (at + p.heads) * p.P + block * 16 + lane / 16 * 4);
+      const int valid = e.total() - key0 - 16 * b;  // tokens of the block
+      const float* k16 = p.tail_scales + at * p.P + block * 16;
+      const float* v16 = k16 + static_cast<int64_t>(p.heads) * p.P;
+      const float k_own = lane % 16 < valid ? k16[lane % 16] : 0.0f, v_own = lane % 16 < valid ? v16[lane % 16] : 0.0f;
+      ks[b] = row_max(k_own);
+      vs[b] = row_max(v_own);
+      k_rel[b] = relative(k_own, ks[b]);
+      const f32x4 k4 = *reinterpret_cast<const f32x4*>(k16 + lane / 16 * 4), v4 = *reinterpret_cast<const f32x4*>(v16 + lane / 16 * 4);
 #pragma unroll
-      for (int i4 = 0; i4 < 4; ++i4) {
-        const bool in = ok[b] && key0 + 16 * b + lane / 16 * 4 + i4 < e.total();
-        ks[b][i4] = in ? x[i4] : 0.0f;
-        vs[b][i4] = in ? y[i4] : 0.0f;
+      for (int j = 0; j < 4; ++j) {
+        const bool in = lane / 16 * 4 + j < valid;
+        v_rel[b][j] = in ? relative(v4[j], vs[b]) : 0.0f;
+        mark[b][j] = in ? nan_mark(k4[j], v4[j]) : 0.0f;
       }
     }
-    t.template step<NB, 4>(
-        key0, true, ks, vs, ok,
-        [&](int b, int c) { return *reinterpret_cast<const half8*>(k + (unit[b] * 2 + c) * 1024 + lane * 16); },
-        [&](int h, int f) {
-          typedef _Float16 half4 __attribute__((ext_vector_type(4)));
-          const int in = f / 4 * 2048 + f % 4 / 2 * 1024 + lane * 16 + f % 2 * 8;
-          const half4 x = *reinterpret_cast<const half4*>(v + unit[2 * h] * 2048 + in);
-          const half4 y = *reinterpret_cast<const half4*>(v + unit[2 * h + 1] * 2048 + in);
-          return __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
-        });
+    t.template scores<NB>(s, [&](int b, int c) {
+      half8 x8 = *reinterpret_cast<const half8*>(k + (unit[b] * 2 + c) * 1024 + lane * 16);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x8[j] = static_cast<_Float16>(static_cast<float>(x8[j]) * k_rel[b]);
+      return x8;
+    });
+    t.template mask<NB>(s, key0, ok, mark);
+    t.template tops<NB>(s, tops);
+    t.template weights<NB>(s, tops, wt, ks, vs);
+    t.template outputs<NB>(wt, [&](int h, int f) {
+      typedef _Float16 half4 __attribute__((ext_vector_type(4)));
+      const int in = f / 4 * 2048 + f % 4 / 2 * 1024 + lane * 16 + f % 2 * 8;
+      half4 x4[2];
+#pragma unroll
+      for (int i2 = 0; i2 < 2; ++i2) {
+        x4[i2] = *reinterpret_cast<const half4*>(v + unit[2 * h + i2] * 2048 + in);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x4[i2][j] = static_cast<_Float16>(static_cast<float>(x4[i2][j]) * v_rel[2 * h + i2][j]);
+      }
+      return __builtin_shufflevector(x4[0], x4[1], 0, 1, 2, 3, 4, 5, 6, 7);
+    });
   }
   t.finish();
 
   // the waves' results of a row together, in their order
   constexpr int LD = D + 4;  // (a row starts four banks behind the one before)
   float* sums = lds;
-  float* ml = lds + kStreamWaves * 16 * LD;
+  float* ml = lds + NW * 16 * LD;
 #pragma unroll
   for (int r = 0; r < MR; ++r) {
     if (r) __syncthreads();
@@ -508,19 +737,19 @@ __global__ __launch_bounds__(kStreamThreads, D * MR >= 256 ? 1 : 2) void kv_stre
       ml[(wave * 16 + lane) * 2 + 1] = t.l[r];
     }
     __syncthreads();
-    for (int item = threadIdx.x; item < 16 * D / 8; item += kStreamThreads) {
+    for (int item = threadIdx.x; item < 16 * D / 8; item += NW * kWave) {
       const int row = item / (D / 8), d = item % (D / 8) * 8, at_row = r0 + 16 * r + row;
       if (at_row >= rows) continue;
-      float m = kNone, l = 0.0f, f[kStreamWaves], v[8] = {};
+      float m = kNone, l = 0.0f, f[NW], v[8] = {};
 #pragma unroll
-      for (int i = 0; i < kStreamWaves; ++i) m = fmaxf(m, ml[(i * 16 + row) * 2]);
+      for (int i = 0; i < NW; ++i) m = fmaxf(m, ml[(i * 16 + row) * 2]);
 #pragma unroll
-      for (int i = 0; i < kStreamWaves; ++i) {
+      for (int i = 0; i < NW; ++i) {
         f[i] = __builtin_amdgcn_exp2f(ml[(i * 16 + row) * 2] - (m == kNone ? 0.0f : m));
         l += f[i] * ml[(i * 16 + row) * 2 + 1];
       }
 #pragma unroll
-      for (int i = 0; i < kStreamWaves; ++i)
+      for (int i = 0; i < NW; ++i)
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] += f[i] * sums[(i * 16 + row) * LD + d + j];
       if (w.pieces == 1) {
@@ -548,10 +777,15 @@ constexpr int tile_frags = D <= 128 ? 2 : 1;
 
 template <int D>
 struct TileLds {
-  half8 k[4][D / 32][kWave];   // [block of 16 keys][32 channels][lane]
-  half8 v[2][D / 16][kWave];   // [32 keys][16 channels][lane]
-  float ks[64], vs[64];
-  int bad[4];
+  half8 k[4][D / 32][kWave];  // [block of 16 keys][32 channels][lane]
+  half8 v[2][D / 16][kWave];  // [32 keys][16 channels][lane]
+  float mark[2][64];          // of the tail's tokens: NaN for one with a NaN, else 0
+};
+// Scales of a step's blocks, keys' and values'; the keys' is -1 where a block's page is
+// none.  Written two steps ahead, read during the products before they are used: four
+// places, one for both of TileLds' two.
+struct TileScales {
+  f32x4 of[4][2];
 };
 
 template <int D>
@@ -560,6 +794,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void kv_tile_kernel(AttnParams a) 
   typedef _Float16 half4 __attribute__((ext_vector_type(4)));
   extern __shared__ __align__(16) char raw_lds[];
   TileLds<D>* lds = reinterpret_cast<TileLds<D>*>(raw_lds);
+  TileScales& steps = *reinterpret_cast<TileScales*>(lds + 2);
   const KvParams& p = a.c;
   Work w;
   if (!find_work<kTileThreads, STEP, BM>(a, w)) return;
@@ -575,101 +810,182 @@ __global__ __launch_bounds__(kTileThreads, 2) void kv_tile_kernel(AttnParams a) 
   if (some) seen(a, e, r0, min(16 * MR, rows - r0), wave_lo, wave_hi);
 
   Rows<D, MR> t;
-  t.load(a, e, w.head, r0, rows);
+  typename Rows<D, MR>::Raw raw;
+  t.issue(raw, a, e, w.head, r0, rows);
 
   // Staging: this wave brings block `block` of 16 keys (waves 0 to 3: keys, 4 to 7:
   // values) of a step into LDS; its scales come with it.
   const int block = wave % 4, which = wave / 4;
   const int64_t page_bytes = int64_t{p.P} * p.D;
-  auto page_of = [&](int s) {  // the page of this wave's block in step s, -1 outside the full pages
-    const int key = st.first(s) + 16 * block;
-    return s < min(s1, st.full_steps) && key < st.full_keys ? kv_page(p, w.entry, key >> p.shift) : -1;
-  };
-  u32x4 st_raw[2 * NU];
-  float st_scale = 0.0f;
-  bool st_ok = false;
-  auto fetch = [&](int s, int page) {
-    const int key0 = st.first(s) + 16 * block;
-    if (s < st.full_steps) {
-      const int64_t at = kv_page_at(p, max(page, 0), which, w.head);
-      const uint8_t* src = p.codes + at * page_bytes + (key0 & (p.P - 1)) * D + lane * 16;
-#pragma unroll
-      for (int c = 0; c < NU; ++c) st_raw[c] = *reinterpret_cast<const u32x4*>(src + c * 1024);
-      st_scale = p.scales[at];
-      st_ok = page >= 0;
+  // Where the block is and its scale, of 64 steps, a lane each.  Vector loads, since a
+  // barrier waits for scalar ones; complete addresses, since a step has no time for them.
+  int from = 0;
+  float scales = 0.0f;
+  uint64_t sources = 0;
+  auto look_up = [&](int s) {
+    const int key = st.first(s + lane) + 16 * block;
+    from = s;
+    if (s + lane < st.full_steps) {
+      const int id = s + lane < s1 && key < st.full_keys ? kv_page(p, w.entry, key >> p.shift) : -1;
+      const int64_t at = kv_page_at(p, max(id, 0), which, w.head);
+      scales = id >= 0 ? p.scales[at] : which ? 0.0f : -1.0f;
+      sources = reinterpret_cast<uint64_t>(p.codes + at * page_bytes + (key & (p.P - 1)) * D);
     } else {
-      const int64_t at = kv_page_at(p, e.slot, which, w.head);
-      st_ok = key0 - st.full_keys < p.P;
-      const int in_tail = st_ok ? key0 - st.full_keys : 0;
-      const char* src = reinterpret_cast<const char*>(p.tails + at * page_bytes + in_tail * D) + lane * 16;
-#pragma unroll
-      for (int c = 0; c < 2 * NU; ++c) st_raw[c] = *reinterpret_cast<const u32x4*>(src + c * 1024);
-      st_scale = p.tail_scales[at * p.P + in_tail + lane % 16];
-      if (key0 + lane % 16 >= e.total()) st_scale = 0.0f;
+      // a block of the tail has the largest scale of its tokens
+      sources = reinterpret_cast<uint64_t>(p.codes);
+      scales = which ? 0.0f : -1.0f;
+      if (s + lane < s1 && key - st.full_keys < p.P) {
+        const float* x = p.tail_scales + kv_page_at(p, e.slot, which, w.head) * p.P + (key - st.full_keys);
+        const int n = min(16, e.total() - key);
+        scales = 0.0f;
+        for (int i = 0; i < n; ++i) scales = fmaxf(scales, x[i]);
+      }
     }
   };
+  auto tell = [&](int s) {  // step s's scale to the others
+    if (s - from < kWave) {
+      const float scale = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(scales), s - from));
+      if (lane == 0) reinterpret_cast<float*>(&steps.of[s & 3][which])[block] = scale;
+    }
+  };
+  // (loaded for every step, from the first page where there are no codes: a load under a
+  // condition would be waited for where the two ways meet)
+  u32x4 st_raw[NU];
+  auto fetch = [&](int s) {
+    if (s - from >= kWave) look_up(s);
+    const uint32_t lo = __builtin_amdgcn_readlane(static_cast<uint32_t>(sources), s - from);
+    const uint32_t hi = __builtin_amdgcn_readlane(static_cast<uint32_t>(sources >> 32), s - from);
+    // (an address made of integers is none of global memory to the compiler unless told,
+    // and a barrier waits for loads that may be LDS's)
+    const GlobalBytes* src = reinterpret_cast<const GlobalBytes*>(static_cast<uint64_t>(hi) << 32 | lo);
+#pragma unroll
+    for (int c = 0; c < NU; ++c) st_raw[c] = *reinterpret_cast<const GlobalPiece*>(src + (c * 1024 + lane * 16));
+  };
   auto stage = [&](int s, TileLds<D>& to) {
-    if (which == 0) {
+    auto put = [&](int c, int h, half8 x) {  // channels 64 c + .. of piece h
+      if (which == 0) {
+        to.k[block][2 * c + h][lane] = x;
+      } else {
+#pragma unroll
+        for (int f = 0; f < 2; ++f)
+          reinterpret_cast<half4*>(&to.v[block / 2][4 * c + 2 * h + f][lane])[block % 2] =
+              f ? __builtin_shufflevector(x, x, 4, 5, 6, 7) : __builtin_shufflevector(x, x, 0, 1, 2, 3);
+      }
+    };
+    if (s < st.full_steps) {
 #pragma unroll
       for (int c = 0; c < NU; ++c)
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-          to.k[block][2 * c + h][lane] = s < st.full_steps ? kv_codes8(st_raw[c][2 * h], st_raw[c][2 * h + 1])
-                                                           : __builtin_bit_cast(half8, st_raw[2 * c + h]);
+        for (int h = 0; h < 2; ++h) put(c, h, kv_codes8(st_raw[c][2 * h], st_raw[c][2 * h + 1]));
     } else {
+      const int key0 = st.first(s) + 16 * block;
+      const int64_t at = kv_page_at(p, e.slot, which, w.head);
+      const bool in = key0 - st.full_keys < p.P;
+      const int in_tail = in ? key0 - st.full_keys : 0;
+      const char* src = reinterpret_cast<const char*>(p.tails + at * page_bytes + in_tail * D) + lane * 16;
+      float token = p.tail_scales[at * p.P + in_tail + lane % 16];
+      if (key0 + lane % 16 >= e.total()) token = 0.0f;
+      const float scale = row_max(token), own = relative(token, scale), mark = nan_mark(token, 0.0f);
+      // of the lane's eight values' tokens: one (keys) or four, twice (values)
+      float rel[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) rel[i] = which ? __shfl(own, lane / 16 * 4 + i) : own;
 #pragma unroll
       for (int c = 0; c < NU; ++c)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const half8 x = s < st.full_steps ? kv_codes8(st_raw[c][2 * h], st_raw[c][2 * h + 1])
-                                            : __builtin_bit_cast(half8, st_raw[2 * c + h]);
+          half8 x = *reinterpret_cast<const half8*>(src + (2 * c + h) * 1024);
 #pragma unroll
-          for (int f = 0; f < 2; ++f)
-            reinterpret_cast<half4*>(&to.v[block / 2][4 * c + 2 * h + f][lane])[block % 2] =
-                f ? __builtin_shufflevector(x, x, 4, 5, 6, 7) : __builtin_shufflevector(x, x, 0, 1, 2, 3);
+          for (int i = 0; i < 8; ++i) x[i] = static_cast<_Float16>(static_cast<float>(x[i]) * rel[i % 4]);
+          put(c, h, x);
         }
+      if (lane < 16) to.mark[which][16 * block + lane] = mark;
     }
-    if (lane < 16) (which ? to.vs : to.ks)[16 * block + lane] = st_ok ? st_scale : 0.0f;
-    if (which == 0 && lane == 0) to.bad[block] = !st_ok;
   };
 
-  int page = page_of(s0);
   if (s0 < s1) {
-    fetch(s0, page);
-    page = page_of(s0 + 1);
-    stage(s0, lds[0]);
+    look_up(s0);
+    fetch(s0);
   }
-  __syncthreads();
-  for (int s = s0; s < s1; ++s) {
-    TileLds<D>& now = lds[(s - s0) & 1];
-    const bool more = s + 1 < s1;
-    if (more) {
-      fetch(s + 1, page);
-      page = page_of(s + 2);
-    }
-    const int key0 = st.first(s);
-    if (some && key0 <= wave_hi && key0 + STEP > wave_lo) {
-      float ks[NB][4], vs[NB][4];
-      bool ok[NB], all = true;
+  t.prepare(raw, a);
+  if (s0 < s1) {
+    tell(s0);
+    tell(s0 + 1);
+    stage(s0, lds[0]);
+    fetch(s0 + 1);
+  }
+  // Each step is two slots between barriers: the softmax with the staging of the next step,
+  // and the matrix products (this step's outputs and the next one's scores).  Waves 4 to 7,
+  // which share the SIMDs with waves 0 to 3, run one slot behind them, so that in every
+  // slot one half keeps the matrix units busy and the other the vector units.  (With slot
+  // 0 the first scores: step s's keys are written in slot 2 s - 1 of the first half and read
+  // in slots 2 s and 2 s + 1, its values written in slot 2 s of the second half and read in
+  // 2 s + 2 and 2 s + 3; each has two places.  The last products read keys of a step that is
+  // not there: whatever scores they give are not used.)
+  if (s0 < s1) {
+    f32x4 sc[MR][NB];
+    float tops[MR][NB];
+    half8 wt[MR][NB / 2];
+    if (which) lds_barrier();
+    lds_barrier();
+    if (some) t.template scores<NB>(sc, [&](int b, int k) { return lds[0].k[b][k][lane]; });
+    f32x4 ks4 = steps.of[s0 & 3][0], vs4 = steps.of[s0 & 3][1];
+#pragma unroll 1
+    for (int s = s0; s < s1; ++s) {
+      TileLds<D>& now = lds[(s - s0) & 1];
+      TileLds<D>& next = lds[(s - s0 + 1) & 1];
+      lds_barrier();
+      if (some) {
+        const int key0 = st.first(s);
+        float ks[NB], vs[NB];
+        uint32_t odd = 0;  // (a negative number and a NaN are above every scale, as bits)
 #pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        const f32x4 x = *reinterpret_cast<const f32x4*>(now.ks + 16 * b + lane / 16 * 4);
-        const f32x4 y = *reinterpret_cast<const f32x4*>(now.vs + 16 * b + lane / 16 * 4);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          ks[b][i] = x[i];
-          vs[b][i] = y[i];
+        for (int b = 0; b < NB; ++b) {
+          ks[b] = ks4[b];
+          vs[b] = vs4[b];
+          odd = max(odd, max(__float_as_uint(ks[b]), __float_as_uint(vs[b])));
         }
-        ok[b] = !now.bad[b];
-        all = all && ok[b];
+        t.template tops<NB>(sc, tops);
+        if (static_cast<uint32_t>(uniform(odd)) >= 0x7f800000u || s >= st.full_steps || key0 < t.all_lo ||
+            key0 + STEP > t.all_hi) {
+          bool ok[NB];
+          f32x4 mark[NB];
+#pragma unroll
+          for (int b = 0; b < NB; ++b) {
+            ok[b] = !(ks[b] < 0.0f);
+            if (s < st.full_steps)
+              mark[b] = f32x4{} + nan_mark(ks[b], vs[b]);
+            else
+              mark[b] = *reinterpret_cast<const f32x4*>(now.mark[0] + 16 * b + lane / 16 * 4) +
+                        *reinterpret_cast<const f32x4*>(now.mark[1] + 16 * b + lane / 16 * 4);
+          }
+          t.template mask<NB>(sc, key0, ok, mark);
+          t.template tops<NB>(sc, tops);
+        }
+        t.template weights<NB>(sc, tops, wt, ks, vs);
       }
-      const bool masked = !all || key0 < t.all_lo || key0 + STEP > t.all_hi;
-      auto key = [&](int b, int k) { return now.k[b][k][lane]; };
-      auto value = [&](int h, int f) { return now.v[h][f][lane]; };
-      t.template step<NB, 4>(key0, masked, ks, vs, ok, key, value);
+      if (s + 1 < s1) stage(s + 1, next);
+      fetch(s + 2);
+      tell(s + 2);
+      lds_barrier();
+      ks4 = steps.of[(s + 1) & 3][0];
+      vs4 = steps.of[(s + 1) & 3][1];
+      if (some) {
+        t.template outputs<NB>(wt, [&](int h, int f) { return now.v[h][f][lane]; });
+        t.template scores<NB>(sc, [&](int b, int k) { return next.k[b][k][lane]; });
+        // Operands are read kAhead before their products: left to itself the compiler reads two
+        // and waits (a read takes about 130 cycles, its products 16 MR).
+        constexpr int kReads = D / 4, kAhead = 6;
+        __builtin_amdgcn_sched_group_barrier(0x100, kAhead, 0);
+#pragma unroll
+        for (int i = 0; i < kReads - kAhead; ++i) {
+          __builtin_amdgcn_sched_group_barrier(0x008, MR, 0);
+          __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        }
+        __builtin_amdgcn_sched_group_barrier(0x008, kAhead * MR, 0);
+      }
     }
-    if (more) stage(s + 1, lds[(s + 1 - s0) & 1]);
-    __syncthreads();
+    if (!which) lds_barrier();
   }
   t.finish();
   if (!some) return;
@@ -699,46 +1015,58 @@ __global__ __launch_bounds__(kTileThreads, 2) void kv_tile_kernel(AttnParams a) 
   }
 }
 
-// Pieces of a row joined in their order.  A block takes every gridDim.y-th row of a cut
-// tile: a thread four channels of every LANES-th piece.
-constexpr int kJoinThreads = 256;
+// Pieces of a row joined in their order.  One wave a row, or where there are few rows the
+// block's four (SPLIT) for one, each with a quarter of the pieces; a lane has four channels.
+constexpr int kJoinThreads = 256, kJoinWaves = kJoinThreads / kWave;
 
-template <int D>
+template <int D, int SPLIT>
 __global__ __launch_bounds__(kJoinThreads) void kv_join_kernel(AttnParams a, int bm) {
-  constexpr int CH = D / 4, GROUPS = kJoinThreads / CH;
-  __shared__ float top[kJoinThreads / kWave], sum[GROUPS][D + 4], sum_l[GROUPS];
+  constexpr int CH = D / 4, PER = kWave / CH, ROWS = kJoinWaves / SPLIT;  // PER pieces at once
+  __shared__ f32x4 sums[kJoinWaves][CH];
+  __shared__ float sums_l[kJoinWaves];
   if (static_cast<int>(blockIdx.x) >= *a.join_count) return;
   const KvJoin j = a.joins[blockIdx.x];
-  const int ch = threadIdx.x % CH, group = threadIdx.x / CH;
-  for (int row = blockIdx.y; row < j.rows; row += gridDim.y) {
+  const int lane = threadIdx.x & (kWave - 1), wave = uniform(threadIdx.x / kWave);
+  const int ch = lane % CH, sub = lane / CH;
+  for (int r = blockIdx.y * ROWS; r < j.rows; r += gridDim.y * ROWS) {
+    const int row = r + wave / SPLIT;
+    const bool in = row < j.rows;
     auto at = [&](int piece) { return (int64_t{j.slot} + int64_t{piece} * j.stride) * bm + row; };
-    float m = kNone;
-    for (int i = threadIdx.x; i < j.pieces; i += kJoinThreads) m = fmaxf(m, a.part_ml[at(i) * 2]);
-    m = wave_max(m);
-    __syncthreads();
-    if (threadIdx.x % kWave == 0) top[threadIdx.x / kWave] = m;
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kJoinThreads / kWave; ++i) m = fmaxf(m, top[i]);
-    const float base = m == kNone ? 0.0f : m;
+    float m = kNone, l = 0.0f;
     f32x4 v{};
-    float l = 0.0f;
-    if (group < GROUPS) {
-      for (int i = group; i < j.pieces; i += GROUPS) {
+    if (in) {
+      for (int i = lane; i < j.pieces; i += kWave) m = fmaxf(m, a.part_ml[at(i) * 2]);
+    }
+    m = wave_max(m);
+    const float base = m == kNone ? 0.0f : m;
+    if (in && sub < PER) {
+#pragma unroll 8
+      for (int i = wave % SPLIT * PER + sub; i < j.pieces; i += SPLIT * PER) {
         const float f = __builtin_amdgcn_exp2f(a.part_ml[at(i) * 2] - base);
         l += f * a.part_ml[at(i) * 2 + 1];
         v += f * *reinterpret_cast<const f32x4*>(a.part + at(i) * D + 4 * ch);
       }
-      *reinterpret_cast<f32x4*>(&sum[group][4 * ch]) = v;
-      if (ch == 0) sum_l[group] = l;
     }
-    __syncthreads();
-    if (group == 0) {
 #pragma unroll
-      for (int i = 1; i < GROUPS; ++i) {
-        v += *reinterpret_cast<const f32x4*>(&sum[i][4 * ch]);
-        l += sum_l[i];
+    for (int d = CH; d < kWave && PER > 1; d *= 2) {
+      l += __shfl_xor(l, d);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] += __shfl_xor(v[i], d);
+    }
+    if constexpr (SPLIT > 1) {
+      __syncthreads();
+      if (lane < CH) sums[wave][lane] = v;
+      if (lane == 0) sums_l[wave] = l;
+      __syncthreads();
+      if (wave % SPLIT == 0 && lane < CH) {
+#pragma unroll
+        for (int i = 1; i < SPLIT; ++i) {
+          v += sums[wave + i][lane];
+          l += sums_l[wave + i];
+        }
       }
+    }
+    if (in && wave % SPLIT == 0 && lane < CH) {
       const float inv = l == 0.0f ? 0.0f : 1.0f / l;
       const float out[4] = {v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv};
       const int64_t to = out_at(a, j.first, j.head, j.row + row) + 4 * ch;
@@ -756,8 +1084,7 @@ __global__ __launch_bounds__(kJoinThreads) void kv_join_kernel(AttnParams a, int
 struct Cut {
   bool use;
   int bm, target, least_steps, rows_above, rows_most;
-  int64_t tiles, slots, joins;  // upper bounds, kv heads included
-  int64_t blocks() const { return target + tiles; }
+  int64_t tiles, slots, joins, blocks;  // upper bounds, kv heads included
 };
 struct Plan {
   Cut stream, tile;
@@ -767,18 +1094,22 @@ struct Plan {
 // Keys below which a sequence stays in one piece and no join is launched.
 constexpr int64_t kWholeKeys = 1024;
 
-Cut make_cut(const KvParams& p, int group, int bm, int step, int target, int least_steps) {
+Cut make_cut(const KvParams& p, int group, int bm, int step, int target, int least_steps, int rows_above, int rows_most) {
   Cut c{};
   c.use = true;
   c.bm = bm;
-  c.rows_most = INT_MAX;
-  const int64_t rows = int64_t{p.tokens} * group;
-  c.tiles = (p.cu ? rows / bm + std::min(p.entries, p.tokens) : int64_t{p.entries} * ((group + bm - 1) / bm)) * p.heads;
-  const int64_t keys = int64_t{p.width} << p.shift, steps = keys / step + 2;
+  c.rows_above = rows_above;
+  c.rows_most = rows_most;
+  const int64_t rows = int64_t{p.tokens} * group, entries = std::min(p.entries, p.tokens);
+  c.tiles = p.cu ? rows / bm + entries : entries * ((group + bm - 1) / bm);
+  c.tiles = std::min(c.tiles, entries * ((int64_t{rows_most} + bm - 1) / bm)) * p.heads;
+  c.blocks = c.tiles;
+  const int64_t keys = int64_t{p.width} << p.shift, most = (keys / step + 2 + least_steps - 1) / least_steps;
   if (keys <= kWholeKeys || (p.entries == 1 && rows / bm * p.heads >= target)) return c;
   c.target = target;
   c.least_steps = least_steps;
-  c.slots = std::min(int64_t{2} * target, c.tiles * ((steps + least_steps - 1) / least_steps));
+  c.blocks = std::min(target + c.tiles, c.tiles * most);
+  c.slots = std::min(int64_t{2} * target, c.tiles * most);
   c.joins = std::min(int64_t{target}, c.tiles);
   return c;
 }
@@ -787,11 +1118,14 @@ template <int D>
 Plan make_plan(const KvParams& p, int group) {
   Plan x{};
   x.mr = group > 16 || (p.cu && p.tokens > p.entries) ? 2 : 1;
-  const int most = 32, rows = static_cast<int>(std::min(int64_t{p.tokens} * group, int64_t{INT_MAX}));
-  const bool stream = !p.cu || rows <= most, tile = !stream && p.entries == 1;
-  if (!tile) x.stream = make_cut(p, group, 16 * x.mr, 16 * (x.mr == 1 ? stream_blocks_of_step<D, 1> : stream_blocks_of_step<D, 2>), 1024, 8);
-  if (!stream) x.tile = make_cut(p, group, 16 * tile_frags<D> * kTileWaves, 64, 256, 8);
-  if (!tile && !stream) x.stream.rows_most = x.tile.rows_above = most;
+  const int most = 32, all = INT_MAX / 2;
+  const int64_t rows = int64_t{p.tokens} * group;
+  const bool stream = !p.cu || rows <= most, tile = !stream && p.entries == 1, both = !stream && !tile;
+  if (!tile) {
+    const int step = 16 * (x.mr == 1 ? stream_blocks_of_step<D, 1> : stream_blocks_of_step<D, 2>);
+    x.stream = make_cut(p, group, 16 * x.mr, step, 768, 16, 0, both ? most : all);
+  }
+  if (!stream) x.tile = make_cut(p, group, 16 * tile_frags<D> * kTileWaves, 64, 256, 8, both ? most : 0, all);
   return x;
 }
 
@@ -845,17 +1179,22 @@ hipError_t allow_lds(K kernel, int bytes) {
 template <int D>
 hipError_t join(const AttnParams& a, const Cut& c, hipStream_t s) {
   if (!c.target) return hipSuccess;
-  const int64_t rows = std::max<int64_t>(1, std::min<int64_t>(c.bm, 2048 / c.joins));
-  kv_join_kernel<D><<<dim3(c.joins, rows), kJoinThreads, 0, s>>>(a, c.bm);
+  const int64_t rows = c.rows_most < c.bm ? c.rows_most : c.bm;
+  if (c.joins * rows >= 1024) {
+    const int64_t y = std::max<int64_t>(1, std::min<int64_t>((rows + 3) / 4, 2048 / c.joins));
+    kv_join_kernel<D, 1><<<dim3(c.joins, y), kJoinThreads, 0, s>>>(a, c.bm);
+  } else {
+    kv_join_kernel<D, kJoinWaves><<<dim3(c.joins, rows), kJoinThreads, 0, s>>>(a, c.bm);
+  }
   return hipGetLastError();
 }
 
-template <int D, int MR>
+template <int D, int MR, int NW>
 hipError_t run_stream(const AttnParams& a, const Cut& c, hipStream_t s) {
-  constexpr int kLds = (kStreamWaves * 16 * (D + 4) + kStreamWaves * 16 * 2) * 4;
-  static const hipError_t allowed = allow_lds(kv_stream_kernel<D, MR>, kLds);
+  constexpr int kLds = (NW * 16 * (D + 4) + NW * 16 * 2) * 4;
+  static const hipError_t allowed = allow_lds(kv_stream_kernel<D, MR, NW>, kLds);
   if (allowed != hipSuccess) return allowed;
-  kv_stream_kernel<D, MR><<<c.blocks(), kStreamThreads, kLds, s>>>(a);
+  kv_stream_kernel<D, MR, NW><<<c.blocks, NW * kWave, kLds, s>>>(a);
   const hipError_t e = hipGetLastError();
   return e != hipSuccess ? e : join<D>(a, c, s);
 }
@@ -865,24 +1204,25 @@ hipError_t run(const KvAttention& k, char* ws, hipStream_t s) {
   const Plan x = make_plan<D>(k.c, k.group);
   const Area sa = area(x.stream, D, 0), ta = area(x.tile, D, sa.end);
   if (x.tile.use) {
-    constexpr int kLds = 2 * sizeof(TileLds<D>);
+    constexpr int kLds = 2 * sizeof(TileLds<D>) + sizeof(TileScales);
     static const hipError_t allowed = allow_lds(kv_tile_kernel<D>, kLds);
     if (allowed != hipSuccess) return allowed;
     const AttnParams a = with(k, x.tile, ta, ws);
-    kv_tile_kernel<D><<<x.tile.blocks(), kTileThreads, kLds, s>>>(a);
+    kv_tile_kernel<D><<<x.tile.blocks, kTileThreads, kLds, s>>>(a);
     hipError_t e = hipGetLastError();
     if (e == hipSuccess) e = join<D>(a, x.tile, s);
     if (e != hipSuccess) return e;
   }
   if (!x.stream.use) return hipSuccess;
   const AttnParams a = with(k, x.stream, sa, ws);
-  return x.mr == 1 ? run_stream<D, 1>(a, x.stream, s) : run_stream<D, 2>(a, x.stream, s);
+  if (x.mr == 2) return run_stream<D, 2, 4>(a, x.stream, s);
+  return x.stream.target || x.stream.blocks > 256 ? run_stream<D, 1, 4>(a, x.stream, s) : run_stream<D, 1, 8>(a, x.stream, s);
 }
 
 template <int D>
 int64_t bytes(const KvParams& p, int group, int64_t* blocks) {
   const Plan x = make_plan<D>(p, group);
-  *blocks = std::max(x.stream.use ? x.stream.blocks() : 0, x.tile.use ? x.tile.blocks() : 0);
+  *blocks = std::max(x.stream.blocks, x.tile.blocks);
   return area(x.tile, D, area(x.stream, D, 0).end).end;
 }
 

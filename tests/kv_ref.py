@@ -39,8 +39,8 @@ def attention(q, k, v, first, scale, window=0, hidden=None):
     last rounding, the same shape.
 
     The kernel's sums, maxima and exponentials are binary32, its products exact in binary32 up to that, a weight
-    is rounded to 11 bits: of relative 2^-11, or, below 2^-14 of its format's range (which starts at 2^14), of
-    2^-39 of the largest.  A sum of n terms is off by at most n 2^-23 of the sum of magnitudes, a score by D 2^-23 of its
+    is rounded to fp16 as a multiple of 2^-11 of the largest that there can be: by relative 2^-11, or, among fp16's
+    subnormal numbers (steps of 2^-24), by half of 2^-24 2^-11 = 2^-36 of the largest.  A sum of n terms is off by at most n 2^-23 of the sum of magnitudes, a score by D 2^-23 of its
     products' magnitudes, and 8 more roundings on the way."""
     q, k, v = (t.detach().double().cpu() for t in (q, k, v))
     n, heads, D = q.shape
@@ -75,7 +75,7 @@ def attention(q, k, v, first, scale, window=0, hidden=None):
         delta = (D + 8) * 2.0 ** -23 * size + 2.0 ** -22
         mass = p[:, some] @ vv[some].abs()
         most = vv[some].abs().amax(0, keepdim=True) if some.numel() else 0.0
-        far[:, h] = (2.0 ** -11 + 2.1 * delta + (total + 16) * 2.0 ** -23) * mass + total * 2.0 ** -38 * most
+        far[:, h] = (2.0 ** -11 + 2.1 * delta + (total + 16) * 2.0 ** -23) * mass + total * 2.0 ** -36 * most
     return out, far
 
 
