@@ -123,15 +123,6 @@ __device__ __forceinline__ Count entry_blocks(const AttnParams& a, int tiles, in
   return c;
 }
 
-__device__ __forceinline__ uint32_t wave_scan(uint32_t v) {  // sum over the lanes up to this one
-  v += __builtin_amdgcn_update_dpp(0u, v, 0x111, 0xF, 0xF, false);  // row_shr 1, 2, 4, 8
-  v += __builtin_amdgcn_update_dpp(0u, v, 0x112, 0xF, 0xF, false);
-  v += __builtin_amdgcn_update_dpp(0u, v, 0x114, 0xF, 0xF, false);
-  v += __builtin_amdgcn_update_dpp(0u, v, 0x118, 0xF, 0xF, false);
-  v += __builtin_amdgcn_update_dpp(0u, v, 0x142, 0xA, 0xF, false);  // lane 15 and 47 of the row before
-  v += __builtin_amdgcn_update_dpp(0u, v, 0x143, 0xC, 0xF, false);  // lane 31
-  return v;
-}
 __device__ __forceinline__ float wave_total(float v) {
 #pragma unroll
   for (int d = 1; d < kWave; d *= 2) v += __shfl_xor(v, d);

@@ -31,6 +31,40 @@ __device__ __forceinline__ int find_page(const KvParams& p, int index, KvEntry& 
     number = e.len >> p.shift;
     return e.n > 0 ? index : -1;
   }
+  if (p.entries <= 4 * kWave) {
+    // every wave finds it by itself, up to four entries a lane, without a barrier
+    const int lane = threadIdx.x & (kWave - 1), per = (p.entries + kWave - 1) / kWave;
+    KvEntry x[4];
+    uint32_t c[4], own = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int i = lane * per + k;
+      x[k] = KvEntry{};
+      if (k < per && i < p.entries) x[k] = kv_entry(p, i);
+      c[k] = static_cast<uint32_t>(kv_touched(p, x[k]));
+      own += c[k];
+    }
+    uint32_t in = static_cast<uint32_t>(index) - (wave_scan(own) - own);
+    const uint64_t here = __ballot(in < own);
+    if (!here) return -1;
+    const int from = __builtin_ctzll(here);
+    int mine = 0;
+#pragma unroll
+    for (int k = 0; k < 3; ++k)
+      if (mine == k && in >= c[k]) {
+        in -= c[k];
+        mine = k + 1;
+      }
+#pragma unroll
+    for (int k = 1; k < 4; ++k)
+      if (mine == k) x[0] = x[k];
+    e.len = __builtin_amdgcn_readlane(x[0].len, from);
+    e.n = __builtin_amdgcn_readlane(x[0].n, from);
+    e.first = __builtin_amdgcn_readlane(x[0].first, from);
+    e.slot = __builtin_amdgcn_readlane(x[0].slot, from);
+    number = (e.len >> p.shift) + __builtin_amdgcn_readlane(static_cast<int>(in), from);
+    return from * per + __builtin_amdgcn_readlane(mine, from);
+  }
   if (threadIdx.x == 0) found[0] = -1;
   const int per = (p.entries + kThreads - 1) / kThreads;
   const int a = threadIdx.x * per, b = min(a + per, p.entries);
@@ -50,10 +84,10 @@ __device__ __forceinline__ int find_page(const KvParams& p, int index, KvEntry& 
     }
   }
   __syncthreads();
-  const int i = found[0];
+  const int i = __builtin_amdgcn_readfirstlane(found[0]);
   if (i < 0) return -1;
   e = kv_entry(p, i);
-  number = (e.len >> p.shift) + found[1];
+  number = (e.len >> p.shift) + __builtin_amdgcn_readfirstlane(found[1]);
   return i;
 }
 

@@ -111,6 +111,16 @@ __device__ __forceinline__ half8 kv_codes8(uint32_t a, uint32_t b) {
   return half8{r0[0], r0[1], r1[0], r1[1], r2[0], r2[1], r3[0], r3[1]};
 }
 
+__device__ __forceinline__ uint32_t wave_scan(uint32_t v) {  // sum over the lanes up to this one
+  v += __builtin_amdgcn_update_dpp(0u, v, 0x111, 0xF, 0xF, false);  // row_shr 1, 2, 4, 8
+  v += __builtin_amdgcn_update_dpp(0u, v, 0x112, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0u, v, 0x114, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0u, v, 0x118, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0u, v, 0x142, 0xA, 0xF, false);  // lane 15 and 47 of the row before
+  v += __builtin_amdgcn_update_dpp(0u, v, 0x143, 0xC, 0xF, false);  // lane 31
+  return v;
+}
+
 // Sum over the block's threads up to and including this one (`total`: over all).
 // buf: one slot a wave; every thread calls it, and a barrier stands between two calls
 // that use the same buf.
