@@ -56,6 +56,7 @@ struct AttnParams {
   // keys are cut into pieces of at least least_steps steps, about `target` of all tiles
   // together (0: never cut)
   int target, least_steps;
+  uint32_t blocks;
   KvJoin* joins;      // of tiles in pieces, *join_count of them
   int* join_count;
   float* part;        // [slot][rows of a tile][D] sums, then
@@ -134,11 +135,21 @@ __device__ __forceinline__ float wave_total(float v) {
 // index falls.  Up to 256 entries every wave does so by itself, up to four entries a
 // lane, without a barrier; more are the block's together.
 template <int THREADS, int STEP, int BM>
-__device__ __forceinline__ bool find_work(const AttnParams& a, Work& w) {
+__device__ __forceinline__ bool find_work(const AttnParams& a, uint32_t block, Work& w) {
   const KvParams& p = a.c;
   const int lane = threadIdx.x & (kWave - 1);
-  const uint32_t want = blockIdx.x / p.heads;
-  w.head = blockIdx.x % p.heads;
+  const uint32_t want = block / p.heads;
+  w.head = block % p.heads;
+  if (!a.target && !p.cu) {  // every entry has one token, every tile one block
+    const uint32_t tiles = (a.group + BM - 1) / BM;
+    w.entry = want / tiles;
+    w.e = kv_entry(p, w.entry);
+    w.tiles = tiles;
+    w.tile = want % tiles;
+    w.pieces = 1;
+    w.piece = w.slot = 0;
+    return w.e.n > 0;
+  }
   uint32_t total_blocks, total_cut;
   int index, cut_before;
   if (p.entries <= 4 * kWave) {
@@ -263,8 +274,8 @@ __device__ __forceinline__ bool find_work(const AttnParams& a, Work& w) {
     }
   }
   // (entries that share tokens can need more blocks than there are: such a call does nothing)
-  const bool fits = static_cast<uint64_t>(total_blocks) * p.heads <= gridDim.x;
-  if (a.target && blockIdx.x == 0 && threadIdx.x == 0)
+  const bool fits = static_cast<uint64_t>(total_blocks) * p.heads <= a.blocks;
+  if (a.target && block == 0 && threadIdx.x == 0)
     *a.join_count = fits ? static_cast<int>(total_cut & 4095) * p.heads : 0;
   if (!fits || w.entry < 0) return false;
   // the last rows see the most keys: their tiles first
@@ -362,42 +373,46 @@ struct Rows {
     inv = kUnit / kLeastUnit;
   }
 
-  template <typename T>
-  __device__ __forceinline__ void scale_q(const Raw& raw, float scale) {
-    // the largest finite magnitude of the tile, as bits
-    uint32_t top = 0;
-#pragma unroll
-    for (int r = 0; r < MR; ++r)
-#pragma unroll
-      for (int k = 0; k < D / 32; ++k)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float x, y;
-          T::unpack(raw.x[r][k][i], x, y);
-          const uint32_t bx = __float_as_uint(x) & 0x7fffffffu, by = __float_as_uint(y) & 0x7fffffffu;
-          top = max(top, max(bx < 0x7f800000u ? bx : 0u, by < 0x7f800000u ? by : 0u));
-        }
-    top = __float_as_uint(wave_max(__uint_as_float(top)));
-    const int exp = max(static_cast<int>(top >> 23) - 127 - 14, -126);
-    // the scale's sign is q's (the largest score is then the largest product)
-    const float sign = scale < 0.0f ? -1.0f : scale > 0.0f ? 1.0f : 0.0f;
-    const float mul = sign * __uint_as_float(static_cast<uint32_t>(127 - exp) << 23);
-    c = fabsf(scale) * kLog2e * __uint_as_float(static_cast<uint32_t>(127 + exp) << 23);
-#pragma unroll
-    for (int r = 0; r < MR; ++r)
-#pragma unroll
-      for (int k = 0; k < D / 32; ++k)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float x, y;
-          T::unpack(raw.x[r][k][i], x, y);
-          q[r][k][2 * i] = static_cast<_Float16>(x * mul);
-          q[r][k][2 * i + 1] = static_cast<_Float16>(y * mul);
-        }
-  }
+  // fp16 operands; the scale's sign is q's (the largest score is then the largest product).
   __device__ __forceinline__ void prepare(const Raw& raw, const AttnParams& a) {
-    if (a.bf16) scale_q<Bf16>(raw, a.scale);
-    else scale_q<F16>(raw, a.scale);
+    c = fabsf(a.scale) * kLog2e;
+    if (!a.bf16) {
+      const uint32_t keep = a.scale == 0.0f ? 0u : ~0u, flip = a.scale < 0.0f ? 0x80008000u : 0u;
+#pragma unroll
+      for (int r = 0; r < MR; ++r)
+#pragma unroll
+        for (int k = 0; k < D / 32; ++k) q[r][k] = __builtin_bit_cast(half8, (raw.x[r][k] & keep) ^ flip);
+      return;
+    }
+    // The largest finite magnitude of the tile: with 0x80 added to its bits an infinity or a
+    // NaN is a negative number to the signed maximum.
+    typedef short short2v __attribute__((ext_vector_type(2)));
+    short2v most = {0, 0};
+#pragma unroll
+    for (int r = 0; r < MR; ++r)
+#pragma unroll
+      for (int k = 0; k < D / 32; ++k)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t w = raw.x[r][k][i] & 0x7fff7fffu;
+          most = __builtin_elementwise_max(most, __builtin_bit_cast(short2v, w) + short2v{0x80, 0x80});
+        }
+    const float top = wave_max(static_cast<float>(max(most[0], most[1])));
+    const int exp = max((max(static_cast<int>(top) - 0x80, 0) >> 7) - 127 - 14, -126);
+    const float sign = a.scale < 0.0f ? -1.0f : a.scale > 0.0f ? 1.0f : 0.0f;
+    const float mul = sign * __uint_as_float(static_cast<uint32_t>(127 - exp) << 23);
+    c *= __uint_as_float(static_cast<uint32_t>(127 + exp) << 23);
+#pragma unroll
+    for (int r = 0; r < MR; ++r)
+#pragma unroll
+      for (int k = 0; k < D / 32; ++k)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          typedef float f32x2 __attribute__((ext_vector_type(2)));
+          const half2v h = __builtin_convertvector((f32x2{bf16_lo(raw.x[r][k][i]) * mul, bf16_hi(raw.x[r][k][i]) * mul}), half2v);
+          q[r][k][2 * i] = h[0];
+          q[r][k][2 * i + 1] = h[1];
+        }
   }
 
   // One step, 16 NB keys, in three parts.  s: products of q and the keys.  key(b, k): a
@@ -557,20 +572,17 @@ __device__ __forceinline__ void put8(const AttnParams& a, int64_t at, const floa
 // next step's loads in flight while one is computed; the results meet in LDS.  Steps are
 // short and their code stands once: a call of one short sequence is bound by the way
 // through memory to instructions and codes, and a CU has twelve waves of loads in flight.
-template <int D, int MR>
-constexpr int stream_blocks_of_step = 2;
 constexpr int stream_waves_of_simd(int D, int MR, int NW) {
   return NW > 4 ? 2 : D * MR <= 128 ? 3 : D * MR <= 256 ? 2 : 1;
 }
 
 template <int D, int MR, int NW>
-__global__ __launch_bounds__(NW * kWave, (stream_waves_of_simd(D, MR, NW))) void kv_stream_kernel(AttnParams a) {
-  constexpr int NB = stream_blocks_of_step<D, MR>, STEP = 16 * NB, NU = D / 64, BM = 16 * MR;
+__device__ __forceinline__ void stream_block(const AttnParams& a, uint32_t index, float* lds) {
+  constexpr int NB = 2, STEP = 16 * NB, NU = D / 64, BM = 16 * MR;
   constexpr int kBatch = kWave / NB;  // steps whose pages a wave looks up together
-  extern __shared__ __align__(16) float lds[];
   const KvParams& p = a.c;
   Work w;
-  if (!find_work<NW * kWave, STEP, BM>(a, w)) return;
+  if (!find_work<NW * kWave, STEP, BM>(a, index, w)) return;
   const KvEntry& e = w.e;
   const int lane = threadIdx.x & (kWave - 1), wave = uniform(threadIdx.x / kWave);
   const int r0 = w.tile * BM, rows = e.n * a.group;
@@ -580,8 +592,9 @@ __global__ __launch_bounds__(NW * kWave, (stream_waves_of_simd(D, MR, NW))) void
   piece_steps<STEP>(st, w, lo, hi, s0, s1);
 
   const int64_t page_bytes = int64_t{p.P} * p.D;
-  const int mine = wave < s1 - s0 ? (s1 - s0 - wave + NW - 1) / NW : 0;  // steps of this wave
-  const int of_codes = max(0, min(mine, (min(s1, st.full_steps) - s0 - wave + NW - 1) / NW));
+  // This wave's steps: every NW-th of the pages', and the tail's from the last wave on.
+  const int codes = min(s1, st.full_steps) - s0, tail0 = max(s0, st.full_steps);
+  const int of_codes = wave < codes ? (codes - wave + NW - 1) / NW : 0;
 
   // A batch of steps' pages.  Lane NB j + b: block b of this wave's step b0 + j.
   int id = -1;
@@ -660,55 +673,53 @@ __global__ __launch_bounds__(NW * kWave, (stream_waves_of_simd(D, MR, NW))) void
 
   // the tail's steps
 #pragma unroll 1
-  for (int i = of_codes; i < mine; ++i) {
-    const int key0 = st.first(s0 + wave + i * NW), in_tail = key0 - st.full_keys;
+  for (int i = tail0 + NW - 1 - wave; i < s1; i += NW) {
+    const int key0 = st.first(i), in_tail = key0 - st.full_keys;
     const int64_t at = kv_page_at(p, e.slot, 0, w.head);
-    const char* k = reinterpret_cast<const char*>(p.tails + at * page_bytes);
-    const char* v = reinterpret_cast<const char*>(p.tails + (at + p.heads) * page_bytes);
-    float ks[NB], vs[NB], k_rel[NB];
-    f32x4 v_rel[NB], mark[NB];
+    const char* k = reinterpret_cast<const char*>(p.tails + at * page_bytes) + lane * 16;
+    const char* v = k + p.heads * page_bytes * 2;
+    half8 xk[NB][2 * NU], xv[NB][2 * NU];
+    float ks[NB], vs[NB];
+    f32x4 mark[NB];
     bool ok[NB];
-    int unit[NB];  // (a block behind the page is out of sight; its operands are the page's first)
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
+      // (a block behind the page is out of sight; its operands are the page's first)
       ok[b] = in_tail + 16 * b < p.P;
       const int block = ok[b] ? in_tail / 16 + b : 0;
-      unit[b] = block * NU;
+#pragma unroll
+      for (int c = 0; c < 2 * NU; ++c) {
+        xk[b][c] = *reinterpret_cast<const half8*>(k + (block * 2 * NU + c) * 1024);
+        xv[b][c] = *reinterpret_cast<const half8*>(v + (block * 2 * NU + c) * 1024);
+      }
       const int valid = e.total() - key0 - 16 * b;  // tokens of the block
       const float* k16 = p.tail_scales + at * p.P + block * 16;
       const float* v16 = k16 + static_cast<int64_t>(p.heads) * p.P;
       const float k_own = lane % 16 < valid ? k16[lane % 16] : 0.0f, v_own = lane % 16 < valid ? v16[lane % 16] : 0.0f;
       ks[b] = row_max(k_own);
       vs[b] = row_max(v_own);
-      k_rel[b] = relative(k_own, ks[b]);
-      const f32x4 k4 = *reinterpret_cast<const f32x4*>(k16 + lane / 16 * 4), v4 = *reinterpret_cast<const f32x4*>(v16 + lane / 16 * 4);
+      const float k_rel = relative(k_own, ks[b]), v_lane = relative(v_own, vs[b]), nan = nan_mark(k_own, v_own);
+      float v_rel[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const bool in = lane / 16 * 4 + j < valid;
-        v_rel[b][j] = in ? relative(v4[j], vs[b]) : 0.0f;
-        mark[b][j] = in ? nan_mark(k4[j], v4[j]) : 0.0f;
+        v_rel[j] = __shfl(v_lane, lane / 16 * 4 + j);
+        mark[b][j] = __shfl(nan, lane / 16 * 4 + j);
       }
-    }
-    t.template scores<NB>(s, [&](int b, int c) {
-      half8 x8 = *reinterpret_cast<const half8*>(k + (unit[b] * 2 + c) * 1024 + lane * 16);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) x8[j] = static_cast<_Float16>(static_cast<float>(x8[j]) * k_rel[b]);
-      return x8;
-    });
+      for (int c = 0; c < 2 * NU; ++c)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          xk[b][c][j] = static_cast<_Float16>(static_cast<float>(xk[b][c][j]) * k_rel);
+          xv[b][c][j] = static_cast<_Float16>(static_cast<float>(xv[b][c][j]) * v_rel[j % 4]);
+        }
+    }
+    t.template scores<NB>(s, [&](int b, int c) { return xk[b][c]; });
     t.template mask<NB>(s, key0, ok, mark);
     t.template tops<NB>(s, tops);
     t.template weights<NB>(s, tops, wt, ks, vs);
     t.template outputs<NB>(wt, [&](int h, int f) {
-      typedef _Float16 half4 __attribute__((ext_vector_type(4)));
-      const int in = f / 4 * 2048 + f % 4 / 2 * 1024 + lane * 16 + f % 2 * 8;
-      half4 x4[2];
-#pragma unroll
-      for (int i2 = 0; i2 < 2; ++i2) {
-        x4[i2] = *reinterpret_cast<const half4*>(v + unit[2 * h + i2] * 2048 + in);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) x4[i2][j] = static_cast<_Float16>(static_cast<float>(x4[i2][j]) * v_rel[2 * h + i2][j]);
-      }
-      return __builtin_shufflevector(x4[0], x4[1], 0, 1, 2, 3, 4, 5, 6, 7);
+      const half8 x0 = xv[2 * h][f / 2], x1 = xv[2 * h + 1][f / 2];
+      return f % 2 ? __builtin_shufflevector(x0, x1, 4, 5, 6, 7, 12, 13, 14, 15) : __builtin_shufflevector(x0, x1, 0, 1, 2, 3, 8, 9, 10, 11);
     });
   }
   t.finish();
@@ -760,6 +771,12 @@ __global__ __launch_bounds__(NW * kWave, (stream_waves_of_simd(D, MR, NW))) void
   }
 }
 
+template <int D, int MR, int NW>
+__global__ __launch_bounds__(NW * kWave, (stream_waves_of_simd(D, MR, NW))) void kv_stream_kernel(AttnParams a) {
+  extern __shared__ __align__(16) float stream_lds[];
+  stream_block<D, MR, NW>(a, blockIdx.x, stream_lds);
+}
+
 // Many rows: eight waves of 16 MR rows each share every step's keys and values, which
 // are made fp16 once, on their way into LDS.
 constexpr int kTileWaves = 8, kTileThreads = kTileWaves * kWave;
@@ -780,15 +797,14 @@ struct TileScales {
 };
 
 template <int D>
-__global__ __launch_bounds__(kTileThreads, 2) void kv_tile_kernel(AttnParams a) {
+__device__ __forceinline__ void tile_block(const AttnParams& a, uint32_t index, char* raw_lds) {
   constexpr int MR = tile_frags<D>, BM = 16 * MR * kTileWaves, STEP = 64, NB = 4, NU = D / 64;
   typedef _Float16 half4 __attribute__((ext_vector_type(4)));
-  extern __shared__ __align__(16) char raw_lds[];
   TileLds<D>* lds = reinterpret_cast<TileLds<D>*>(raw_lds);
   TileScales& steps = *reinterpret_cast<TileScales*>(lds + 2);
   const KvParams& p = a.c;
   Work w;
-  if (!find_work<kTileThreads, STEP, BM>(a, w)) return;
+  if (!find_work<kTileThreads, STEP, BM>(a, index, w)) return;
   const KvEntry& e = w.e;
   const int lane = threadIdx.x & (kWave - 1), wave = uniform(threadIdx.x / kWave);
   const int t0 = w.tile * BM, rows = e.n * a.group, r0 = t0 + wave * 16 * MR;
@@ -1020,17 +1036,41 @@ __global__ __launch_bounds__(kTileThreads, 2) void kv_tile_kernel(AttnParams a) 
   }
 }
 
+template <int D>
+__global__ __launch_bounds__(kTileThreads, 2) void kv_tile_kernel(AttnParams a) {
+  extern __shared__ __align__(16) char tile_lds[];
+  tile_block<D>(a, blockIdx.x, tile_lds);
+}
+
+// Entries of many and of few rows together, each kind by its blocks: one launch, and neither
+// waits for the other (9 entries, 501 tokens at most, D = 64: in two launches 12 us more).
+template <int D>
+__global__ __launch_bounds__(kTileThreads, 2) void kv_mixed_kernel(AttnParams many, AttnParams few) {
+  extern __shared__ __align__(16) char mixed_lds[];
+  if (blockIdx.x < many.blocks) tile_block<D>(many, blockIdx.x, mixed_lds);
+  else stream_block<D, 1, kTileWaves>(few, blockIdx.x - many.blocks, reinterpret_cast<float*>(mixed_lds));
+}
+
 // Pieces of a row joined in their order.  One wave a row, or where there are few rows the
 // block's four (SPLIT) for one, each with a quarter of the pieces; a lane has four channels.
 constexpr int kJoinThreads = 256, kJoinWaves = kJoinThreads / kWave;
 
 template <int D, int SPLIT>
-__global__ __launch_bounds__(kJoinThreads) void kv_join_kernel(AttnParams a, int bm) {
+__global__ __launch_bounds__(kJoinThreads) void kv_join_kernel(AttnParams a, int bm, int joins, AttnParams b, int b_bm) {
   constexpr int CH = D / 4, PER = kWave / CH, ROWS = kJoinWaves / SPLIT;  // PER pieces at once
   __shared__ f32x4 sums[kJoinWaves][CH];
   __shared__ float sums_l[kJoinWaves];
-  if (static_cast<int>(blockIdx.x) >= *a.join_count) return;
-  const KvJoin j = a.joins[blockIdx.x];
+  int index = blockIdx.x;
+  if (index >= joins) {
+    index -= joins;
+    a.joins = b.joins;
+    a.join_count = b.join_count;
+    a.part = b.part;
+    a.part_ml = b.part_ml;
+    bm = b_bm;
+  }
+  if (index >= *a.join_count) return;
+  const KvJoin j = a.joins[index];
   const int lane = threadIdx.x & (kWave - 1), wave = uniform(threadIdx.x / kWave);
   const int ch = lane % CH, sub = lane / CH;
   for (int r = blockIdx.y * ROWS; r < j.rows; r += gridDim.y * ROWS) {
@@ -1122,14 +1162,13 @@ Cut make_cut(const KvParams& p, int group, int bm, int step, int target, int lea
 template <int D>
 Plan make_plan(const KvParams& p, int group) {
   Plan x{};
-  x.mr = group > 16 || (p.cu && p.tokens > p.entries) ? 2 : 1;
   const int most = 32, all = INT_MAX / 2;
   const int64_t rows = int64_t{p.tokens} * group;
   const bool stream = !p.cu || rows <= most, tile = !stream && p.entries == 1, both = !stream && !tile;
-  if (!tile) {
-    const int step = 16 * (x.mr == 1 ? stream_blocks_of_step<D, 1> : stream_blocks_of_step<D, 2>);
-    x.stream = make_cut(p, group, 16 * x.mr, step, 768, 16, 0, both ? most : all);
-  }
+  x.mr = stream && (group > 16 || (p.cu && p.tokens > p.entries)) ? 2 : 1;
+  // (blocks at once: two a CU of four waves, one of eight)
+  if (!tile)
+    x.stream = make_cut(p, group, 16 * x.mr, 32, both ? 256 : 512, 16, 0, both ? most : all);
   if (!stream) x.tile = make_cut(p, group, 16 * tile_frags<D> * kTileWaves, 64, 256, 8, both ? most : 0, all);
   return x;
 }
@@ -1167,6 +1206,7 @@ AttnParams with(const KvAttention& k, const Cut& c, const Area& at, char* ws) {
   a.rows_most = c.rows_most;
   a.target = c.target;
   a.least_steps = c.least_steps;
+  a.blocks = static_cast<uint32_t>(c.blocks);
   if (c.target) {
     a.join_count = reinterpret_cast<int*>(ws + at.count);
     a.joins = reinterpret_cast<KvJoin*>(ws + at.joins);
@@ -1181,53 +1221,63 @@ hipError_t allow_lds(K kernel, int bytes) {
   return hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
 
+// Joins of one or (b) two kinds of blocks.
 template <int D>
-hipError_t join(const AttnParams& a, const Cut& c, hipStream_t s) {
-  if (!c.target) return hipSuccess;
-  const int64_t rows = c.rows_most < c.bm ? c.rows_most : c.bm;
-  if (c.joins * rows >= 1024) {
-    const int64_t y = std::max<int64_t>(1, std::min<int64_t>((rows + 3) / 4, 2048 / c.joins));
-    kv_join_kernel<D, 1><<<dim3(c.joins, y), kJoinThreads, 0, s>>>(a, c.bm);
+hipError_t join(const AttnParams& a, const Cut& c, const AttnParams& b, const Cut& d, hipStream_t s) {
+  if (!c.target && !d.target) return hipSuccess;
+  if (!c.target) return join<D>(b, d, a, c, s);
+  const int64_t joins = c.joins + (d.target ? d.joins : 0), rows = c.rows_most < c.bm ? c.rows_most : c.bm;
+  if (joins * rows >= 1024) {
+    const int64_t y = std::max<int64_t>(1, std::min<int64_t>((rows + 3) / 4, 2048 / joins));
+    kv_join_kernel<D, 1><<<dim3(joins, y), kJoinThreads, 0, s>>>(a, c.bm, c.joins, b, d.bm);
   } else {
-    kv_join_kernel<D, kJoinWaves><<<dim3(c.joins, rows), kJoinThreads, 0, s>>>(a, c.bm);
+    kv_join_kernel<D, kJoinWaves><<<dim3(joins, rows), kJoinThreads, 0, s>>>(a, c.bm, c.joins, b, d.bm);
   }
   return hipGetLastError();
 }
 
+constexpr int stream_lds_bytes(int D, int NW) { return (NW * 16 * (D + 4) + NW * 16 * 2) * 4; }
+template <int D>
+constexpr int tile_lds_bytes = 2 * sizeof(TileLds<D>) + sizeof(TileScales);
+
 template <int D, int MR, int NW>
-hipError_t run_stream(const AttnParams& a, const Cut& c, hipStream_t s) {
-  constexpr int kLds = (NW * 16 * (D + 4) + NW * 16 * 2) * 4;
+hipError_t run_stream(const AttnParams& a, hipStream_t s) {
+  constexpr int kLds = stream_lds_bytes(D, NW);
   static const hipError_t allowed = allow_lds(kv_stream_kernel<D, MR, NW>, kLds);
   if (allowed != hipSuccess) return allowed;
-  kv_stream_kernel<D, MR, NW><<<c.blocks, NW * kWave, kLds, s>>>(a);
-  const hipError_t e = hipGetLastError();
-  return e != hipSuccess ? e : join<D>(a, c, s);
+  kv_stream_kernel<D, MR, NW><<<a.blocks, NW * kWave, kLds, s>>>(a);
+  return hipGetLastError();
 }
 
 template <int D>
 hipError_t run(const KvAttention& k, char* ws, hipStream_t s) {
   const Plan x = make_plan<D>(k.c, k.group);
   const Area sa = area(x.stream, D, 0), ta = area(x.tile, D, sa.end);
-  if (x.tile.use) {
-    constexpr int kLds = 2 * sizeof(TileLds<D>) + sizeof(TileScales);
-    static const hipError_t allowed = allow_lds(kv_tile_kernel<D>, kLds);
+  const AttnParams few = with(k, x.stream, sa, ws), many = with(k, x.tile, ta, ws);
+  hipError_t e;
+  if (x.tile.use && x.stream.use) {
+    constexpr int kLds = std::max(tile_lds_bytes<D>, stream_lds_bytes(D, kTileWaves));
+    static const hipError_t allowed = allow_lds(kv_mixed_kernel<D>, kLds);
     if (allowed != hipSuccess) return allowed;
-    const AttnParams a = with(k, x.tile, ta, ws);
-    kv_tile_kernel<D><<<x.tile.blocks, kTileThreads, kLds, s>>>(a);
-    hipError_t e = hipGetLastError();
-    if (e == hipSuccess) e = join<D>(a, x.tile, s);
-    if (e != hipSuccess) return e;
+    kv_mixed_kernel<D><<<many.blocks + few.blocks, kTileThreads, kLds, s>>>(many, few);
+    e = hipGetLastError();
+  } else if (x.tile.use) {
+    static const hipError_t allowed = allow_lds(kv_tile_kernel<D>, tile_lds_bytes<D>);
+    if (allowed != hipSuccess) return allowed;
+    kv_tile_kernel<D><<<many.blocks, kTileThreads, tile_lds_bytes<D>, s>>>(many);
+    e = hipGetLastError();
+  } else if (x.mr == 2) {
+    e = run_stream<D, 2, 4>(few, s);
+  } else {
+    e = x.stream.target || few.blocks > 256 ? run_stream<D, 1, 4>(few, s) : run_stream<D, 1, 8>(few, s);
   }
-  if (!x.stream.use) return hipSuccess;
-  const AttnParams a = with(k, x.stream, sa, ws);
-  if (x.mr == 2) return run_stream<D, 2, 4>(a, x.stream, s);
-  return x.stream.target || x.stream.blocks > 256 ? run_stream<D, 1, 4>(a, x.stream, s) : run_stream<D, 1, 8>(a, x.stream, s);
+  return e != hipSuccess ? e : join<D>(many, x.tile, few, x.stream, s);
 }
 
 template <int D>
 int64_t bytes(const KvParams& p, int group, int64_t* blocks) {
   const Plan x = make_plan<D>(p, group);
-  *blocks = std::max(x.stream.blocks, x.tile.blocks);
+  *blocks = x.stream.blocks + x.tile.blocks;
   return area(x.tile, D, area(x.stream, D, 0).end).end;
 }
 

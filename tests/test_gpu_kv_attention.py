@@ -78,6 +78,16 @@ def test_peaked_and_flat_scores():
     _run(b, 8, q_scale=1e-3, cache=cache)
 
 
+def test_subnormal_fp16_queries():
+    """Products with numbers below fp16's normal range are not dropped."""
+    b = kv_ref.Batch([150], [4], 1, 64, 64, torch.float16)
+    q = (b.queries(2).float() * 2.0 ** -18).to(torch.float16)
+    _run(b, 2, q=q, scale=2.0 ** 15)
+    b = kv_ref.Batch([150], [40], 1, 128, 16, torch.float16)
+    q = (b.queries(2).float() * 2.0 ** -18).to(torch.float16)
+    _run(b, 2, q=q, scale=-(2.0 ** 15))
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
 def test_growing_scores_and_values(dtype):
     """The running maximum and the values' unit grow with nearly every page."""
