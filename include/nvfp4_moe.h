@@ -279,7 +279,7 @@ int int8_linear_workspace(int64_t M, int64_t K, int64_t* bytes);
  *   all of it is NaN.
  * The tokens of a sequence's last, incomplete page are held as they came, in its
  * slot (bf16 and fp16 values exactly, except values under 2^-29 of their token's
- * largest, which are within 2^-40 of it; a token with an infinity or a NaN is NaN
+ * largest, which are within 2^-39 of it; a token with an infinity or a NaN is NaN
  * throughout its head).  So every value is rounded once, from what was given; the
  * cache's contents do not depend on how a sequence's tokens were split over calls;
  * and full pages never change: sequences may share them.
@@ -310,7 +310,8 @@ typedef struct kv_cache {
  *              table_width of them, ld_table >= table_width, are the call's
  *   lens_dev, slots_dev   i32 [entries];  cu_dev   i32 [entries + 1] or NULL
  *   entries, tokens >= 0 (either 0: no-op), table_width * page_size <= 2^30
- * These are read on the device, so that a captured step follows their new values.
+ * These are read on the device, so that a captured step follows their new values.  A
+ * table's entry is used once its page is full; the incomplete page needs none yet.
  * An entry whose slot or length is negative is padding: it has no tokens.  Numbers
  * outside the cache or the call's tensors are never followed: an entry whose slot,
  * length or first token is outside is padding too, tokens behind the table's last

@@ -23,6 +23,7 @@
 // piece of the keys; pieces are made where there are too few tiles for the chip and
 // joined by a second kernel, in order.
 #include <algorithm>
+#include <atomic>
 #include <climits>
 
 #include "kernels.hpp"
@@ -1044,11 +1045,11 @@ __global__ __launch_bounds__(kTileThreads, 2) void kv_tile_kernel(AttnParams a) 
 
 // Entries of many and of few rows together, each kind by its blocks: one launch, and neither
 // waits for the other (9 entries, 501 tokens at most, D = 64: in two launches 12 us more).
-template <int D>
+template <int D, int MR>
 __global__ __launch_bounds__(kTileThreads, 2) void kv_mixed_kernel(AttnParams many, AttnParams few) {
   extern __shared__ __align__(16) char mixed_lds[];
   if (blockIdx.x < many.blocks) tile_block<D>(many, blockIdx.x, mixed_lds);
-  else stream_block<D, 1, kTileWaves>(few, blockIdx.x - many.blocks, reinterpret_cast<float*>(mixed_lds));
+  else stream_block<D, MR, kTileWaves>(few, blockIdx.x - many.blocks, reinterpret_cast<float*>(mixed_lds));
 }
 
 // Pieces of a row joined in their order.  One wave a row, or where there are few rows the
@@ -1162,10 +1163,16 @@ Cut make_cut(const KvParams& p, int group, int bm, int step, int target, int lea
 template <int D>
 Plan make_plan(const KvParams& p, int group) {
   Plan x{};
-  const int most = 32, all = INT_MAX / 2;
-  const int64_t rows = int64_t{p.tokens} * group;
-  const bool stream = !p.cu || rows <= most, tile = !stream && p.entries == 1, both = !stream && !tile;
-  x.mr = stream && (group > 16 || (p.cu && p.tokens > p.entries)) ? 2 : 1;
+  // Entries of up to three tiles are the stream kernel's: a tile of the other has eight
+  // waves, of which they would keep two or three busy (64 entries of 8 tokens, 8 heads a kv head, at
+  // 8000 tokens: 206 us, by the other 442).  Tiles of 32 rows where the entries have between
+  // 16 and 96 on average, and 256 registers hold them; else those of few rows are likely
+  // single tokens (9 entries, 501 tokens at most, 3 heads a kv head: 35 us, with tiles of 32 rows 37).
+  const int all = INT_MAX / 2;
+  const int64_t rows = int64_t{p.tokens} * group, entries = std::max(1, std::min(p.entries, p.tokens));
+  const int frags = D <= 128 && rows > 16 * entries && rows <= 96 * entries ? 2 : 1, most = 48 * frags;
+  const bool stream = !p.cu || rows <= 32, tile = !stream && p.entries == 1, both = !stream && !tile;
+  x.mr = stream ? (group > 16 || (p.cu && p.tokens > p.entries) ? 2 : 1) : frags;
   // (blocks at once: two a CU of four waves, one of eight)
   if (!tile)
     x.stream = make_cut(p, group, 16 * x.mr, 32, both ? 256 : 512, 16, 0, both ? most : all);
@@ -1216,9 +1223,18 @@ AttnParams with(const KvAttention& k, const Cut& c, const Area& at, char* ws) {
   return a;
 }
 
+// Lets a kernel use `bytes` of dynamic LDS, once a device (devices past the mask's 64 on
+// every call).
 template <typename K>
-hipError_t allow_lds(K kernel, int bytes) {
-  return hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+hipError_t allow_lds(K kernel, int bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  hipError_t e = hipGetDevice(&dev);
+  if (e != hipSuccess) return e;
+  const uint64_t bit = dev >= 0 && dev < 64 ? uint64_t{1} << dev : 0;
+  if (bit != 0 && (done.load(std::memory_order_relaxed) & bit) != 0) return hipSuccess;
+  e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == hipSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
 }
 
 // Joins of one or (b) two kinds of blocks.
@@ -1243,8 +1259,9 @@ constexpr int tile_lds_bytes = 2 * sizeof(TileLds<D>) + sizeof(TileScales);
 template <int D, int MR, int NW>
 hipError_t run_stream(const AttnParams& a, hipStream_t s) {
   constexpr int kLds = stream_lds_bytes(D, NW);
-  static const hipError_t allowed = allow_lds(kv_stream_kernel<D, MR, NW>, kLds);
-  if (allowed != hipSuccess) return allowed;
+  static std::atomic<uint64_t> done{0};
+  const hipError_t e = allow_lds(kv_stream_kernel<D, MR, NW>, kLds, done);
+  if (e != hipSuccess) return e;
   kv_stream_kernel<D, MR, NW><<<a.blocks, NW * kWave, kLds, s>>>(a);
   return hipGetLastError();
 }
@@ -1257,13 +1274,19 @@ hipError_t run(const KvAttention& k, char* ws, hipStream_t s) {
   hipError_t e;
   if (x.tile.use && x.stream.use) {
     constexpr int kLds = std::max(tile_lds_bytes<D>, stream_lds_bytes(D, kTileWaves));
-    static const hipError_t allowed = allow_lds(kv_mixed_kernel<D>, kLds);
-    if (allowed != hipSuccess) return allowed;
-    kv_mixed_kernel<D><<<many.blocks + few.blocks, kTileThreads, kLds, s>>>(many, few);
-    e = hipGetLastError();
+    const auto launch = [&](auto kernel, std::atomic<uint64_t>& done) {
+      const hipError_t set = allow_lds(kernel, kLds, done);
+      if (set != hipSuccess) return set;
+      kernel<<<many.blocks + few.blocks, kTileThreads, kLds, s>>>(many, few);
+      return hipGetLastError();
+    };
+    static std::atomic<uint64_t> done[2];
+    if constexpr (D <= 128) e = x.mr == 2 ? launch(kv_mixed_kernel<D, 2>, done[1]) : launch(kv_mixed_kernel<D, 1>, done[0]);
+    else e = launch(kv_mixed_kernel<D, 1>, done[0]);
   } else if (x.tile.use) {
-    static const hipError_t allowed = allow_lds(kv_tile_kernel<D>, tile_lds_bytes<D>);
-    if (allowed != hipSuccess) return allowed;
+    static std::atomic<uint64_t> done{0};
+    e = allow_lds(kv_tile_kernel<D>, tile_lds_bytes<D>, done);
+    if (e != hipSuccess) return e;
     kv_tile_kernel<D><<<many.blocks, kTileThreads, tile_lds_bytes<D>, s>>>(many);
     e = hipGetLastError();
   } else if (x.mr == 2) {

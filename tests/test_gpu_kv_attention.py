@@ -233,6 +233,17 @@ def test_strided_queries_and_outputs():
     kv_ref.check(got, want, far)
 
 
+@pytest.mark.parametrize("D,G,new", [(128, 8, 8), (64, 8, 5), (192, 8, 5), (256, 3, 9), (128, 1, 97), (64, 4, 12), (128, 3, 17)])
+def test_entries_of_a_few_tokens(D, G, new):
+    """Between single tokens and chunks: entries of one to four tiles of the kernel for few rows, alike and mixed
+    with others, short and cut into pieces."""
+    b = kv_ref.Batch([1500, 0, 77, 300], [new] * 4, 2, D, 32)
+    _run(b, 2 * G)
+    b = kv_ref.Batch([1500, 64, 3, 0, 10], [new, 1, 200, new, 0], 1, D, 64, torch.float16)
+    _run(b, G)
+    _run(b, G, window=70)
+
+
 def test_no_tokens():
     b = kv_ref.Batch([20], [1], 2, 64, 16)
     cache = b.cache(binding)

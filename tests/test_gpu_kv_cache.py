@@ -264,3 +264,36 @@ def test_no_pairs_and_no_entries():
     binding.kv_append(cache, empty, empty, table, lens, slots, cu=b.ints([0, 0]))
     k, v = binding.kv_read(cache, table, lens, slots, cu=b.ints([0, 0]), tokens=0)
     assert k.shape == v.shape == (0, 2, 64)
+
+
+def test_offsets_past_32_bits():
+    """Codes and tails of more than 2^32 bytes: the pages and slots at their far ends."""
+    P, D, kv = 64, 128, 8
+    pages, slots_n = 34000, 17000  # 4.5 GB of codes, 4.5 GB of tails
+    cache = binding.KvCache(pages, slots_n, kv, D, page_size=P)
+    b = kv_ref.Batch([0, 0], [2 * P + 9, P + 1], kv, D, P, spare=0)
+    b.pages = pages
+    b.table_cpu = torch.tensor([[pages - 1, 3, 0], [pages - 2, 0, 0]], dtype=torch.int32)
+    b.slots_cpu = torch.tensor([slots_n - 1, slots_n - 2], dtype=torch.int32)
+    b.append_new(binding, cache)
+    _check_all(b, cache, b.new)
+    assert (cache.codes[pages - 1] != 0).any() and (cache.tails[slots_n - 1] != 0).any()
+    q = torch.randn((2, 16, D), generator=b.gen).to(torch.bfloat16).cuda()
+    held = [n - 1 for n in b.new]
+    table, lens, slots, _ = b.args(held, [1, 1])
+    out = binding.kv_attention(cache, q, table, lens, slots)
+    for i in range(2):
+        want, far = kv_ref.attention(q[i:i + 1], kv_ref.held_values(b.k_all[i], P), kv_ref.held_values(b.v_all[i], P),
+                                     held[i], D ** -0.5)
+        kv_ref.check(out[i:i + 1], want, far)
+    chunk = torch.randn((P, 16, D), generator=b.gen).to(torch.bfloat16).cuda()
+    table, lens, slots, cu = b.args([b.new[0] - P, 0], [P, 0])
+    out = binding.kv_attention(cache, chunk, table, lens, slots, cu=cu)
+    want, far = kv_ref.attention(chunk, kv_ref.held_values(b.k_all[0], P), kv_ref.held_values(b.v_all[0], P),
+                                 b.new[0] - P, D ** -0.5)
+    kv_ref.check(out, want, far)
+    src, dst = b.ints([0]), b.ints([1])
+    binding.kv_fork(cache, table, b.ints(b.new), slots, src, dst)
+    assert torch.equal(cache.tails[slots_n - 1, :, :, :16 * D], cache.tails[slots_n - 2, :, :, :16 * D])
+    del cache
+    torch.cuda.empty_cache()
