@@ -1244,7 +1244,7 @@ hipError_t join(const AttnParams& a, const Cut& c, const AttnParams& b, const Cu
   if (!c.target) return join<D>(b, d, a, c, s);
   const int64_t joins = c.joins + (d.target ? d.joins : 0), rows = c.rows_most < c.bm ? c.rows_most : c.bm;
   if (joins * rows >= 1024) {
-    const int64_t y = std::max<int64_t>(1, std::min<int64_t>((rows + 3) / 4, 2048 / joins));
+    const int64_t y = std::max<int64_t>(1, std::min<int64_t>((rows + 3) / 4, 8192 / joins));
     kv_join_kernel<D, 1><<<dim3(joins, y), kJoinThreads, 0, s>>>(a, c.bm, c.joins, b, d.bm);
   } else {
     kv_join_kernel<D, kJoinWaves><<<dim3(joins, rows), kJoinThreads, 0, s>>>(a, c.bm, c.joins, b, d.bm);
