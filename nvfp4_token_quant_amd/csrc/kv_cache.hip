@@ -9,7 +9,11 @@
 // One block takes the keys or the values of one page and head, as pieces of 4
 // tokens x 8 channels a thread: rows are read and written in 16-byte pieces, and
 // four tokens of a channel are one dword of the values' order.  Codes pass
-// through LDS, so that a page leaves in whole 16-byte pieces too.
+// through LDS, so that a page leaves in whole 16-byte pieces too.  Bound by memory where
+// there is enough of it: prompts of 4 x 8192 tokens (8 heads, D = 128, pages of 64) 56 us, 3.6
+// TB/s with two trips to memory a block (five blocks a CU; six or eight, which spill, 57
+// and 86), read back in 35 us, 5.8 TB/s; a decode batch of 64 sequences 5.7 and 5.0 us, of which a
+// launch that does nothing takes 2.6.
 #include "kernels.hpp"
 #include "kv_cache.hpp"
 
