@@ -316,9 +316,12 @@ typedef struct kv_cache {
  * outside the cache or the call's tensors are never followed: an entry whose slot,
  * length or first token is outside is padding too, tokens behind the table's last
  * page or the call's last token are dropped, a page outside the cache keeps nothing
- * and holds nothing that attention sees (kv_read gives 0).  The outputs of tokens that belong
- * to no entry are left as they were.  cu has to be ascending; entries of an append
- * have different slots, and pages that they complete are theirs alone.
+ * and holds nothing that attention sees (kv_read gives 0).  A step may take tokens back (a
+ * smaller length than there are) as far as to the start of the incomplete page, or to the
+ * end of any full one: the tokens of a page that got full are no longer there as they came.
+ * The outputs of tokens that belong to no entry are left as they were.  cu has to be
+ * ascending; entries of an append have different slots, and pages that they complete
+ * are theirs alone.
  */
 typedef struct kv_batch {
   int64_t entries, tokens;

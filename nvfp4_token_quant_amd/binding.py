@@ -396,7 +396,9 @@ def int8_linear(x, w_codes, w_scale, bias=None, out_dtype=None, out=None, stream
 # are kept) and cu int32 [B + 1], or None where each sequence gets one token: the
 # call's tokens cu[i] .. cu[i + 1] - 1 are sequence i's, at its positions from
 # lens[i] on.  They are read on the device: a captured step follows their values.
-# Entries with a negative slot or length are padding (kv_batch).
+# Entries with a negative slot or length are padding.  A smaller length than before
+# takes tokens back, as far as to the start of the incomplete page or to the end of a
+# full one (kv_batch).
 
 class KvCache:
     """A layer's key-value cache (kv_cache): `num_pages` pages of `page_size`

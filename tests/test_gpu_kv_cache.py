@@ -147,6 +147,20 @@ def test_numbers_near_ties_are_rounded_as_defined():
     _check_all(b, cache, [P])
 
 
+@pytest.mark.parametrize("back", [32 + 3, 32, 16])
+def test_tokens_taken_back(back):
+    """To inside the incomplete page, to its start, to the end of an older page; other tokens come instead."""
+    P, D = 16, 64
+    b = kv_ref.Batch([45], [30], 2, D, P)
+    cache = b.cache(binding)
+    for x in (b.k_all, b.v_all):
+        x[0] = torch.cat((x[0][:back], -x[0][back:]))
+    b.held = [back]
+    b.new = [75 - back]
+    b.append_new(binding, cache)
+    _check_all(b, cache, [75])
+
+
 def test_reading_the_last_tokens_only():
     b = kv_ref.Batch([0] * 3, [100, 33, 64], 2, 64, 16)
     cache = b.cache(binding)
